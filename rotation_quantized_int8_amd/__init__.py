@@ -10,6 +10,10 @@ Functions mirror the C entry points:
   quantize_weights, linear_w8a8, linear_w8a8_noalloc, linear_w8a8_ex, linear_w8a16, linear_w8a16_rs,
   linear_dequant, dequantize_weights, act_quant, act_rotate_f16, act_rotate_scaled,
   gemm_i8_i32, gemm_i8_f16, gemm_f16, workspace_bytes.
+
+The attention side (a paged key/value cache, rotated and quantised the same
+way; C ABI in ``include/convrot_kv.h``) is in ``kv.py``:
+  KVCache, kv_append, kv_read, kv_attention, kv_workspace_bytes.
 """
 
 from __future__ import annotations
@@ -453,3 +457,6 @@ def gemm_f16(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
         _check(lib().convrot_gemm_f16(_ptr(x), _ptr(w), M, N, K, _ptr(y), _stream(x)),
                "convrot_gemm_f16")
     return y
+
+
+from .kv import KVCache, kv_append, kv_attention, kv_read, kv_workspace_bytes  # noqa: E402,F401

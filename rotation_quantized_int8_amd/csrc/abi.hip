@@ -2,53 +2,19 @@
 // the launches on the caller's stream.  Declarations and the full contract
 // are in include/convrot.h.
 
-#include <atomic>
-#include <cstring>
 #include <initializer_list>
 #include <mutex>
 
-#include "convrot.h"
+#include "checks.hpp"
 #include "launch.hpp"
-
 
 using namespace convrot;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-// 0 = unknown, 1 = gfx950, 2 = other / error
-std::atomic<int> g_device_state[kMaxDevices];
-
-convrot_status check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return CONVROT_ERR_DEVICE;
-  int st = g_device_state[dev].load(std::memory_order_acquire);
-  if (st == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
-      st = 2;
-    } else {
-      st = (std::strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : 2;
-    }
-    g_device_state[dev].store(st, std::memory_order_release);
-  }
-  return st == 1 ? CONVROT_OK : CONVROT_ERR_DEVICE;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // K = 0 is an empty contraction (see empty_linear); otherwise a multiple of
 // the group size up to kKMax.
 bool k_ok(int64_t K) { return K >= 0 && K % kGroup == 0 && K <= kKMax; }
-
-// [a, a + na) and [b, b + nb) overlap?  (null or empty ranges never overlap)
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 int lora_ld(int64_t rank) { return rank > 0 ? (int)((rank + 31) / 32 * 32) : 0; }
 
@@ -79,10 +45,6 @@ LoraWs lora_ws(char* base, int64_t M, int64_t N, int64_t K, int64_t rank) {
   if (lora_splits(K) > 1) w.P = reinterpret_cast<float*>(base + off);
   return w;
 }
-
-convrot_status launched(hipError_t e) { return e == hipSuccess ? CONVROT_OK : CONVROT_ERR_LAUNCH; }
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 struct In {
   const void* p;
@@ -135,7 +97,8 @@ const char* convrot_status_string(int status) {
   switch (status) {
     case CONVROT_OK: return "ok";
     case CONVROT_ERR_INVALID_ARG: return "invalid argument (null pointer or overlapping output)";
-    case CONVROT_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 256 in 0..131072, or bad LoRA rank)";
+    case CONVROT_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 256 in 0..131072, bad LoRA rank, or a size or "
+             "stride that the key/value cache does not take)";
     case CONVROT_ERR_ALIGNMENT: return "tensor pointer not 16-byte aligned";
     case CONVROT_ERR_DEVICE: return "current HIP device is not gfx950 or cannot be queried";
     case CONVROT_ERR_LAUNCH: return "kernel launch failed";

@@ -1,0 +1,95 @@
+// The rotated, quantised key/value cache: what its kernels share (internal to
+// the library; the layout and arithmetic are stated in include/convrot_kv.h).
+#pragma once
+
+#include "common.hpp"
+
+namespace convrot {
+
+typedef short v2s __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+struct KvCache {
+  uint8_t* kc;      // codes [pages, heads, page, D bits / 8]
+  float* ks;        // scales [pages, heads, page]
+  uint8_t* vc;
+  float* vs;
+  int64_t slots;    // pages * page
+  int pages;
+  int page_log2;
+  int heads;
+  int head_dim;
+  int bits;
+};
+
+struct KvRows {     // 16-bit rows of D elements, [tokens, heads, D] with strides in elements
+  const uint16_t* p;
+  int64_t token, head;
+};
+
+struct KvAttn {
+  KvCache c;
+  KvRows q;
+  uint16_t* o;            // [T, q_heads, D], dense
+  const int* table;       // [batch, width]
+  const int* kv_lens;     // [batch]
+  const int* q_start;     // [batch + 1], or null: each_q queries a sequence
+  int64_t T;
+  int64_t width;
+  int batch, q_heads, group;
+  int each_q;
+  int max_q, max_kv;
+  float scale;            // sm_scale
+  int causal, bf16;
+};
+
+hipError_t launch_kv_append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16, const int64_t* slots,
+                            int64_t T, hipStream_t stream);
+hipError_t launch_kv_read(const KvCache& c, const int64_t* slots, int64_t T, uint16_t* K, uint16_t* V, bool bf16,
+                          hipStream_t stream);
+size_t kv_attention_workspace(const KvAttn& a);
+hipError_t launch_kv_attention(const KvAttn& a, void* workspace, hipStream_t stream);
+
+// fp32(D^-1/2)
+__host__ __device__ constexpr float kv_rsqrt(int D) {
+  return D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float in16_f32(uint32_t bits) {
+  if constexpr (BF16) return __uint_as_float(bits << 16);
+  else return __half2float(__ushort_as_half((uint16_t)bits));
+}
+
+__device__ __forceinline__ uint32_t out16(float f, bool bf16) {
+  return bf16 ? f32_to_bf16_rn(f) : __half_as_ushort(__float2half_rn(f));
+}
+// Two fp32 values to 16 bits each, packed low then high.
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
+  return bf16 ? (uint32_t)f32_to_bf16_rn(a) | ((uint32_t)f32_to_bf16_rn(b) << 16) : pack_f16x2_rn(a, b);
+}
+
+// The queries and tokens of sequence b, made safe: rows [first, first + n) lie
+// in [0, T), and 0 <= kv <= max_kv.
+struct KvSeq {
+  int64_t first;
+  int n, kv;
+};
+__device__ __forceinline__ KvSeq kv_sequence(const KvAttn& a, int b) {
+  KvSeq s;
+  int64_t from = (int64_t)b * a.each_q, to = from + a.each_q;
+  if (a.q_start) {
+    from = a.q_start[b];
+    to = a.q_start[b + 1];
+  }
+  from = from < 0 ? 0 : from > a.T ? a.T : from;
+  to = to < from ? from : to > a.T ? a.T : to;
+  s.first = from;
+  s.n = to - from > a.max_q ? a.max_q : (int)(to - from);
+  const int kv = a.kv_lens[b];
+  s.kv = kv < 0 ? 0 : kv > a.max_kv ? a.max_kv : kv;
+  return s;
+}
+
+}  // namespace convrot

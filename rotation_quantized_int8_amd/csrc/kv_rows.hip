@@ -1,0 +1,272 @@
+// Writing rows into the rotated, quantised key/value cache and reading them
+// back (convrot_kv_append, convrot_kv_read).
+//
+// A row of D elements is held by D / 32 neighbouring lanes, 32 contiguous
+// elements each: of the log2 D butterfly stages of the rotation, five run in
+// a lane's registers and the last one to three between lanes, by DPP
+// permutations inside a 16-lane row (no LDS).
+//
+// Both kernels are bound by HBM: a row costs 2 D bytes on its 16-bit side and
+// D bits / 8 + 4 in the cache, against about log2 D additions an element.
+
+#include "kv.hpp"
+
+namespace convrot {
+namespace {
+
+// The value of the lane whose number differs in bit BIT (0, 1 or 2).
+template <int BIT>
+__device__ __forceinline__ int lane_swap(int v) {
+  if constexpr (BIT == 0) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);        // quad [1,0,3,2]
+  else if constexpr (BIT == 1) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // quad [2,3,0,1]
+  else {   // mirror the 8 lanes (i -> i ^ 7), then each quad (i -> i ^ 3)
+    const int m = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);
+    return __builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);
+  }
+}
+template <int BIT>
+__device__ __forceinline__ double lane_swap(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)lane_swap<BIT>((int)(uint32_t)u), hi = (uint32_t)lane_swap<BIT>((int)(u >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// One stage between lanes: the lane with bit BIT clear keeps the sum, the
+// other the difference (first minus second): v = other + sign * v.
+template <int BIT>
+__device__ __forceinline__ void stage_f64(double (&v)[32], int lane) {
+  const double sign = (lane >> BIT) & 1 ? -1.0 : 1.0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = fma(v[i], sign, lane_swap<BIT>(v[i]));   // a product by +-1: one rounding
+}
+template <int BIT>
+__device__ __forceinline__ void stage_i16(v2s (&v)[16], int lane) {
+  const short sign = (lane >> BIT) & 1 ? -1 : 1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    v[i] = v[i] * (v2s){sign, sign} + __builtin_bit_cast(v2s, lane_swap<BIT>(__builtin_bit_cast(int, v[i])));
+}
+
+// Codes of 32 values u with scale s, as 16 (4 bits) or 32 (8 bits) bytes.
+// Rounds u / s half to even through the product with the reciprocal: with r
+// within one ulp of 1 / s and |u / s| <= 127 (1 + 2^-23), u r lies within
+// 1.6e-5 of u / s and fp32(u / s) within 3.9e-6, so unless u r is within 3e-5
+// of a half-integer both round to the same integer, which fma(u, r, 1.5 2^23)
+// leaves in its low mantissa bits.  Lanes with a closer value, and scales
+// whose reciprocal could leave fp32's normal range, divide.
+template <int BITS>
+__device__ __forceinline__ void codes32(const float (&u)[32], float s, uint32_t (&w)[BITS]) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
+  const float r = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+  uint32_t b[32];
+  float off = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float m = __fmaf_rn(u[i], r, kMagic);
+    off = fmaxf(off, fabsf(__fmaf_rn(u[i], r, -__fsub_rn(m, kMagic))));
+    b[i] = __float_as_uint(m);
+  }
+  if (off > 0.49997f || s < 1e-30f || s > 1e30f) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) b[i] = __float_as_uint(__fadd_rn(s == 0.0f ? 0.0f : u[i] / s, kMagic));
+  }
+#pragma unroll
+  for (int j = 0; j < BITS; ++j) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < 32 / BITS; ++i) x |= (b[32 / BITS * j + i] & ((1u << BITS) - 1)) << (BITS * i);
+    w[j] = x;
+  }
+}
+
+// blockIdx.y: 0 keys, 1 values.  The rotation runs in fp64, where the sums
+// are exact (an fp16 value is a multiple of 2^-24 below 2^16, so a sum of 256
+// of them has at most 48 significand bits).
+template <int D, int BITS, bool BF16>
+__global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, KvRows vr,
+                                                        const int64_t* __restrict__ slots, int rows) {
+  constexpr int L = D / 32;
+  const KvRows in = blockIdx.y ? vr : kr;
+  uint8_t* codes = blockIdx.y ? c.vc : c.kc;
+  float* scales = blockIdx.y ? c.vs : c.ks;
+  const int lane = threadIdx.x % L;
+  const int per = 256 / L;
+  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
+    const int64_t r = base + threadIdx.x / L;
+    const int t = (int)(r / c.heads), h = (int)(r - (int64_t)t * c.heads);
+    int64_t slot = r < rows ? slots[t] : -1;
+    if (slot >= c.slots) slot = -1;
+    v4u raw[4] = {};
+    if (slot >= 0) {
+      const v4u* src = reinterpret_cast<const v4u*>(in.p + t * in.token + h * in.head + lane * 32);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) raw[j] = src[j];
+    }
+    double v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t word = raw[i / 8][i / 2 % 4];
+      v[i] = (double)in16_f32<BF16>(i & 1 ? word >> 16 : word & 0xFFFFu);
+    }
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if ((i & k) == 0) {
+          const double a = v[i], b = v[i + k];
+          v[i] = a + b;
+          v[i + k] = a - b;
+        }
+    stage_f64<0>(v, lane);
+    if constexpr (L > 2) stage_f64<1>(v, lane);
+    if constexpr (L > 4) stage_f64<2>(v, lane);
+    float u[32];
+    uint32_t top = 0;   // the largest |u| by its bits, where a NaN is above infinity
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      u[i] = (float)v[i];
+      top = max(top, __float_as_uint(u[i]) & 0x7FFFFFFFu);
+    }
+    top = max(top, (uint32_t)lane_swap<0>((int)top));
+    if constexpr (L > 2) top = max(top, (uint32_t)lane_swap<1>((int)top));
+    if constexpr (L > 4) top = max(top, (uint32_t)lane_swap<2>((int)top));
+    const bool finite = top < 0x7F800000u;
+    const float s = __uint_as_float(top) / (BITS == 4 ? 7.0f : 127.0f);
+    uint32_t w[BITS];
+    codes32<BITS>(u, finite ? s : 0.0f, w);
+    if (slot < 0) continue;
+    const int64_t row = ((slot >> c.page_log2) * c.heads + h << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
+    v4u* dst = reinterpret_cast<v4u*>(codes + row * (D * BITS / 8) + lane * (4 * BITS));
+#pragma unroll
+    for (int j = 0; j < BITS / 4; ++j)
+      dst[j] = finite ? (v4u){w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]} : (v4u){0, 0, 0, 0};
+    if (lane == 0) scales[row] = finite ? __fmul_rn(s, kv_rsqrt(D)) : __uint_as_float(0x7FC00000u);
+  }
+}
+
+// The codes' transform runs in packed 16-bit integers: |sum| <= 127 * 256 =
+// 32512, so it is exact.
+template <int D, int BITS>
+__global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* __restrict__ slots, int rows,
+                                                      uint16_t* ko, uint16_t* vo, int bf16) {
+  constexpr int L = D / 32;
+  const bool second = blockIdx.y || !ko;
+  const uint8_t* codes = second ? c.vc : c.kc;
+  const float* scales = second ? c.vs : c.ks;
+  uint16_t* out = second ? vo : ko;
+  const int lane = threadIdx.x % L;
+  const int per = 256 / L;
+  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
+    const int64_t r = base + threadIdx.x / L;
+    const int t = (int)(r / c.heads), h = (int)(r - (int64_t)t * c.heads);
+    int64_t slot = r < rows ? slots[t] : -1;
+    if (slot >= c.slots) slot = -1;
+    v4u raw[BITS / 4] = {};
+    float f = 0.0f;
+    if (slot >= 0) {
+      const int64_t row = ((slot >> c.page_log2) * c.heads + h << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
+      const v4u* src = reinterpret_cast<const v4u*>(codes + row * (D * BITS / 8) + lane * (4 * BITS));
+#pragma unroll
+      for (int j = 0; j < BITS / 4; ++j) raw[j] = src[j];
+      f = __fmul_rn(scales[row], kv_rsqrt(D));
+    }
+    // v[i] holds two elements `gap` apart
+    constexpr int gap = BITS == 4 ? 4 : 2;
+    v2s v[16];
+#pragma unroll
+    for (int j = 0; j < BITS; ++j)
+#pragma unroll
+      for (int i = 0; i < gap; ++i) {
+        const uint32_t x = raw[j / 4][j % 4] << (16 - BITS - BITS * i);
+        v[gap * j + i] = __builtin_bit_cast(v2s, x) >> (v2s){16 - BITS, 16 - BITS};
+      }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {   // the two halves: (a, b) -> (a + b, a - b)
+      const uint32_t x = __builtin_bit_cast(uint32_t, v[i]);
+      v[i] = v[i] * (v2s){1, -1} + __builtin_bit_cast(v2s, (x << 16) | (x >> 16));
+    }
+#pragma unroll
+    for (int k = 1; k < 16; k <<= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((i & k) == 0) {
+          const v2s a = v[i], b = v[i + k];
+          v[i] = a + b;
+          v[i + k] = a - b;
+        }
+    stage_i16<0>(v, lane);
+    if constexpr (L > 2) stage_i16<1>(v, lane);
+    if constexpr (L > 4) stage_i16<2>(v, lane);
+    if (r >= rows) continue;
+    v4u* dst = reinterpret_cast<v4u*>(out + r * D + lane * 32);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v4u w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int i = 8 * j + 2 * e + z;   // element of the lane
+          x[z] = __fmul_rn((float)v[i / (2 * gap) * gap + i % gap][i / gap % 2], f);
+        }
+        w[e] = pack16(x[0], x[1], bf16);
+      }
+      dst[j] = w;
+    }
+  }
+}
+
+// Workgroups of a launch over `rows` rows: one pass of the grid up to 8192
+// workgroups (8 waves a SIMD on 256 CUs), then a stride.
+unsigned row_grid(int64_t rows, int D) {
+  const int64_t per = 256 / (D / 32), n = (rows + per - 1) / per;
+  return (unsigned)(n < 8192 ? n : 8192);
+}
+
+template <int D, int BITS>
+hipError_t append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16, const int64_t* slots, int64_t T,
+                  hipStream_t stream) {
+  const int rows = (int)(T * c.heads);
+  const dim3 grid(row_grid(rows, D), 2);
+  if (bf16) kv_append_kernel<D, BITS, true><<<grid, 256, 0, stream>>>(c, k, v, slots, rows);
+  else kv_append_kernel<D, BITS, false><<<grid, 256, 0, stream>>>(c, k, v, slots, rows);
+  return hipGetLastError();
+}
+
+template <int D, int BITS>
+hipError_t read(const KvCache& c, const int64_t* slots, int64_t T, uint16_t* K, uint16_t* V, bool bf16,
+                hipStream_t stream) {
+  const int rows = (int)(T * c.heads);
+  const dim3 grid(row_grid(rows, D), K && V ? 2 : 1);
+  kv_read_kernel<D, BITS><<<grid, 256, 0, stream>>>(c, slots, rows, K, V, bf16);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16, const int64_t* slots,
+                            int64_t T, hipStream_t stream) {
+  switch (c.head_dim * 16 + c.bits) {
+    case 64 * 16 + 4: return append<64, 4>(c, k, v, bf16, slots, T, stream);
+    case 64 * 16 + 8: return append<64, 8>(c, k, v, bf16, slots, T, stream);
+    case 128 * 16 + 4: return append<128, 4>(c, k, v, bf16, slots, T, stream);
+    case 128 * 16 + 8: return append<128, 8>(c, k, v, bf16, slots, T, stream);
+    case 256 * 16 + 4: return append<256, 4>(c, k, v, bf16, slots, T, stream);
+    default: return append<256, 8>(c, k, v, bf16, slots, T, stream);
+  }
+}
+
+hipError_t launch_kv_read(const KvCache& c, const int64_t* slots, int64_t T, uint16_t* K, uint16_t* V, bool bf16,
+                          hipStream_t stream) {
+  switch (c.head_dim * 16 + c.bits) {
+    case 64 * 16 + 4: return read<64, 4>(c, slots, T, K, V, bf16, stream);
+    case 64 * 16 + 8: return read<64, 8>(c, slots, T, K, V, bf16, stream);
+    case 128 * 16 + 4: return read<128, 4>(c, slots, T, K, V, bf16, stream);
+    case 128 * 16 + 8: return read<128, 8>(c, slots, T, K, V, bf16, stream);
+    case 256 * 16 + 4: return read<256, 4>(c, slots, T, K, V, bf16, stream);
+    default: return read<256, 8>(c, slots, T, K, V, bf16, stream);
+  }
+}
+
+}  // namespace convrot
