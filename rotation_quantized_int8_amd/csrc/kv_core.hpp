@@ -1,0 +1,101 @@
+// Device pieces and plans shared by the attention kernels over the key/value
+// cache (internal to the library).
+#pragma once
+
+#include "convrot_kv.h"
+#include "kv.hpp"
+
+namespace convrot {
+
+// How a call is split: the rows (query, head in group) of one key head in
+// tiles of `rows`, the tokens in `splits` chunks.  With more than one split
+// the partial outputs go through the workspace: row() numbers them.
+struct KvSplit {
+  int rows, tiles, kept;     // kept: rows of a tile that can be valid
+  int splits, chunk;
+  int heads;
+  float* o;                  // [.., D], unnormalised, rotated basis
+  float* ml;                 // [.., 2]: maximum (log2 units) and sum
+  __device__ __forceinline__ int64_t row(int b, int h, int tile, int split, int r) const {
+    return ((((int64_t)b * heads + h) * tiles + tile) * splits + split) * kept + r;
+  }
+};
+struct KvPlan {
+  KvSplit split;
+  int64_t parts;             // partial rows
+  size_t bytes;              // workspace
+};
+
+KvPlan kv_decode_plan(const KvAttn& a);
+hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream);
+
+// The value of the lane whose number in its 16-lane row differs in bit BIT.
+template <int BIT>
+__device__ __forceinline__ float row_swap(float v) {
+  if constexpr (BIT == 0) return dpp_f32<0xB1>(v);                  // quad [1,0,3,2]
+  else if constexpr (BIT == 1) return dpp_f32<0x4E>(v);             // quad [2,3,0,1]
+  else if constexpr (BIT == 2) return dpp_f32<0x1B>(dpp_f32<0x141>(v));   // i ^ 7, then i ^ 3
+  else return dpp_f32<0x128>(v);                                    // rotate the row by 8
+}
+
+// x W over 16 lanes with E = D / 16 contiguous elements each (fp32).
+template <int D>
+__device__ __forceinline__ void rotate_row(float (&x)[D / 16], int seg) {
+  constexpr int E = D / 16;
+#pragma unroll
+  for (int k = 1; k < E; k <<= 1)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if ((i & k) == 0) {
+        const float a = x[i], b = x[i + k];
+        x[i] = a + b;
+        x[i + k] = a - b;
+      }
+#pragma unroll
+  for (int bit = 0; bit < 4; ++bit) {
+    const float sign = (seg >> bit) & 1 ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float y = bit == 0 ? row_swap<0>(x[i]) : bit == 1 ? row_swap<1>(x[i]) : bit == 2 ? row_swap<2>(x[i]) : row_swap<3>(x[i]);
+      x[i] = __fmaf_rn(x[i], sign, y);
+    }
+  }
+}
+
+// E 16-bit values at p (E = 4, 8 or 16; aligned to 2 E bytes, 16 at most).
+template <int E>
+__device__ __forceinline__ void load_row(const uint16_t* p, bool bf16, float (&x)[E]) {
+  uint32_t w[E / 2];
+  if constexpr (E == 4) {
+    const v2u r = *reinterpret_cast<const v2u*>(p);
+    w[0] = r[0], w[1] = r[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+      const v4u r = reinterpret_cast<const v4u*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = r[j];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const uint32_t b = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+    x[i] = bf16 ? in16_f32<true>(b) : in16_f32<false>(b);
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_row(uint16_t* p, bool bf16, const float (&x)[E]) {
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) w[i] = pack16(x[2 * i], x[2 * i + 1], bf16);
+  if constexpr (E == 4) {
+    *reinterpret_cast<v2u*>(p) = (v2u){w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i)
+      reinterpret_cast<v4u*>(p)[i] = (v4u){w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+  }
+}
+
+}  // namespace convrot

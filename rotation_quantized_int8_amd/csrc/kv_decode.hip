@@ -1,0 +1,543 @@
+// Attention of few query rows over the rotated, quantised key/value cache:
+// single tokens, and the join of a sequence's splits.
+//
+// Mathematics.  H is orthonormal and symmetric, so q . k = (q H) . (k H): the
+// query row is rotated once, the cached codes c are used as they are, and only
+// the finished output row is rotated back.  With the row's softmax weight p_j,
+//   score_j = sm_scale scale_j (q H) . c_j,     o = (sum_j p_j scale'_j c'_j / sum_j p_j) H.
+//
+// Both products run on the matrix cores with the keys' and values' codes as
+// the left operand, so that a lane owns one query row (column lane % 16 of
+// the result) throughout:
+//   S^T = C_k Q^T   mfma i32 16x16x64 i8.  The rotated query is held as 16-bit
+//                   fixed point of its own maximum in two int8 planes,
+//                   q = 256 hi + lo, so the product is exact; a 4-bit code
+//                   enters as 16 c (its nibble moved to the upper half of a
+//                   byte, one AND or a shift and an AND for four codes).
+//   O^T = C_v^T W^T mfma f32 16x16x32 f16.  The result layout of S^T (rows
+//                   4 (lane / 16) + r) is the operand layout of W^T, so the
+//                   weights never leave their lane; a lane loads, for each of
+//                   its 8 tokens, the D / 16 codes of its own D / 16 elements
+//                   and interleaves pairs of tokens by byte permutes.
+// W = p scale', normalised by a power of two M >= every scale' seen so far,
+// and p carries 2^8, so fp16 keeps weights down to 2^-32 of the largest.  The
+// running maximum is only raised when a score exceeds it by more than 2^7
+// (p <= 2^15), so most steps neither reduce over lanes nor rescale.
+//
+// What bounds it: HBM (each cached row is read once for all rows of its key
+// head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
+// sequence and key head; the wavefronts take 32 tokens in turn, with the next
+// 32 loading while these are used.
+
+#include "kv.hpp"
+#include "kv_core.hpp"
+
+namespace convrot {
+namespace {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kStep = 32;                     // tokens a wavefront takes at once
+constexpr int kChunkMax = 4096;               // tokens of a workgroup at most (its page numbers are kept in LDS)
+constexpr float kWeightBits = 8.0f;           // p = 2^(score - m + 8)
+constexpr float kRaise = 7.0f;                // m is raised past this excess
+constexpr float kLowest = -1e30f;             // m of a row that has seen no token
+
+// One key's or value's codes of a lane: N 32-bit words (N = 0: 16 bits).
+template <int BYTES>
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
+  if constexpr (BYTES == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+  else if constexpr (BYTES == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+  else if constexpr (BYTES == 8) {
+    const v2u x = *reinterpret_cast<const v2u*>(p);
+    w[0] = x[0], w[1] = x[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const v4u x = reinterpret_cast<const v4u*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
+    }
+  }
+}
+
+template <int D, int BITS>
+struct Tile {
+  static constexpr int kRow = D * BITS / 8;
+  static constexpr int kKeyBytes = kRow / 4, kValueBytes = kRow / 16;
+  static constexpr int kValueWords = kValueBytes < 4 ? 1 : kValueBytes / 4;
+  uint32_t k[2][kKeyBytes / 4];       // 16 tokens: token lane % 16, elements (lane / 16) D / 4 ..
+  uint32_t v[2][4][kValueWords];      // token 4 (lane / 16) + r, elements (lane % 16) D / 16 ..
+  v4f ks[2], vs[2];                   // of tokens 4 (lane / 16) + r
+};
+
+// S^T operand of 16 tokens: D / 64 times 16 int8 (16 c for 4-bit codes: the
+// even elements of the lane's D / 4, then the odd ones).
+template <int D, int BITS>
+__device__ __forceinline__ v4i key_operand(const uint32_t* w, int m) {
+  v4i a;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (BITS == 8) {
+      a[j] = (int)w[4 * m + j];
+    } else {
+      constexpr int half = D / 32;             // words of the even elements
+      const int i = 4 * m + j;
+      a[j] = (int)(i < half ? (w[i] << 4) & 0xF0F0F0F0u : w[i - half] & 0xF0F0F0F0u);
+    }
+  }
+  return a;
+}
+
+// O^T operands: of 8 tokens' words, the D / 16 tiles' four half pairs.  With
+// 4-bit codes the odd tiles hold 16 c.
+template <int D, int BITS>
+__device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Tile<D, BITS>::kValueWords],
+                                               v4u (&f)[D / 16]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {                // token pairs (0,1), (2,3) of each half
+    const uint32_t* a = v[p / 2][2 * (p % 2)];
+    const uint32_t* b = v[p / 2][2 * (p % 2) + 1];
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 4) {
+        const uint32_t x = __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u) ^ 0x88888888u;
+        const uint32_t y = x >> 8;
+        // 1024 + (c + 8) and 1024 + 16 (c + 8)
+        const h2 one = {(_Float16)1032.0f, (_Float16)1032.0f}, sixteen = {(_Float16)1152.0f, (_Float16)1152.0f};
+        f[i][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - one);
+        f[i + 1][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) - sixteen);
+        f[i + 2][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x000F000Fu) | 0x64006400u) - one);
+        f[i + 3][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x00F000F0u) | 0x64006400u) - sixteen);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t x = __builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)(i % 4) * 0x00010001u);
+        const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};   // 1024 + (c + 128)
+        f[i][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x ^ 0x64806480u)) - off);
+      }
+    }
+  }
+}
+
+template <int D, int BITS, int QT>
+__global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSplit sp) {
+  using T = Tile<D, BITS>;
+  constexpr int E = D / 16;                    // elements of a lane's output tiles, and of a rotation lane
+  constexpr int KM = D / 64;                   // matrix steps of a score
+  constexpr int ROWS = 16 * QT;
+  constexpr int PASS = E < 8 ? E : 8;          // elements of a row segment joined at once
+  constexpr int PITCH = 16 * PASS + 4;
+  __shared__ __align__(16) union {
+    int8_t q[2][16][D + 16];
+    float o[kWaves][16][PITCH];
+  } sh;
+  __shared__ float qscale[ROWS];
+  __shared__ float stat[kWaves][16][2];
+  __shared__ int pages[kChunkMax / CONVROT_KV_PAGE_MIN + 1];
+
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, col = lane % 16, quad = lane / 16;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x % sp.splits, tile = blockIdx.x / sp.splits;
+  const int c0 = split * sp.chunk, log2p = a.c.page_log2;
+
+  const KvSeq s = kv_sequence(a, b);
+  const int rows = s.n * a.group - tile * ROWS;      // valid rows from this tile on
+  if (rows <= 0) return;
+  // the tokens that the tile's last and first row see
+  const int last = a.causal ? s.kv - s.n + (tile * ROWS + (rows < ROWS ? rows : ROWS) - 1) / a.group + 1 : s.kv;
+  const int first = a.causal ? s.kv - s.n + tile * ROWS / a.group + 1 : s.kv;
+  const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
+  if (c1 <= c0 && split > 0) return;                 // the join leaves it out by the same rule
+
+  const int page0 = c0 >> log2p, npages = c1 > c0 ? ((c1 - 1) >> log2p) - page0 + 1 : 0;
+  for (int i = tid; i < npages; i += 64 * kWaves) {
+    const int p = a.table[(int64_t)b * a.width + page0 + i];
+    pages[i] = p >= 0 && p < a.c.pages ? p : -1;
+  }
+
+  // ---- the rotated queries, as two int8 planes
+  v4i q[QT][2][KM];
+  float qf[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    __syncthreads();
+    const int r = tid / 16, seg = tid % 16;          // 16 rows, E elements a lane
+    const int row = tile * ROWS + 16 * t + r;
+    const int i = row / a.group, head = h * a.group + row - i * a.group;
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.0f;
+    if (i < s.n) load_row<E>(a.q.p + (s.first + i) * a.q.token + head * a.q.head + seg * E, a.bf16, x);
+    rotate_row<D>(x, seg);
+    float top = 0.0f;
+    bool fine = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e])), fine = fine && fabsf(x[e]) < INFINITY;
+    top = warp_max16(top);
+    const float to = top > 0.0f ? 32512.0f / top : 0.0f;
+    int8_t hi[E], lo[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int n = (int)rintf(x[e] * to);
+      hi[e] = (int8_t)((n + 128) >> 8);
+      lo[e] = (int8_t)(n - (((n + 128) >> 8) << 8));
+    }
+    // element order of the key operand: 4-bit codes take the even elements of each D / 4 first
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int d = seg * E + e;
+      const int at = BITS == 8 ? d : d / (D / 4) * (D / 4) + d % 2 * (D / 8) + d % (D / 4) / 2;
+      sh.q[0][r][at] = hi[e];
+      sh.q[1][r][at] = lo[e];
+    }
+    // sm_scale, the rotation's 1 / sqrt(D), the fixed point and the codes' 16
+    const float f = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * (top / 32512.0f) *
+                    (BITS == 4 ? 0.0625f : 1.0f);
+    const uint64_t bad = __ballot(!fine);
+    if (seg == 0) qscale[16 * t + r] = (bad >> (lane & 48)) & 0xFFFFu ? __uint_as_float(0x7FC00000u) : fmaxf(f, 1e-37f);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int m = 0; m < KM; ++m)
+        q[t][p][m] = *reinterpret_cast<const v4i*>(&sh.q[p][col][quad * (D / 4) + 16 * m]);
+    qf[t] = qscale[16 * t + col];
+  }
+  const float flip = a.scale < 0.0f ? -1.0f : 1.0f;
+  int end[QT];                                        // tokens this lane's row sees
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int i = (tile * ROWS + 16 * t + col) / a.group;
+    end[t] = i >= s.n ? 0 : a.causal ? s.kv - s.n + i + 1 : s.kv;
+  }
+
+  v4f o[QT][E];
+  float m[QT], l[QT], vmax = 0x1p-126f;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    m[t] = kLowest;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[t][i] = (v4f){0, 0, 0, 0};
+  }
+
+  auto page_of = [&](int j) { return __builtin_amdgcn_readfirstlane(j < c1 ? pages[(j >> log2p) - page0] : -1); };
+  auto load = [&](T& x, int j0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = j0 + 16 * u, p = page_of(j);
+      const int64_t at = (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
+      load_codes<T::kKeyBytes>(a.c.kc + (at + col) * T::kRow + quad * T::kKeyBytes, x.k[u]);
+      x.ks[u] = *reinterpret_cast<const v4f*>(a.c.ks + at + 4 * quad);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        load_codes<T::kValueBytes>(a.c.vc + (at + 4 * quad + r) * T::kRow + col * T::kValueBytes, x.v[u][r]);
+      x.vs[u] = *reinterpret_cast<const v4f*>(a.c.vs + at + 4 * quad);
+    }
+  };
+
+  auto use = [&](T& x, int j0) {
+    const bool whole = j0 + kStep <= first && page_of(j0) >= 0 && page_of(j0 + 16) >= 0;
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool here = page_of(j0 + 16 * u) >= 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool in = here && j0 + 16 * u + 4 * quad + r < c1;
+          x.ks[u][r] = in ? x.ks[u][r] : 0.0f;
+          x.vs[u][r] = in ? x.vs[u][r] : 0.0f;
+        }
+      }
+    }
+    // the values' scales, against the power of two that holds them all
+    float most = vmax;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) most = fmaxf(most, x.vs[u][r]);
+    if (__any(most > vmax)) {
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      // twice the power of two above the largest: room for it to double
+      const uint32_t e = (__float_as_uint(most) >> 23) + 2u;
+      const float next = __uint_as_float(__builtin_amdgcn_readfirstlane((e < 254u ? e : 254u) << 23));
+      const float by = vmax / next;
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[t][i] *= by;
+      vmax = next;
+    }
+    const float vnorm = 1.0f / vmax;
+    v4f vs[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) vs[u] = x.vs[u] * vnorm;
+
+    v8h w[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      float sc[2][4], best = kLowest;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        v4i hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+          const v4i c = key_operand<D, BITS>(x.k[u], k);
+          hi = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, q[t][0][k], hi, 0, 0, 0);
+          lo = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, q[t][1][k], lo, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sc[u][r] = (float)((hi[r] << 8) + lo[r]) * (x.ks[u][r] * (qf[t] * flip));
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = j0 + 16 * u + 4 * quad + r;
+            sc[u][r] = j < end[t] && page_of(j0 + 16 * u) >= 0 ? sc[u][r] : -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) best = fmaxf(best, sc[u][r]);
+      if (__any(best > m[t] + kRaise)) {
+        best = fmaxf(best, __shfl_xor(best, 16));
+        best = fmaxf(best, __shfl_xor(best, 32));
+        const float next = fmaxf(m[t], best), by = __builtin_amdgcn_exp2f(m[t] - next);
+        l[t] *= by;
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[t][i] *= by;
+        m[t] = next;
+      }
+      const float base = kWeightBits - m[t];
+      float p[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[4 * u + r] = __builtin_amdgcn_exp2f(sc[u][r] + base);
+      l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      v4u packed;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int u = e / 2, r = 2 * (e % 2);
+        float wa = p[2 * e] * vs[u][r], wb = p[2 * e + 1] * vs[u][r + 1];
+        if (!whole) {   // a token that another row sees may have a NaN scale
+          wa = p[2 * e] == 0.0f ? 0.0f : wa;
+          wb = p[2 * e + 1] == 0.0f ? 0.0f : wb;
+        }
+        packed[e] = pack_f16x2_rn(wa, wb);
+      }
+      w[t] = __builtin_bit_cast(v8h, packed);
+    }
+    v4u f[E];
+    value_operands<D, BITS>(x.v, f);
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+        o[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f[i]), w[t], o[t][i], 0, 0, 0);
+  };
+
+  constexpr int kStride = kStep * kWaves;
+  int j = c0 + kStep * wave;
+  T x, y;
+  if (j < c1) load(x, j);
+  for (; j < c1; j += 2 * kStride) {
+    if (j + kStride < c1) load(y, j + kStride);
+    use(x, j);
+    if (j + kStride >= c1) break;
+    if (j + 2 * kStride < c1) load(x, j + 2 * kStride);
+    use(y, j + kStride);
+  }
+
+  // ---- join the wavefronts, 16 rows at a time
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    __syncthreads();
+    if (quad == 0) {
+      stat[wave][col][0] = m[t];
+      stat[wave][col][1] = l[t];
+    }
+    __syncthreads();
+    float top = kLowest;
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) top = fmaxf(top, stat[v][col][0]);
+    const float mine = __builtin_amdgcn_exp2f(m[t] - top) * vmax;
+    const int r = tid / 16, seg = tid % 16;
+    float rtop = kLowest, sum = 0.0f, out[E];
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) rtop = fmaxf(rtop, stat[v][r][0]);
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) sum += __builtin_amdgcn_exp2f(stat[v][r][0] - rtop) * stat[v][r][1];
+#pragma unroll
+    for (int p = 0; p < E / PASS; ++p) {
+      if (p) __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < PASS; ++i)
+          sh.o[wave][col][PASS * (4 * quad + e) + i] =
+              o[t][PASS * p + i][e] * (BITS == 4 && i % 2 ? mine * 0.0625f : mine);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) {
+        float z = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) z += sh.o[v][r][PASS * seg + i];
+        out[PASS * p + i] = z;
+      }
+    }
+    const int rr = 16 * t + r;
+    if (sp.splits > 1) {
+      if (rr < rows) {
+        const int64_t at = sp.row(b, h, tile, split, rr);
+        float* dst = sp.o + at * D + seg * E;
+#pragma unroll
+        for (int i = 0; i < E; i += 4) *reinterpret_cast<v4f*>(dst + i) = (v4f){out[i], out[i + 1], out[i + 2], out[i + 3]};
+        if (seg == 0) {
+          sp.ml[2 * at] = rtop;
+          sp.ml[2 * at + 1] = sum;
+        }
+      }
+    } else {
+      const float by = sum == 0.0f ? 0.0f : kv_rsqrt(D) / sum;
+#pragma unroll
+      for (int i = 0; i < E; ++i) out[i] = sum == 0.0f ? 0.0f : out[i] * by;
+      rotate_row<D>(out, seg);
+      if (rr < rows) {
+        const int row = tile * ROWS + rr, i = row / a.group, head = h * a.group + row - i * a.group;
+        store_row<E>(a.o + ((s.first + i) * a.q_heads + head) * D + seg * E, a.bf16, out);
+      }
+    }
+  }
+}
+
+// Joins the splits of each row: segments of 16 lanes take the splits in turn,
+// E elements a lane, then one segment rotates the row back.
+template <int D>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int segs) {
+  constexpr int E = D / 16;
+  __shared__ float part[16][D + 4];
+  __shared__ float stat[16][2];
+  const int sub = threadIdx.x / 16, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
+  const KvSeq s = kv_sequence(a, b);
+  const int row = blockIdx.x * (16 / segs) + sub / segs;     // of the sequence's rows with this key head
+  const int i = row / a.group;
+  const bool valid = i < s.n;
+  const int tile = row / sp.rows, rr = row - tile * sp.rows;
+  // the splits that the row's tile ran: up to the last token its last row sees
+  int last = s.kv;
+  if (a.causal) {
+    int r1 = (tile + 1) * sp.rows - 1;
+    r1 = r1 < s.n * a.group ? r1 : s.n * a.group - 1;
+    last = s.kv - s.n + r1 / a.group + 1;
+  }
+  int n = (last + sp.chunk - 1) / sp.chunk;
+  n = valid ? (n < 1 ? 1 : n < sp.splits ? n : sp.splits) : 0;
+  float m = kLowest, l = 0.0f, x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+  for (int z = sub % segs; z < n; z += segs) {
+    const int64_t at = sp.row(b, h, tile, z, rr);
+    const float mz = sp.ml[2 * at], lz = sp.ml[2 * at + 1];
+    v4f o[E / 4];
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) o[e] = *reinterpret_cast<const v4f*>(sp.o + at * D + seg * E + 4 * e);
+    const float next = fmaxf(m, mz), keep = __builtin_amdgcn_exp2f(m - next), add = __builtin_amdgcn_exp2f(mz - next);
+    m = next;
+    l = l * keep + lz * add;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = x[e] * keep + o[e / 4][e % 4] * add;
+  }
+  if (seg == 0) {
+    stat[sub][0] = m;
+    stat[sub][1] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[sub][seg * E + e] = x[e];
+  __syncthreads();
+  if (sub % segs || !valid) return;
+  float top = kLowest, sum = 0.0f;
+  for (int z = 0; z < segs; ++z) top = fmaxf(top, stat[sub + z][0]);
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+  for (int z = 0; z < segs; ++z) {
+    const float by = __builtin_amdgcn_exp2f(stat[sub + z][0] - top);
+    sum += by * stat[sub + z][1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] += by * part[sub + z][seg * E + e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] * (kv_rsqrt(D) / sum);
+  rotate_row<D>(x, seg);
+  store_row<E>(a.o + ((s.first + i) * a.q_heads + h * a.group + row - i * a.group) * D + seg * E, a.bf16, x);
+}
+
+template <int D, int BITS, int QT>
+hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
+  KvSplit sp = p.split;
+  sp.o = static_cast<float*>(workspace);
+  sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
+  kv_decode_kernel<D, BITS, QT><<<dim3(sp.splits * sp.tiles, a.c.heads, a.batch), 64 * kWaves, 0, stream>>>(a, sp);
+  if (sp.splits > 1) {
+    int segs = 1;
+    while (segs < 16 && segs < sp.splits) segs *= 2;
+    const unsigned per = 16 / segs, rows = (unsigned)a.max_q * a.group;
+    kv_join_kernel<D><<<dim3((rows + per - 1) / per, a.c.heads, a.batch), 256, 0, stream>>>(a, sp, segs);
+  }
+  return hipGetLastError();
+}
+
+template <int D, int BITS>
+hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
+  return p.split.rows == 16 ? run<D, BITS, 1>(a, p, workspace, stream) : run<D, BITS, 2>(a, p, workspace, stream);
+}
+
+}  // namespace
+
+KvPlan kv_decode_plan(const KvAttn& a) {
+  KvPlan p{};
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  KvSplit& s = p.split;
+  s.rows = rows <= 16 ? 16 : 32;
+  s.tiles = (int)((rows + s.rows - 1) / s.rows);
+  s.kept = (int)(rows < s.rows ? rows : s.rows);
+  s.heads = a.c.heads;
+  const int64_t base = (int64_t)s.tiles * a.c.heads * a.batch;
+  int64_t splits = (1024 + base - 1) / base;
+  const int64_t most = (a.max_kv + 255) / 256, least = ((int64_t)a.max_kv + kChunkMax - 1) / kChunkMax;
+  if (splits > most) splits = most;
+  if (splits < least) splits = least;
+  if (splits < 1) splits = 1;
+  const int64_t chunk = (a.max_kv + splits - 1) / splits;
+  s.chunk = (int)((chunk + 127) / 128 * 128);
+  if (s.chunk < 128) s.chunk = 128;
+  s.splits = (int)((a.max_kv + s.chunk - 1) / s.chunk);
+  if (s.splits < 1) s.splits = 1;
+  p.parts = s.splits > 1 ? base * s.splits * s.kept : 0;
+  p.bytes = (size_t)p.parts * (a.c.head_dim + 2) * 4;
+  return p;
+}
+
+hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
+  switch (a.c.head_dim * 16 + a.c.bits) {
+    case 64 * 16 + 4: return run<64, 4>(a, p, workspace, stream);
+    case 64 * 16 + 8: return run<64, 8>(a, p, workspace, stream);
+    case 128 * 16 + 4: return run<128, 4>(a, p, workspace, stream);
+    case 128 * 16 + 8: return run<128, 8>(a, p, workspace, stream);
+    case 256 * 16 + 4: return run<256, 4>(a, p, workspace, stream);
+    default: return run<256, 8>(a, p, workspace, stream);
+  }
+}
+
+}  // namespace convrot
