@@ -73,12 +73,13 @@ def read_f32(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
 
 def attention(q, k, v, scale, causal):
     """q [n, heads_q, D], k and v [m, heads, D] of one sequence, float64 ->
-    (o [n, heads_q, D], spread [n, heads_q]): o by the definition (zeros where
-    no key is visible), and spread = sum_j p_j |v_j|, the size that rounding
-    errors of the softmax weights are relative to."""
+    (o [n, heads_q, D], spread [n, heads_q, 2]): o by the definition (zeros
+    where no key is visible), and what rounding errors of the softmax weights
+    are relative to: spread[..., 0] = sum_j p_j |v_j| for errors that add up,
+    spread[..., 1] = sqrt(sum_j p_j^2 |v_j|^2) for independent ones."""
     n, hq, d = q.shape
     m, h = k.shape[0], k.shape[1]
-    o, spread = np.zeros((n, hq, d)), np.zeros((n, hq))
+    o, spread = np.zeros((n, hq, d)), np.zeros((n, hq, 2))
     for a in range(hq if m else 0):
         s = scale * (q[:, a] @ k[:, a // (hq // h)].T)
         if causal:
@@ -89,5 +90,7 @@ def attention(q, k, v, scale, causal):
         p = np.divide(e, total, out=np.zeros_like(e), where=total > 0)
         vh = v[:, a // (hq // h)]
         o[:, a] = p @ vh
-        spread[:, a] = p @ np.sqrt((vh * vh).sum(-1))
+        size = (vh * vh).sum(-1)
+        spread[:, a, 0] = p @ np.sqrt(size)
+        spread[:, a, 1] = np.sqrt((p * p) @ size)
     return o, spread

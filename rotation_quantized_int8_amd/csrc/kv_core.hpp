@@ -28,6 +28,10 @@ struct KvPlan {
 
 KvPlan kv_decode_plan(const KvAttn& a);
 hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream);
+KvPlan kv_prompt_plan(const KvAttn& a);
+hipError_t launch_kv_prompt(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream);
+// The finished rows from the splits' partial ones.
+hipError_t launch_kv_join(const KvAttn& a, const KvSplit& sp, hipStream_t stream);
 
 // The value of the lane whose number in its 16-lane row differs in bit BIT.
 template <int BIT>

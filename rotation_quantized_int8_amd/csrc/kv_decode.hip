@@ -489,13 +489,8 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
   sp.o = static_cast<float*>(workspace);
   sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
   kv_decode_kernel<D, BITS, QT><<<dim3(sp.splits * sp.tiles, a.c.heads, a.batch), 64 * kWaves, 0, stream>>>(a, sp);
-  if (sp.splits > 1) {
-    int segs = 1;
-    while (segs < 16 && segs < sp.splits) segs *= 2;
-    const unsigned per = 16 / segs, rows = (unsigned)a.max_q * a.group;
-    kv_join_kernel<D><<<dim3((rows + per - 1) / per, a.c.heads, a.batch), 256, 0, stream>>>(a, sp, segs);
-  }
-  return hipGetLastError();
+  if (hipError_t e = hipGetLastError()) return e;
+  return sp.splits > 1 ? launch_kv_join(a, sp, stream) : hipSuccess;
 }
 
 template <int D, int BITS>
@@ -527,6 +522,17 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   p.parts = s.splits > 1 ? base * s.splits * s.kept : 0;
   p.bytes = (size_t)p.parts * (a.c.head_dim + 2) * 4;
   return p;
+}
+
+hipError_t launch_kv_join(const KvAttn& a, const KvSplit& sp, hipStream_t stream) {
+  int segs = 1;
+  while (segs < 16 && segs < sp.splits) segs *= 2;
+  const unsigned per = 16 / segs, rows = (unsigned)a.max_q * a.group;
+  const dim3 grid((rows + per - 1) / per, a.c.heads, a.batch);
+  if (a.c.head_dim == 64) kv_join_kernel<64><<<grid, 256, 0, stream>>>(a, sp, segs);
+  else if (a.c.head_dim == 128) kv_join_kernel<128><<<grid, 256, 0, stream>>>(a, sp, segs);
+  else kv_join_kernel<256><<<grid, 256, 0, stream>>>(a, sp, segs);
+  return hipGetLastError();
 }
 
 hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {

@@ -1,0 +1,531 @@
+// Attention of many query rows over the rotated, quantised key/value cache:
+// prompts, chunks of prompts, cross attention.
+//
+// The mathematics is that of the single-token kernel (kv_decode.hip): rotate
+// the queries once, use the codes as they are with their scales outside the
+// products, rotate the result back.  Here the arithmetic counts, so a
+// workgroup of 4 wavefronts takes 128 rows (queries times heads of one group)
+// and shares the decoding: of each 64 tokens every thread turns a 128th of
+// the codes into fp16 (exact) and writes them to LDS in the order in which
+// the matrix instructions take their operands (16 bytes a lane, no bank
+// conflicts), two buffers deep, so that a step costs one barrier.
+//   S^T = C_k Q^T     mfma f32 32x32x16 f16, 32 tokens x 32 rows
+//   O^T = C_v^T W^T   the same, 32 elements x 32 rows
+// A lane owns one row (column lane % 32); the result layout of S^T is the
+// operand layout of W^T up to an order of the tokens that C_v^T is stored in.
+// The rotated queries are rounded to fp16 after a power of two common to the
+// workgroup; it, sm_scale and log2 e are multiplied into the keys' scales, so
+// a weight is exp2(fma(S, scale_j, base_row)): one operation, its exponential
+// and the product with the value's scale, against 2 D / 32 matrix operations
+// of 8 passes for 32 elements of S.  The running maximum is raised only when
+// a weight passes 2^15 (they start at 2^8 for the largest).
+
+#include "kv_core.hpp"
+#include "launch.hpp"
+
+namespace convrot {
+namespace {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;
+constexpr int kStep = 64;                     // tokens of a step
+constexpr float kWeightBits = 8.0f;
+constexpr float kMostWeight = 32768.0f;
+constexpr float kUnset = 1e30f;               // base of a row that has seen no token
+constexpr float kLowest = -1e30f;             // its maximum
+
+__device__ __forceinline__ uint32_t less(uint32_t x, float by) {
+  const h2 off = {(_Float16)by, (_Float16)by};
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) - off);
+}
+
+// Eight codes as fp16 operands of the keys.  4 bits: elements 0 4 1 5 2 6 3 7,
+// the odd ones times 16; 8 bits: in order.
+template <int BITS>
+__device__ __forceinline__ v4u key_halves(const uint32_t* w) {
+  v4u f;
+  if constexpr (BITS == 4) {
+    const uint32_t x = w[0] ^ 0x88888888u, y = x >> 8;
+    f[0] = less((x & 0x000F000Fu) | 0x64006400u, 1032.0f);
+    f[1] = less((x & 0x00F000F0u) | 0x64006400u, 1152.0f);
+    f[2] = less((y & 0x000F000Fu) | 0x64006400u, 1032.0f);
+    f[3] = less((y & 0x00F000F0u) | 0x64006400u, 1152.0f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = less(__builtin_amdgcn_perm(0, w[i / 2], i % 2 ? 0x0C030C02u : 0x0C010C00u) ^ 0x64806480u, 1152.0f);
+  }
+  return f;
+}
+
+// Element of its unit of 8 that half j of a key operand holds, and the factor
+// that its code enters with.
+template <int BITS>
+__device__ __forceinline__ constexpr int key_element(int j) {
+  return BITS == 8 ? j : j / 2 + 4 * (j % 2);
+}
+template <int BITS>
+__device__ __forceinline__ constexpr float key_factor(int e) { return BITS == 4 && e % 2 ? 16.0f : 1.0f; }
+
+// Element i of the unit for two tokens a and b, as a half pair (4 bits: the
+// odd elements times 16).
+template <int BITS>
+__device__ __forceinline__ void value_halves(const uint32_t* a, const uint32_t* b, uint32_t (&f)[8]) {
+  if constexpr (BITS == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const uint32_t x = __builtin_amdgcn_perm(b[0], a[0], i ? 0x07060302u : 0x05040100u) ^ 0x88888888u, y = x >> 8;
+      f[i] = less((x & 0x000F000Fu) | 0x64006400u, 1032.0f);
+      f[i + 1] = less((x & 0x00F000F0u) | 0x64006400u, 1152.0f);
+      f[i + 2] = less((y & 0x000F000Fu) | 0x64006400u, 1032.0f);
+      f[i + 3] = less((y & 0x00F000F0u) | 0x64006400u, 1152.0f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f[i] = less(__builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)(i % 4) * 0x00010001u) ^ 0x64806480u,
+                  1152.0f);
+  }
+}
+
+template <int D, int BITS>
+struct Prompt {
+  static constexpr int kRow = D * BITS / 8;            // bytes of a cached row
+  static constexpr int kUnit = BITS;                   // bytes of 8 codes
+  static constexpr int kUnits = D / 8;
+  static constexpr int kSteps = D / 16;                // matrix steps of a score
+  static constexpr int kTiles = D / 32;                // output tiles
+  static constexpr int kSpread = 256 / D;              // elements of a unit that share an output tile
+  // decoding: a key task is 16 bytes of one token's row, a value task one unit of 4 tokens
+  static constexpr int kKeyTasks = kStep * kRow / 16, kValueTasks = kStep / 4 * kUnits;
+  static constexpr int kKeyEach = (kKeyTasks + kThreads - 1) / kThreads;
+  static constexpr int kValueEach = (kValueTasks + kThreads - 1) / kThreads;
+  static constexpr int kBuffer = kStep * D * 2;        // bytes of a step's keys, and of its values
+  static constexpr int kQPitch = D * 2 + 16;
+  static constexpr int kBytes = 4 * kBuffer > kRows * kQPitch ? 4 * kBuffer : kRows * kQPitch;
+};
+
+template <int D, int BITS>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(KvAttn a, KvSplit sp) {
+  using P = Prompt<D, BITS>;
+  constexpr int E = D / 16;
+  extern __shared__ __align__(16) char lds[];          // keys [2], values [2]; first the queries
+  __shared__ __align__(16) float kscale[2][kStep], vscale[2][kStep];
+  __shared__ __align__(16) int absent[2][4];
+  __shared__ float vtop[2];
+  __shared__ float qtop[kWaves];
+
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, col = lane % 32, hi = lane / 32;
+  const int b = blockIdx.z;
+  // the key head is the fastest index, so that the workgroups of one head meet in one XCD's L2 where the head
+  // count is a multiple of 8; the last tiles, which see the most tokens, start first
+  const int h = blockIdx.x % a.c.heads;
+  const int rest = blockIdx.x / a.c.heads;
+  const int split = rest % sp.splits, tile = sp.tiles - 1 - rest / sp.splits;
+  const int log2p = a.c.page_log2;
+
+  const KvSeq s = kv_sequence(a, b);
+  const int rows = s.n * a.group - tile * kRows;
+  if (rows <= 0) return;
+  const int c0 = split * sp.chunk;
+  const int last = a.causal ? s.kv - s.n + (tile * kRows + (rows < kRows ? rows : kRows) - 1) / a.group + 1 : s.kv;
+  const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
+  if (c1 <= c0 && split > 0) return;
+
+  // ---- raw codes and scales of a step, prefetched into registers
+  struct Raw {
+    v4u k[P::kKeyEach];
+    uint32_t v[P::kValueEach][4][P::kUnit / 4];
+    float scale;
+    int page;                                          // of the scale's token
+  } raw;
+  const int pages = a.c.pages;
+  auto page_of = [&](int j) {
+    const int p = j < c1 ? a.table[(int64_t)b * a.width + (j >> log2p)] : -1;
+    return p >= 0 && p < pages ? p : -1;
+  };
+  auto row_of = [&](int j, int p) {
+    return (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
+  };
+  int kp[P::kKeyEach], vp[P::kValueEach], scp;         // pages of the next step's tokens
+  auto find = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < P::kKeyEach; ++i) {
+      const int task = tid + i * kThreads;
+      kp[i] = page_of(j0 + task / P::kRow * 16 + task % 16);
+    }
+#pragma unroll
+    for (int i = 0; i < P::kValueEach; ++i) vp[i] = page_of(j0 + (tid + i * kThreads) / P::kUnits * 4);
+    scp = page_of(j0 + tid % kStep);
+  };
+  // a key task is the 16-byte piece task / 16 % (row / 16) of token task % 16 of a group of 16 tokens (row tasks a
+  // group), so that 16 lanes write neighbouring operands
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < P::kKeyEach; ++i) {
+      const int task = tid + i * kThreads;
+      if (P::kKeyTasks % kThreads == 0 || task < P::kKeyTasks) {
+        const int j = j0 + task / P::kRow * 16 + task % 16, piece = task / 16 % (P::kRow / 16);
+        raw.k[i] = *reinterpret_cast<const v4u*>(a.c.kc + row_of(j, kp[i]) * P::kRow + piece * 16);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < P::kValueEach; ++i) {
+      const int task = tid + i * kThreads;
+      if (P::kValueTasks % kThreads == 0 || task < P::kValueTasks) {
+        const int j = j0 + task / P::kUnits * 4, unit = task % P::kUnits;
+        const uint8_t* p = a.c.vc + row_of(j, vp[i]) * P::kRow + unit * P::kUnit;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int w = 0; w < P::kUnit / 4; ++w)
+            raw.v[i][t][w] = reinterpret_cast<const uint32_t*>(p + t * P::kRow)[w];
+      }
+    }
+    if (tid < 2 * kStep) {
+      const int j = j0 + tid % kStep;
+      raw.page = j < c1 ? scp : -1;
+      raw.scale = (tid < kStep ? a.c.ks : a.c.vs)[row_of(j, scp)];
+    }
+  };
+
+  find(c0);
+  load(c0);
+  find(c0 + kStep);
+
+  // ---- the rotated queries as fp16, in the element order of the key operands
+  float common;                                        // what a score's product is multiplied by, without the key's scale
+  v8h q[P::kSteps];
+  {
+    constexpr int kPass = kRows / 16;
+    float x[kPass][E];
+    const int r = tid / 16, seg = tid % 16;
+    float top = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kPass; ++t) {
+      const int row = tile * kRows + 16 * t + r, i = row / a.group, head = h * a.group + row - i * a.group;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[t][e] = 0.0f;
+      if (i < s.n) load_row<E>(a.q.p + (s.first + i) * a.q.token + head * a.q.head + seg * E, a.bf16, x[t]);
+      rotate_row<D>(x[t], seg);
+#pragma unroll
+      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[t][e]) < INFINITY ? fabsf(x[t][e]) : 0.0f);
+    }
+    top = wave_max64(top);
+    if (lane == 0) qtop[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, qtop[w]);
+    // 2^e above the largest, so that the queries enter below 1
+    const uint32_t e = (__float_as_uint(top) >> 23) + 1u;
+    const float unit = __uint_as_float((e < 1u ? 1u : e > 253u ? 253u : e) << 23);
+    const float by = (a.scale < 0.0f ? -1.0f : 1.0f) / unit;
+    common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit;
+#pragma unroll
+    for (int t = 0; t < kPass; ++t) {
+      _Float16* dst = reinterpret_cast<_Float16*>(lds + (16 * t + r) * P::kQPitch);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int d = seg * E + i, e8 = d % 8;
+        // where element e8 of its unit stands in the operand
+        const int at = BITS == 8 ? e8 : 2 * (e8 % 4) + e8 / 4;
+        dst[d / 8 * 8 + at] = (_Float16)(x[t][i] * (by / key_factor<BITS>(e8)));
+      }
+    }
+    __syncthreads();
+    const char* mine = lds + (32 * wave + col) * P::kQPitch;
+#pragma unroll
+    for (int k = 0; k < P::kSteps; ++k) q[k] = *reinterpret_cast<const v8h*>(mine + (2 * k + hi) * 16);
+    __syncthreads();
+  }
+
+  char* kbuf = lds;
+  char* vbuf = lds + 2 * P::kBuffer;
+  float vmax = 0x1p-126f;                              // of the scales written so far (kept by wave 1)
+  auto decode = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < P::kKeyEach; ++i) {
+      const int task = tid + i * kThreads;
+      if (P::kKeyTasks % kThreads == 0 || task < P::kKeyTasks) {
+        const int j = task / P::kRow * 16 + task % 16, piece = task / 16 % (P::kRow / 16);
+#pragma unroll
+        for (int n = 0; n < 16 / P::kUnit; ++n) {
+          const int unit = piece * (16 / P::kUnit) + n;
+          uint32_t w[P::kUnit / 4];
+#pragma unroll
+          for (int z = 0; z < P::kUnit / 4; ++z) w[z] = raw.k[i][n * (P::kUnit / 4) + z];
+          *reinterpret_cast<v4u*>(kbuf + buf * P::kBuffer +
+                                  (((j / 32) * P::kSteps + unit / 2) * 64 + unit % 2 * 32 + j % 32) * 16) =
+              key_halves<BITS>(w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < P::kValueEach; ++i) {
+      const int task = tid + i * kThreads;
+      if (P::kValueTasks % kThreads == 0 || task < P::kValueTasks) {
+        const int j = task / P::kUnits * 4, unit = task % P::kUnits;
+        uint32_t f01[8], f23[8];
+        value_halves<BITS>(raw.v[i][0], raw.v[i][1], f01);
+        value_halves<BITS>(raw.v[i][2], raw.v[i][3], f23);
+        // tokens 16 u + 8 half + 4 g + 0..3: step u, lanes of half-wave g, the operand's half `half`
+        const int u = j / 16, half = j / 8 % 2, g = j / 4 % 2;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int t = e / P::kSpread, row = e % P::kSpread * P::kUnits + unit;
+          *reinterpret_cast<v2u*>(vbuf + buf * P::kBuffer + ((t * 4 + u) * 64 + g * 32 + row) * 16 + half * 8) =
+              (v2u){f01[e], f23[e]};
+        }
+      }
+    }
+    if (wave == 0) {
+      kscale[buf][lane] = raw.scale * common;
+      if (lane % 16 == 0) absent[buf][lane / 16] = raw.page < 0;
+    } else if (wave == 1) {
+      const float v = raw.page < 0 ? 0.0f : raw.scale;
+      if (__any(v > vmax)) {
+        float most = wave_max64(fmaxf(v, vmax));
+        const uint32_t e = (__float_as_uint(most) >> 23) + 2u;   // room for the largest to double
+        vmax = __uint_as_float((e < 254u ? e : 254u) << 23);
+      }
+      vscale[buf][lane] = v * (1.0f / vmax);
+      if (lane == 0) vtop[buf] = vmax;
+    }
+  };
+
+  // ---- the steps
+  const int myrow = tile * kRows + 32 * wave + col, myquery = myrow / a.group;
+  const int end = myquery >= s.n ? 0 : a.causal ? s.kv - s.n + myquery + 1 : s.kv;
+  const int first = a.causal ? s.kv - s.n + (tile * kRows + 32 * wave) / a.group + 1 : s.kv;   // the wavefront's first row
+  v16f o[P::kTiles];
+  float base = kUnset, l = 0.0f, vnow = 0x1p-126f;
+#pragma unroll
+  for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
+
+  auto use = [&](int buf, int j0) {
+    const float v = vtop[buf];
+    if (v != vnow) {
+      const float by = vnow / v;
+#pragma unroll
+      for (int t = 0; t < P::kTiles; ++t) o[t] *= by;
+      vnow = v;
+    }
+    const v4i gone = *reinterpret_cast<const v4i*>(absent[buf]);
+    const bool whole = __builtin_amdgcn_readfirstlane(j0 + kStep <= first && !(gone[0] | gone[1] | gone[2] | gone[3]));
+    v16f p[2];                                         // scores, then weights
+    auto score = [&]() {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) p[kt][r] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < P::kSteps; ++k) {
+          const v8h c = *reinterpret_cast<const v8h*>(kbuf + buf * P::kBuffer + ((kt * P::kSteps + k) * 64 + lane) * 16);
+          p[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[k], p[kt], 0, 0, 0);
+        }
+      }
+    };
+    auto seen = [&](int kt, int r) {
+      return j0 + 32 * kt + 8 * (r / 4) + 4 * hi + r % 4 < end && !gone[2 * kt + r / 8];
+    };
+    auto weigh = [&]() {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[kt][r + i] = __builtin_amdgcn_exp2f(__fmaf_rn(p[kt][r + i], ks[i], base));
+        }
+      if (!whole) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) p[kt][r] = seen(kt, r) ? p[kt][r] : 0.0f;
+      }
+    };
+    score();
+    weigh();
+    float most = fmaxf(p[0][0], p[1][0]);
+#pragma unroll
+    for (int r = 1; r < 16; ++r) most = fmaxf(fmaxf(most, p[0][r]), p[1][r]);
+    if (__any(most > kMostWeight)) {                   // rare: form the scores again
+      score();
+      float best = kLowest;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) best = fmaxf(best, whole || seen(kt, r + i) ? p[kt][r + i] * ks[i] : kLowest);
+        }
+      best = fmaxf(best, __shfl_xor(best, 32));
+      const float next = fminf(base, kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base);
+      l *= by;
+#pragma unroll
+      for (int t = 0; t < P::kTiles; ++t) o[t] *= by;
+      base = next;
+      weigh();
+    }
+    v4u w[4];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
+        l += (p[kt][r] + p[kt][r + 1]) + (p[kt][r + 2] + p[kt][r + 3]);
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = p[kt][r + i] * vs[i];
+          if (!whole) x[i] = p[kt][r + i] == 0.0f ? 0.0f : x[i];   // a token that another row sees may have a NaN scale
+        }
+        w[2 * kt + r / 8][r % 8 / 2] = pack_f16x2_rn(x[0], x[1]);
+        w[2 * kt + r / 8][r % 8 / 2 + 1] = pack_f16x2_rn(x[2], x[3]);
+      }
+#pragma unroll
+    for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const v8h c = *reinterpret_cast<const v8h*>(vbuf + buf * P::kBuffer + ((t * 4 + u) * 64 + lane) * 16);
+        o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, __builtin_bit_cast(v8h, w[u]), o[t], 0, 0, 0);
+      }
+  };
+
+  if (c1 > c0) {
+    decode(0);
+    load(c0 + kStep);
+    find(c0 + 2 * kStep);
+    __syncthreads();
+    int buf = 0;
+    for (int j = c0; j < c1; j += kStep, buf ^= 1) {
+      if (j + kStep < c1) {
+        decode(buf ^ 1);
+        load(j + 2 * kStep);
+        find(j + 3 * kStep);
+      }
+      use(buf, j);
+      __syncthreads();
+    }
+  }
+
+  // ---- a lane holds half a row: rotate it back (every bit of (tile, register) and the half-wave is a bit of the
+  // element's number), or leave it to the join
+  l += __shfl_xor(l, 32);
+  if (myquery >= s.n || 32 * wave + col >= rows) return;
+  // element of (tile t, register r): row = 8 (r / 4) + 4 hi + r % 4, unit = row % kUnits, e = t * kSpread + row / kUnits
+  auto unit_of = [&](int r) { return (8 * (r / 4) + 4 * hi + r % 4) % P::kUnits; };
+  auto e_of = [&](int t, int r) { return t * P::kSpread + 8 * (r / 4) / P::kUnits; };
+  if (sp.splits > 1) {
+    const int64_t at = sp.row(b, h, tile, split, 32 * wave + col);
+    float* dst = sp.o + at * D;
+#pragma unroll
+    for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        dst[8 * unit_of(r) + e_of(t, r)] = o[t][r] * (vnow * (BITS == 4 && e_of(t, r) % 2 ? 0.0625f : 1.0f));
+    if (hi == 0) {
+      sp.ml[2 * at] = base == kUnset ? kLowest : kWeightBits - base;
+      sp.ml[2 * at + 1] = l;
+    }
+    return;
+  }
+  const float by = l == 0.0f ? 0.0f : kv_rsqrt(D) * vnow / l;
+  float x[P::kTiles * 16];
+#pragma unroll
+  for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      x[16 * t + r] = l == 0.0f ? 0.0f : o[t][r] * (BITS == 4 && e_of(t, r) % 2 ? by * 0.0625f : by);
+#pragma unroll
+  for (int k = 1; k < P::kTiles * 16; k <<= 1)
+#pragma unroll
+    for (int i = 0; i < P::kTiles * 16; ++i)
+      if ((i & k) == 0) {
+        const float y = x[i], z = x[i + k];
+        x[i] = y + z;
+        x[i + k] = y - z;
+      }
+#pragma unroll
+  for (int i = 0; i < P::kTiles * 16; ++i) {
+    const float other = __shfl_xor(x[i], 32);
+    x[i] = hi ? other - x[i] : x[i] + other;
+  }
+  const int head = h * a.group + myrow - myquery * a.group;
+  uint16_t* dst = a.o + ((s.first + myquery) * a.q_heads + head) * D;
+  // registers of one unit: its 8 elements are (t, r) with e = 0..7
+#pragma unroll
+  for (int n = 0; n < 2 * P::kTiles; ++n) {            // units of this lane
+    float y[8];
+    int unit = 0;
+#pragma unroll
+    for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int nr = r % 4 + 4 * (r / 4 % (P::kUnits / 8));
+        if (nr == n) {
+          y[e_of(t, r)] = x[16 * t + r];
+          unit = unit_of(r);
+        }
+      }
+    store_row<8>(dst + 8 * unit, a.bf16, y);
+  }
+}
+
+template <int D, int BITS>
+hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
+  KvSplit sp = p.split;
+  sp.o = static_cast<float*>(workspace);
+  sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
+  const auto fn = kv_prompt_kernel<D, BITS>;
+  const size_t lds = Prompt<D, BITS>::kBytes;
+  if (hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fn), lds)) return e;
+  fn<<<dim3((unsigned)(a.c.heads * sp.splits * sp.tiles), 1, a.batch), kThreads, lds, stream>>>(a, sp);
+  if (hipError_t e = hipGetLastError()) return e;
+  return sp.splits > 1 ? launch_kv_join(a, sp, stream) : hipSuccess;
+}
+
+}  // namespace
+
+KvPlan kv_prompt_plan(const KvAttn& a) {
+  KvPlan p{};
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  KvSplit& s = p.split;
+  s.rows = kRows;
+  s.tiles = (int)((rows + kRows - 1) / kRows);
+  s.kept = (int)(rows < kRows ? rows : kRows);
+  s.heads = a.c.heads;
+  const int64_t base = (int64_t)s.tiles * a.c.heads * a.batch;
+  int64_t splits = (512 + base - 1) / base;
+  const int64_t most = (a.max_kv + 511) / 512;
+  if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
+  const int64_t chunk = (a.max_kv + splits - 1) / splits;
+  s.chunk = (int)((chunk + kStep - 1) / kStep * kStep);
+  if (s.chunk < kStep) s.chunk = kStep;
+  s.splits = (int)(((int64_t)a.max_kv + s.chunk - 1) / s.chunk);
+  if (s.splits < 1) s.splits = 1;
+  p.parts = s.splits > 1 ? base * s.splits * s.kept : 0;
+  p.bytes = (size_t)p.parts * (a.c.head_dim + 2) * 4;
+  return p;
+}
+
+hipError_t launch_kv_prompt(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
+  switch (a.c.head_dim * 16 + a.c.bits) {
+    case 64 * 16 + 4: return run<64, 4>(a, p, workspace, stream);
+    case 64 * 16 + 8: return run<64, 8>(a, p, workspace, stream);
+    case 128 * 16 + 4: return run<128, 4>(a, p, workspace, stream);
+    case 128 * 16 + 8: return run<128, 8>(a, p, workspace, stream);
+    case 256 * 16 + 4: return run<256, 4>(a, p, workspace, stream);
+    default: return run<256, 8>(a, p, workspace, stream);
+  }
+}
+
+}  // namespace convrot

@@ -13,6 +13,13 @@ rotated elements reaches an element of the output at most by its norm):
                   a score moves by at most 2^-11 S, and a weight, through
                   itself and the sum, by twice that (2^-20: fp32 scores),
   (n + D) 2^-22   fp32 sums over tokens and elements, in any order, and exp.
+That holds for errors that all add up.  They are independent, so the 2-norm
+over a call's outputs is also held to
+  |do|_2 <= h |o|_2 + (2^-11 + 2^-11 2 S / sqrt(D) + (n + D) 2^-22) |even|_2,
+even = sqrt(sum_j p_j^2 |v_j|^2): independent errors of the weights add in
+squares, and of the rotated query, whose elements are all of one size, a score
+takes S / sqrt(D) 2^-11; every term is a largest error where its standard
+deviation, 1 / sqrt(3) of it, would do.
 """
 
 import numpy as np
@@ -205,26 +212,30 @@ def _check_attention(cache, q, table, q_lens, kv_lens, causal, got, scale=None, 
     scale = d ** -0.5 if scale is None else scale
     h = torch.finfo(got.dtype).eps / 2
     tiny = torch.finfo(got.dtype).smallest_normal * h
-    at, worst = 0, 0.0
+    at, worst, norms = 0, 0.0, np.zeros(2)
     for b, (n, m) in enumerate(zip(q_lens, kv_lens)):
         k, v, here = _host_rows(cache, table[b].cpu().numpy(), m)
         qb = _np(q[at:at + n])
         if here.all():
             o, spread = O.attention(qb, k, v, scale, causal)
         else:   # the positions count all tokens; the absent ones are left out
-            o, spread = np.zeros(qb.shape), np.zeros(qb.shape[:2])
+            o, spread = np.zeros(qb.shape), np.zeros((*qb.shape[:2], 2))
             for i in range(n):
                 see = here & (np.arange(m) <= (m - n + i if causal else m))
                 o[i:i + 1], spread[i:i + 1] = O.attention(qb[i:i + 1], k[see], v[see], scale, False)
         big = scale * np.linalg.norm(qb, axis=-1) * (np.linalg.norm(k, axis=-1).max() if m else 0.0)
         bound = h * np.abs(o) + tiny + ((2.0 ** -11 + 2 * (2.0 ** -11 + 2.0 ** -20) * big + (m + d) * 2.0 ** -22)
-                                        * spread)[..., None]
+                                        * spread[..., 0])[..., None]
         off = np.abs(_np(got[at:at + n]) - o)
+        even = (2.0 ** -11 * (1 + 2 * big / np.sqrt(d)) + (m + d) * 2.0 ** -22) * spread[..., 1]
+        norms += [(off ** 2).sum(), (h * h * o ** 2).sum() + (even ** 2).sum() + o.size * tiny ** 2]
         if off.size:
             worst = max(worst, float((off / bound).max()))
         assert (off <= bound).all(), (b, n, m, float((off / bound).max()))
         at += n
-    _say("   largest share of the bound:", tell, round(worst, 3))
+    share = float(np.sqrt(norms[0] / norms[1])) if norms[1] else float(norms[0] > 0)
+    _say("   largest share of the bound:", tell, round(worst, 3), "in the 2-norm:", round(share, 3))
+    assert share <= 1.0
 
 
 def _sequences(g, cache, kv_lens, spare=0):
@@ -388,6 +399,26 @@ def test_attention_sums_a_long_even_tail():
         x = q.expand(rows, 1, d).contiguous().to(DEV)
         got = cr.kv_attention(cache, x, table, lens, scale=float(np.log(60000.0)), causal=False)
         _check_attention(cache, x, table, [rows], [m], False, got, scale=float(np.log(60000.0)))
+
+
+@pytest.mark.parametrize("rows", [1, 20, 40, 150])
+@pytest.mark.parametrize("step", [8, 16, 32, 64, 128])
+def test_attention_scores_that_keep_rising(rows, step):
+    """Every `step` tokens the scores rise, so that the running maximum does too."""
+    _say("rising scores", rows, step)
+    m, d = 777, 128
+    g = _gen(step)
+    k = torch.zeros((m, 1, d))
+    k[:, 0, 0] = (torch.arange(m) // step).float()
+    cache = cr.KVCache.empty(-(-m // 16), 16, 1, d, 4, DEV)
+    cr.kv_append(cache, k.half().to(DEV), _values(g, (m, 1, d), F16).to(DEV), torch.arange(m, device=DEV))
+    table = torch.arange(cache.pages, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([m], dtype=torch.int32, device=DEV)
+    q = torch.zeros((rows, 1, d), dtype=F16)
+    q[..., 0] = torch.linspace(0.01, 1.0, rows)[:, None]
+    for scale in (0.3, 3.0, 8.0):
+        got = cr.kv_attention(cache, q.to(DEV), table, lens, scale=scale)
+        _check_attention(cache, q, table, [rows], [m], True, got, scale=scale)
 
 
 def test_attention_shows_a_nan_that_is_seen_only():
