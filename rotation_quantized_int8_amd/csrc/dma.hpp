@@ -34,6 +34,18 @@ __device__ __forceinline__ void dma16(const void* gptr, uint32_t lds) {
                :: "v"(gptr), "s"(lds) : "memory", "m0");
 }
 
+// The same from a wave-uniform base plus a 32-bit byte offset per lane.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+
+// 64 lanes x 4 bytes.
+__device__ __forceinline__ void dma4(const void* gptr, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :: "v"(gptr), "s"(lds) : "memory", "m0");
+}
+
 // Eight fp16 additions, each rounded once (fp32 sum, then fp16).
 __device__ __forceinline__ v4i add_f16x8(v4i a, v4i b) {
   const __half* x = reinterpret_cast<const __half*>(&a);

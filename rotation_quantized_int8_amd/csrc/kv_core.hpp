@@ -26,6 +26,12 @@ struct KvPlan {
   size_t bytes;              // workspace
 };
 
+// Workgroups of the single-token kernel that a CU holds, as its registers and
+// LDS are sized.
+__host__ __device__ constexpr int kv_decode_wgs(int D, int bits, int QT) {
+  return D * bits <= 512 ? (QT == 1 ? 4 : 2) : D < 256 || QT == 1 ? 2 : 1;
+}
+
 KvPlan kv_decode_plan(const KvAttn& a);
 hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream);
 KvPlan kv_prompt_plan(const KvAttn& a);

@@ -20,16 +20,19 @@
 //                   its 8 tokens, the D / 16 codes of its own D / 16 elements
 //                   and interleaves pairs of tokens by byte permutes.
 // W = p scale', normalised by a power of two M >= every scale' seen so far,
-// and p carries 2^8, so fp16 keeps weights down to 2^-32 of the largest.  The
-// running maximum is only raised when a score exceeds it by more than 2^7
-// (p <= 2^15), so most steps neither reduce over lanes nor rescale.
+// and p = 2^(score - m + 8), so fp16 keeps weights down to 2^-32 of the
+// largest.  m is raised only when a weight passes 2^15, so most steps neither
+// reduce over lanes nor rescale, and no maximum is needed before the
+// exponential.
 //
 // What bounds it: HBM (each cached row is read once for all rows of its key
 // head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
-// sequence and key head; the wavefronts take 32 tokens in turn, with the next
-// 32 loading while these are used.
+// sequence and key head; the wavefronts take 32 tokens in turn.  Codes and
+// scales come by direct loads into a ring in LDS of the wavefront's own, two
+// steps deep (one for rows of 256 bytes), so loads in flight cost no registers
+// and the loop needs no barrier.
 
-#include "kv.hpp"
+#include "dma.hpp"
 #include "kv_core.hpp"
 
 namespace convrot {
@@ -41,96 +44,94 @@ constexpr int kWaves = 4;
 constexpr int kStep = 32;                     // tokens a wavefront takes at once
 constexpr int kChunkMax = 4096;               // tokens of a workgroup at most (its page numbers are kept in LDS)
 constexpr float kWeightBits = 8.0f;           // p = 2^(score - m + 8)
-constexpr float kRaise = 7.0f;                // m is raised past this excess
-constexpr float kLowest = -1e30f;             // m of a row that has seen no token
+constexpr float kMostWeight = 32768.0f;       // m is raised past this weight
+constexpr float kUnset = 1e30f;               // 8 - m of a row that has seen no token
+constexpr float kLowest = -1e30f;             // its m
 
-// One key's or value's codes of a lane: N 32-bit words (N = 0: 16 bits).
-template <int BYTES>
-__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
-  if constexpr (BYTES == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
-  else if constexpr (BYTES == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
-  else if constexpr (BYTES == 8) {
-    const v2u x = *reinterpret_cast<const v2u*>(p);
-    w[0] = x[0], w[1] = x[1];
-  } else {
-#pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) {
-      const v4u x = reinterpret_cast<const v4u*>(p)[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
-    }
-  }
-}
-
+// The ring of a wavefront in LDS: kStages steps of 32 tokens, each the keys'
+// codes, the values' codes and the scales (keys' then values', 16 each).
 template <int D, int BITS>
-struct Tile {
-  static constexpr int kRow = D * BITS / 8;
-  static constexpr int kKeyBytes = kRow / 4, kValueBytes = kRow / 16;
-  static constexpr int kValueWords = kValueBytes < 4 ? 1 : kValueBytes / 4;
-  uint32_t k[2][kKeyBytes / 4];       // 16 tokens: token lane % 16, elements (lane / 16) D / 4 ..
-  uint32_t v[2][4][kValueWords];      // token 4 (lane / 16) + r, elements (lane % 16) D / 16 ..
-  v4f ks[2], vs[2];                   // of tokens 4 (lane / 16) + r
+struct Ring {
+  static constexpr int kRow = D * BITS / 8;            // bytes of a cached row
+  static constexpr int kHalf = kStep * kRow;           // of a step's keys, and of its values
+  static constexpr int kStage = 2 * kHalf + 4 * 64;
+  static constexpr int kStages = kRow > 128 ? 1 : 2;
+  static constexpr int kBytes = kStages * kStage;
+  static constexpr int kLoads = kHalf / 1024;          // direct loads of a half
+  static constexpr int kKeyWords = kRow / 16;          // 32-bit words of a lane's key codes (16 tokens, 4 lanes each)
+  static constexpr int kValueWords = kRow < 64 ? 1 : kRow / 64;
 };
 
-// S^T operand of 16 tokens: D / 64 times 16 int8 (16 c for 4-bit codes: the
-// even elements of the lane's D / 4, then the odd ones).
+// S^T operand k of 16 tokens, 16 int8 a lane.  w: the lane's codes, the 16
+// bytes (lane / 16) of each 64 of its token's row (8 bytes of 32 where a row
+// has 32).  A 4-bit code enters as 16 c: the even elements of the 32 that 16
+// bytes hold, then the odd ones.
 template <int D, int BITS>
-__device__ __forceinline__ v4i key_operand(const uint32_t* w, int m) {
+__device__ __forceinline__ v4i key_operand(const uint32_t* w, int k) {
   v4i a;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if constexpr (BITS == 8) {
-      a[j] = (int)w[4 * m + j];
+      a[j] = (int)w[4 * k + j];
+    } else if constexpr (D == 64) {
+      a[j] = (int)(j < 2 ? (w[j] << 4) & 0xF0F0F0F0u : w[j - 2] & 0xF0F0F0F0u);
     } else {
-      constexpr int half = D / 32;             // words of the even elements
-      const int i = 4 * m + j;
-      a[j] = (int)(i < half ? (w[i] << 4) & 0xF0F0F0F0u : w[i - half] & 0xF0F0F0F0u);
+      const uint32_t x = w[4 * (k / 2) + j];
+      a[j] = (int)(k % 2 == 0 ? (x << 4) & 0xF0F0F0F0u : x & 0xF0F0F0F0u);
     }
   }
   return a;
 }
 
-// O^T operands: of 8 tokens' words, the D / 16 tiles' four half pairs.  With
-// 4-bit codes the odd tiles hold 16 c.
+// Where element d of a query stands among its D int8, so that lane quad reads
+// the D / 4 from quad * D / 4 on in the order of the key operands.
 template <int D, int BITS>
-__device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Tile<D, BITS>::kValueWords],
-                                               v4u (&f)[D / 16]) {
+__device__ __forceinline__ constexpr int query_place(int d) {
+  const int byte = d * BITS / 8;                       // of a cached row
+  if (BITS == 8) return byte / 16 % 4 * (D / 4) + byte / 64 * 16 + byte % 16;
+  if (D == 64) return byte / 8 * 16 + d % 2 * 8 + byte % 8;
+  return byte / 16 % 4 * (D / 4) + byte / 64 * 32 + d % 2 * 16 + byte % 16;
+}
+
+// O^T operands of output tiles i .. i + 3: of 8 tokens' words, four half pairs
+// a tile.  With 4-bit codes the odd tiles hold 16 c.
+template <int D, int BITS>
+__device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Ring<D, BITS>::kValueWords], int i,
+                                               v4u (&f)[4]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {                // token pairs (0,1), (2,3) of each half
     const uint32_t* a = v[p / 2][2 * (p % 2)];
     const uint32_t* b = v[p / 2][2 * (p % 2) + 1];
     if constexpr (BITS == 4) {
-#pragma unroll
-      for (int i = 0; i < D / 16; i += 4) {
-        const uint32_t x = __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u) ^ 0x88888888u;
-        const uint32_t y = x >> 8;
-        // 1024 + (c + 8) and 1024 + 16 (c + 8)
-        const h2 one = {(_Float16)1032.0f, (_Float16)1032.0f}, sixteen = {(_Float16)1152.0f, (_Float16)1152.0f};
-        f[i][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - one);
-        f[i + 1][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) - sixteen);
-        f[i + 2][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x000F000Fu) | 0x64006400u) - one);
-        f[i + 3][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x00F000F0u) | 0x64006400u) - sixteen);
-      }
+      const uint32_t x = __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u) ^ 0x88888888u;
+      const uint32_t y = x >> 8;
+      // 1024 + (c + 8) and 1024 + 16 (c + 8)
+      const h2 one = {(_Float16)1032.0f, (_Float16)1032.0f}, sixteen = {(_Float16)1152.0f, (_Float16)1152.0f};
+      f[0][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - one);
+      f[1][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) - sixteen);
+      f[2][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x000F000Fu) | 0x64006400u) - one);
+      f[3][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x00F000F0u) | 0x64006400u) - sixteen);
     } else {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t x = __builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)(i % 4) * 0x00010001u);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = __builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)e * 0x00010001u);
         const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};   // 1024 + (c + 128)
-        f[i][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x ^ 0x64806480u)) - off);
+        f[e][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x ^ 0x64806480u)) - off);
       }
     }
   }
 }
 
 template <int D, int BITS, int QT>
-__global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSplit sp) {
-  using T = Tile<D, BITS>;
+__global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_decode_kernel(KvAttn a, KvSplit sp) {
+  using R = Ring<D, BITS>;
   constexpr int E = D / 16;                    // elements of a lane's output tiles, and of a rotation lane
   constexpr int KM = D / 64;                   // matrix steps of a score
   constexpr int ROWS = 16 * QT;
   constexpr int PASS = E < 8 ? E : 8;          // elements of a row segment joined at once
   constexpr int PITCH = 16 * PASS + 4;
   __shared__ __align__(16) union {
+    char ring[kWaves][R::kBytes];
     int8_t q[2][16][D + 16];
     float o[kWaves][16][PITCH];
   } sh;
@@ -138,7 +139,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
   __shared__ float stat[kWaves][16][2];
   __shared__ int pages[kChunkMax / CONVROT_KV_PAGE_MIN + 1];
 
-  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, col = lane % 16, quad = lane / 16;
+  const int tid = threadIdx.x, lane = tid % 64, col = lane % 16, quad = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int h = blockIdx.y, b = blockIdx.z;
   const int split = blockIdx.x % sp.splits, tile = blockIdx.x / sp.splits;
   const int c0 = split * sp.chunk, log2p = a.c.page_log2;
@@ -185,11 +187,9 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
       hi[e] = (int8_t)((n + 128) >> 8);
       lo[e] = (int8_t)(n - (((n + 128) >> 8) << 8));
     }
-    // element order of the key operand: 4-bit codes take the even elements of each D / 4 first
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int d = seg * E + e;
-      const int at = BITS == 8 ? d : d / (D / 4) * (D / 4) + d % 2 * (D / 8) + d % (D / 4) / 2;
+      const int at = query_place<D, BITS>(seg * E + e);
       sh.q[0][r][at] = hi[e];
       sh.q[1][r][at] = lo[e];
     }
@@ -204,9 +204,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
 #pragma unroll
       for (int m = 0; m < KM; ++m)
         q[t][p][m] = *reinterpret_cast<const v4i*>(&sh.q[p][col][quad * (D / 4) + 16 * m]);
-    qf[t] = qscale[16 * t + col];
+    qf[t] = a.scale < 0.0f ? -qscale[16 * t + col] : qscale[16 * t + col];
   }
-  const float flip = a.scale < 0.0f ? -1.0f : 1.0f;
   int end[QT];                                        // tokens this lane's row sees
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -215,50 +214,136 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
   }
 
   v4f o[QT][E];
-  float m[QT], l[QT], vmax = 0x1p-126f;
+  float base[QT], l[QT], vmax = 0x1p-126f, vnorm = 0x1p126f;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    m[t] = kLowest;
+    base[t] = kUnset;
     l[t] = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) o[t][i] = (v4f){0, 0, 0, 0};
   }
 
   auto page_of = [&](int j) { return __builtin_amdgcn_readfirstlane(j < c1 ? pages[(j >> log2p) - page0] : -1); };
-  auto load = [&](T& x, int j0) {
+  // Token 4 r + quad of a group of 16 is the one whose score ends up in register r of the lanes of `quad`, so a value
+  // read of register r covers 4 neighbouring rows.  The keys' codes are laid down in operand order, 16 bytes a lane.
+  const int turned = 4 * (col % 4) + col / 4;          // token of the lane's key codes, and of its scale
+  const uint32_t koff = R::kRow < 64 ? 0 : turned * R::kRow + quad * 16, voff = lane * 16;
+  char* ring = sh.ring[wave];
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(lds_ptr_t)ring;
+  auto group_row = [&](int j) {
+    const int p = page_of(j);
+    return (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
+  };
+  auto load_keys = [&](int j, int stage) {             // and all scales
+    const int64_t r0 = group_row(j), r1 = group_row(j + 16);
+    const uint32_t to = __builtin_amdgcn_readfirstlane(ring0 + stage * R::kStage);
+    if constexpr (R::kRow < 64) {
+      dma16(a.c.kc + (lane < 32 ? r0 : r1) * R::kRow + lane % 32 * 16, to);
+    } else {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int j = j0 + 16 * u, p = page_of(j);
-      const int64_t at = (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
-      load_codes<T::kKeyBytes>(a.c.kc + (at + col) * T::kRow + quad * T::kKeyBytes, x.k[u]);
-      x.ks[u] = *reinterpret_cast<const v4f*>(a.c.ks + at + 4 * quad);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        load_codes<T::kValueBytes>(a.c.vc + (at + 4 * quad + r) * T::kRow + col * T::kValueBytes, x.v[u][r]);
-      x.vs[u] = *reinterpret_cast<const v4f*>(a.c.vs + at + 4 * quad);
+        for (int m = 0; m < R::kLoads / 2; ++m)
+          dma16(a.c.kc + (u ? r1 : r0) * R::kRow + m * 64, koff, to + (u * (R::kLoads / 2) + m) * 1024);
+    }
+    dma4((lane < 32 ? a.c.ks : a.c.vs) + (lane & 16 ? r1 : r0) + turned, to + 2 * R::kHalf);
+  };
+  auto load_values = [&](int j, int stage) {
+    const int64_t r0 = group_row(j), r1 = group_row(j + 16);
+    const uint32_t to = __builtin_amdgcn_readfirstlane(ring0 + stage * R::kStage + R::kHalf);
+    if constexpr (R::kRow < 64) {
+      dma16(a.c.vc + (lane < 32 ? r0 : r1) * R::kRow + lane % 32 * 16, to);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int m = 0; m < R::kLoads / 2; ++m)
+          dma16(a.c.vc + (u ? r1 : r0) * R::kRow + m * 1024, voff, to + (u * (R::kLoads / 2) + m) * 1024);
     }
   };
+  // Direct loads return in order: waiting for a half leaves in flight what was issued after it.
+  constexpr int kNK = R::kLoads + 1, kNV = R::kLoads;
 
-  auto use = [&](T& x, int j0) {
-    const bool whole = j0 + kStep <= first && page_of(j0) >= 0 && page_of(j0 + 16) >= 0;
-    if (!whole) {
+  __syncthreads();                                     // the ring takes the place of the staged queries
+  constexpr int kStride = kStep * kWaves, S = R::kStages;
+  int j0 = c0 + kStep * wave, stage = 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bool here = page_of(j0 + 16 * u) >= 0;
+  for (int n = 0; n < S; ++n)
+    if (j0 + n * kStride < c1) {
+      load_keys(j0 + n * kStride, n);
+      load_values(j0 + n * kStride, n);
+    }
+  for (; j0 < c1; j0 += kStride, stage = S == 1 ? 0 : stage ^ 1) {
+    const bool more = j0 + kStride < c1, refill = j0 + S * kStride < c1;
+    const char* here_k = ring + stage * R::kStage;
+    const char* here_v = here_k + R::kHalf;
+    const char* here_s = here_v + R::kHalf;
+    if (S == 2 && more) wait_vmcnt<2 * kNV + kNK>();
+    else wait_vmcnt<kNV>();
+    compiler_fence();
+    uint32_t kw[2][R::kKeyWords];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool in = here && j0 + 16 * u + 4 * quad + r < c1;
-          x.ks[u][r] = in ? x.ks[u][r] : 0.0f;
-          x.vs[u][r] = in ? x.vs[u][r] : 0.0f;
+    for (int u = 0; u < 2; ++u) {
+      if constexpr (R::kRow < 64) {
+        const v2u x = *reinterpret_cast<const v2u*>(here_k + (16 * u + turned) * R::kRow + quad * 8);
+        kw[u][0] = x[0], kw[u][1] = x[1];
+      } else {
+#pragma unroll
+        for (int m = 0; m < R::kLoads / 2; ++m) {
+          const v4u x = *reinterpret_cast<const v4u*>(here_k + (u * (R::kLoads / 2) + m) * 1024 + lane * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kw[u][4 * m + i] = x[i];
         }
       }
     }
-    // the values' scales, against the power of two that holds them all
+    v4f ks[2], vs[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      ks[u] = *reinterpret_cast<const v4f*>(here_s + 64 * u + 16 * quad);
+      vs[u] = *reinterpret_cast<const v4f*>(here_s + 128 + 64 * u + 16 * quad);
+    }
+    const bool here[2] = {page_of(j0) >= 0, page_of(j0 + 16) >= 0};   // false past c1 too
+    const bool whole = j0 + kStep <= first && here[0] && here[1];
+    // ---- scores; the next keys load as soon as these are used
+    v4i sc[QT][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      v4i lo[QT];
+#pragma unroll
+      for (int t = 0; t < QT; ++t) sc[t][u] = lo[t] = (v4i){0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < KM; ++k) {
+        const v4i c = key_operand<D, BITS>(kw[u], k);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          sc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, q[t][0][k], sc[t][u], 0, 0, 0);
+          lo[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, q[t][1][k], lo[t], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sc[t][u][r] = (sc[t][u][r] << 8) + lo[t][r];
+    }
+    if (refill) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the reads are done
+      load_keys(j0 + S * kStride, stage);
+    }
+
+    // ---- weights
+    auto seen = [&](int t, int u, int r) { return (j0 + 16 * u + 4 * r + quad < end[t]) & here[u]; };
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          vs[u][r] = here[u] & (j0 + 16 * u + 4 * r + quad < c1) ? vs[u][r] : 0.0f;
+    }
     float most = vmax;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) most = fmaxf(most, x.vs[u][r]);
+      for (int r = 0; r < 4; ++r) most = fmaxf(most, vs[u][r]);
     if (__any(most > vmax)) {
       most = fmaxf(most, __shfl_xor(most, 16));
       most = fmaxf(most, __shfl_xor(most, 32));
@@ -271,58 +356,46 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
 #pragma unroll
         for (int i = 0; i < E; ++i) o[t][i] *= by;
       vmax = next;
+      vnorm = 1.0f / next;
     }
-    const float vnorm = 1.0f / vmax;
-    v4f vs[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) vs[u] = x.vs[u] * vnorm;
+    for (int u = 0; u < 2; ++u) vs[u] *= vnorm;
 
     v8h w[QT];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      float sc[2][4], best = kLowest;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        v4i hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < KM; ++k) {
-          const v4i c = key_operand<D, BITS>(x.k[u], k);
-          hi = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, q[t][0][k], hi, 0, 0, 0);
-          lo = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, q[t][1][k], lo, 0, 0, 0);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sc[u][r] = (float)((hi[r] << 8) + lo[r]) * (x.ks[u][r] * (qf[t] * flip));
-        }
-      }
-      if (!whole) {
+      float p[8];
+      auto weigh = [&]() {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = j0 + 16 * u + 4 * quad + r;
-            sc[u][r] = j < end[t] && page_of(j0 + 16 * u) >= 0 ? sc[u][r] : -INFINITY;
-          }
-      }
+          for (int r = 0; r < 4; ++r)
+            p[4 * u + r] = __builtin_amdgcn_exp2f(__fmaf_rn((float)sc[t][u][r], ks[u][r] * qf[t], base[t]));
+        if (!whole) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+          for (int e = 0; e < 8; ++e) p[e] = seen(t, e / 4, e % 4) ? p[e] : 0.0f;
+        }
+      };
+      weigh();
+      float top = p[0];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) best = fmaxf(best, sc[u][r]);
-      if (__any(best > m[t] + kRaise)) {
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, p[e]);
+      if (__any(top > kMostWeight)) {                 // raise the maximum
+        float best = kLowest;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            best = fmaxf(best, whole | seen(t, u, r) ? (float)sc[t][u][r] * (ks[u][r] * qf[t]) : kLowest);
         best = fmaxf(best, __shfl_xor(best, 16));
         best = fmaxf(best, __shfl_xor(best, 32));
-        const float next = fmaxf(m[t], best), by = __builtin_amdgcn_exp2f(m[t] - next);
+        const float next = fminf(base[t], kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base[t]);
         l[t] *= by;
 #pragma unroll
         for (int i = 0; i < E; ++i) o[t][i] *= by;
-        m[t] = next;
+        base[t] = next;
+        weigh();
       }
-      const float base = kWeightBits - m[t];
-      float p[8];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) p[4 * u + r] = __builtin_amdgcn_exp2f(sc[u][r] + base);
       l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       v4u packed;
 #pragma unroll
@@ -337,25 +410,43 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
       }
       w[t] = __builtin_bit_cast(v8h, packed);
     }
-    v4u f[E];
-    value_operands<D, BITS>(x.v, f);
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-        o[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f[i]), w[t], o[t][i], 0, 0, 0);
-  };
 
-  constexpr int kStride = kStep * kWaves;
-  int j = c0 + kStep * wave;
-  T x, y;
-  if (j < c1) load(x, j);
-  for (; j < c1; j += 2 * kStride) {
-    if (j + kStride < c1) load(y, j + kStride);
-    use(x, j);
-    if (j + kStride >= c1) break;
-    if (j + 2 * kStride < c1) load(x, j + 2 * kStride);
-    use(y, j + kStride);
+    // ---- outputs; then the next values load
+    if (refill) wait_vmcnt<(S - 1) * (kNK + kNV) + kNK>();
+    else if (S == 2 && more) wait_vmcnt<kNK + kNV>();
+    else wait_vmcnt<0>();
+    compiler_fence();
+    uint32_t vw[2][4][R::kValueWords];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const char* p = here_v + (16 * u + 4 * r + quad) * R::kRow + col * (R::kRow / 16);
+        if constexpr (R::kRow < 64) vw[u][r][0] = *reinterpret_cast<const uint16_t*>(p);
+        else if constexpr (R::kRow == 64) vw[u][r][0] = *reinterpret_cast<const uint32_t*>(p);
+        else if constexpr (R::kRow == 128) {
+          const v2u x = *reinterpret_cast<const v2u*>(p);
+          vw[u][r][0] = x[0], vw[u][r][1] = x[1];
+        } else {
+          const v4u x = *reinterpret_cast<const v4u*>(p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vw[u][r][i] = x[i];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < E; i += 4) {
+      v4u f[4];
+      value_operands<D, BITS>(vw, i, f);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          o[t][i + n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f[n]), w[t], o[t][i + n], 0, 0, 0);
+    }
+    if (refill) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      load_values(j0 + S * kStride, stage);
+    }
   }
 
   // ---- join the wavefronts, 16 rows at a time
@@ -365,14 +456,14 @@ __global__ __launch_bounds__(64 * kWaves) void kv_decode_kernel(KvAttn a, KvSpli
     l[t] += __shfl_xor(l[t], 32);
     __syncthreads();
     if (quad == 0) {
-      stat[wave][col][0] = m[t];
+      stat[wave][col][0] = base[t] == kUnset ? kLowest : kWeightBits - base[t];
       stat[wave][col][1] = l[t];
     }
     __syncthreads();
     float top = kLowest;
 #pragma unroll
     for (int v = 0; v < kWaves; ++v) top = fmaxf(top, stat[v][col][0]);
-    const float mine = __builtin_amdgcn_exp2f(m[t] - top) * vmax;
+    const float mine = __builtin_amdgcn_exp2f((base[t] == kUnset ? kLowest : kWeightBits - base[t]) - top) * vmax;
     const int r = tid / 16, seg = tid % 16;
     float rtop = kLowest, sum = 0.0f, out[E];
 #pragma unroll
@@ -509,7 +600,8 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   s.kept = (int)(rows < s.rows ? rows : s.rows);
   s.heads = a.c.heads;
   const int64_t base = (int64_t)s.tiles * a.c.heads * a.batch;
-  int64_t splits = (1024 + base - 1) / base;
+  const int64_t slots = 256 * kv_decode_wgs(a.c.head_dim, a.c.bits, s.rows / 16);   // resident on 256 CUs
+  int64_t splits = slots / base;
   const int64_t most = (a.max_kv + 255) / 256, least = ((int64_t)a.max_kv + kChunkMax - 1) / kChunkMax;
   if (splits > most) splits = most;
   if (splits < least) splits = least;

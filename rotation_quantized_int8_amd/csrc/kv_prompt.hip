@@ -119,7 +119,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   __shared__ float vtop[2];
   __shared__ float qtop[kWaves];
 
-  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, col = lane % 32, hi = lane / 32;
+  const int tid = threadIdx.x, lane = tid % 64, col = lane % 32, hi = lane / 32;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int b = blockIdx.z;
   // the key head is the fastest index, so that the workgroups of one head meet in one XCD's L2 where the head
   // count is a multiple of 8; the last tiles, which see the most tokens, start first
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
       }
     };
     auto seen = [&](int kt, int r) {
-      return j0 + 32 * kt + 8 * (r / 4) + 4 * hi + r % 4 < end && !gone[2 * kt + r / 8];
+      return (j0 + 32 * kt + 8 * (r / 4) + 4 * hi + r % 4 < end) & !gone[2 * kt + r / 8];
     };
     auto weigh = [&]() {
 #pragma unroll
@@ -364,7 +365,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
         for (int r = 0; r < 16; r += 4) {
           const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) best = fmaxf(best, whole || seen(kt, r + i) ? p[kt][r + i] * ks[i] : kLowest);
+          for (int i = 0; i < 4; ++i) best = fmaxf(best, whole | seen(kt, r + i) ? p[kt][r + i] * ks[i] : kLowest);
         }
       best = fmaxf(best, __shfl_xor(best, 32));
       const float next = fminf(base, kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base);
