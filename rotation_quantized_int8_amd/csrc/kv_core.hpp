@@ -24,13 +24,16 @@ struct KvPlan {
   KvSplit split;
   int64_t parts;             // partial rows
   size_t bytes;              // workspace
+  int waves;                 // of a workgroup (few rows)
 };
 
-// Workgroups of the single-token kernel that a CU holds, as its registers and
-// LDS are sized.
-__host__ __device__ constexpr int kv_decode_wgs(int D, int bits, int QT) {
-  return D * bits <= 512 ? (QT == 1 ? 4 : 2) : D < 256 || QT == 1 ? 2 : 1;
+// Workgroups of `waves` wavefronts of the single-token kernel that a CU holds,
+// as its registers and LDS are sized, and the wavefronts of a workgroup that
+// walks a short context alone.
+__host__ __device__ constexpr int kv_decode_wgs(int D, int QT, int waves) {
+  return waves > 4 ? 1 : D < 256 ? (QT == 1 ? 4 : 2) : QT == 1 ? 2 : 1;
 }
+__host__ __device__ constexpr int kv_decode_wide(int D) { return D < 256 ? 16 : 8; }
 
 KvPlan kv_decode_plan(const KvAttn& a);
 hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream);

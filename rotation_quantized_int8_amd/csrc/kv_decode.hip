@@ -29,7 +29,7 @@
 // head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
 // sequence and key head; the wavefronts take 32 tokens in turn.  Codes and
 // scales come by direct loads into a ring in LDS of the wavefront's own, two
-// steps deep (one for rows of 256 bytes), so loads in flight cost no registers
+// steps deep or one, so loads in flight cost no registers
 // and the loop needs no barrier.
 
 #include "dma.hpp"
@@ -40,7 +40,6 @@ namespace {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;
 constexpr int kStep = 32;                     // tokens a wavefront takes at once
 constexpr int kChunkMax = 4096;               // tokens of a workgroup at most (its page numbers are kept in LDS)
 constexpr float kWeightBits = 8.0f;           // p = 2^(score - m + 8)
@@ -49,13 +48,15 @@ constexpr float kUnset = 1e30f;               // 8 - m of a row that has seen no
 constexpr float kLowest = -1e30f;             // its m
 
 // The ring of a wavefront in LDS: kStages steps of 32 tokens, each the keys'
-// codes, the values' codes and the scales (keys' then values', 16 each).
+// codes, the values' codes and the scales (keys' then values', 16 each).  One
+// step where two would keep a fourth (a second, for heads of 256) workgroup
+// off the CU.
 template <int D, int BITS>
 struct Ring {
   static constexpr int kRow = D * BITS / 8;            // bytes of a cached row
   static constexpr int kHalf = kStep * kRow;           // of a step's keys, and of its values
   static constexpr int kStage = 2 * kHalf + 4 * 64;
-  static constexpr int kStages = kRow > 128 ? 1 : 2;
+  static constexpr int kStages = kRow > 128 || D * BITS == 1024 && D < 256 ? 1 : 2;
   static constexpr int kBytes = kStages * kStage;
   static constexpr int kLoads = kHalf / 1024;          // direct loads of a half
   static constexpr int kKeyWords = kRow / 16;          // 32-bit words of a lane's key codes (16 tokens, 4 lanes each)
@@ -122,29 +123,39 @@ __device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Ring<D,
   }
 }
 
-template <int D, int BITS, int QT>
-__global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_decode_kernel(KvAttn a, KvSplit sp) {
+template <int D, int BITS, int QT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4 * kv_decode_wgs(D, QT, WAVES))
+void kv_decode_kernel(KvAttn a, KvSplit sp) {
   using R = Ring<D, BITS>;
   constexpr int E = D / 16;                    // elements of a lane's output tiles, and of a rotation lane
   constexpr int KM = D / 64;                   // matrix steps of a score
   constexpr int ROWS = 16 * QT;
-  constexpr int PASS = E < 8 ? E : 8;          // elements of a row segment joined at once
+  constexpr int PASS = WAVES > 4 ? 2 : E < 8 ? E : 8;   // elements of a row segment joined at once
   constexpr int PITCH = 16 * PASS + 4;
+  constexpr int S = R::kStages, kStride = kStep * WAVES;
+  constexpr int kNK = R::kLoads + 1, kNV = R::kLoads;    // direct loads of a step's keys (and scales), and values
+  constexpr int QROWS = 4 * QT;                // query rows that a wavefront prepares (the first four do)
+  constexpr int QBYTES = QROWS * 2 * D < 1024 ? 1024 : QROWS * 2 * D;
   __shared__ __align__(16) union {
-    char ring[kWaves][R::kBytes];
-    int8_t q[2][16][D + 16];
-    float o[kWaves][16][PITCH];
+    char ring[WAVES][R::kBytes];
+    float o[WAVES][16][PITCH];
   } sh;
+  __shared__ __align__(16) char qbuf[4][QBYTES];       // the rows as loaded, then each as its two int8 planes
   __shared__ float qscale[ROWS];
-  __shared__ float stat[kWaves][16][2];
+  __shared__ float stat[WAVES][16][2];
   __shared__ int pages[kChunkMax / CONVROT_KV_PAGE_MIN + 1];
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 16, quad = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int h = blockIdx.y, b = blockIdx.z;
   const int split = blockIdx.x % sp.splits, tile = blockIdx.x / sp.splits;
-  const int c0 = split * sp.chunk, log2p = a.c.page_log2;
+  const int c0 = split * sp.chunk, log2p = a.c.page_log2, page0 = c0 >> log2p;
 
+  // the chunk's page numbers, without waiting for the sequence's length
+  for (int i = tid; i <= sp.chunk >> log2p && page0 + i < a.width; i += 64 * WAVES) {
+    const int p = a.table[(int64_t)b * a.width + page0 + i];
+    pages[i] = p >= 0 && p < a.c.pages ? p : -1;
+  }
   const KvSeq s = kv_sequence(a, b);
   const int rows = s.n * a.group - tile * ROWS;      // valid rows from this tile on
   if (rows <= 0) return;
@@ -153,76 +164,21 @@ __global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_de
   const int first = a.causal ? s.kv - s.n + tile * ROWS / a.group + 1 : s.kv;
   const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
   if (c1 <= c0 && split > 0) return;                 // the join leaves it out by the same rule
+  __syncthreads();
 
-  const int page0 = c0 >> log2p, npages = c1 > c0 ? ((c1 - 1) >> log2p) - page0 + 1 : 0;
-  for (int i = tid; i < npages; i += 64 * kWaves) {
-    const int p = a.table[(int64_t)b * a.width + page0 + i];
-    pages[i] = p >= 0 && p < a.c.pages ? p : -1;
-  }
-
-  // ---- the rotated queries, as two int8 planes
-  v4i q[QT][2][KM];
-  float qf[QT];
+  // ---- direct loads: the query rows, then the first steps
+  if (wave < 4) {
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr_t)qbuf[wave];
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    __syncthreads();
-    const int r = tid / 16, seg = tid % 16;          // 16 rows, E elements a lane
-    const int row = tile * ROWS + 16 * t + r;
-    const int i = row / a.group, head = h * a.group + row - i * a.group;
-    float x[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = 0.0f;
-    if (i < s.n) load_row<E>(a.q.p + (s.first + i) * a.q.token + head * a.q.head + seg * E, a.bf16, x);
-    rotate_row<D>(x, seg);
-    float top = 0.0f;
-    bool fine = true;
-#pragma unroll
-    for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e])), fine = fine && fabsf(x[e]) < INFINITY;
-    top = warp_max16(top);
-    const float to = top > 0.0f ? 32512.0f / top : 0.0f;
-    int8_t hi[E], lo[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int n = (int)rintf(x[e] * to);
-      hi[e] = (int8_t)((n + 128) >> 8);
-      lo[e] = (int8_t)(n - (((n + 128) >> 8) << 8));
+    for (int n = 0; n < QBYTES / 1024; ++n) {
+      const int off = n * 1024 + lane * 16, lr = off / (2 * D);
+      const int row = tile * ROWS + 16 * (lr / 4) + 4 * wave + lr % 4;
+      const int i = row / a.group, head = h * a.group + row - i * a.group;
+      const bool in = lr < QROWS && i < s.n;
+      dma16(a.q.p + (in ? (s.first + i) * a.q.token + head * a.q.head + off % (2 * D) / 2 : 0),
+            __builtin_amdgcn_readfirstlane(to + n * 1024));
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int at = query_place<D, BITS>(seg * E + e);
-      sh.q[0][r][at] = hi[e];
-      sh.q[1][r][at] = lo[e];
-    }
-    // sm_scale, the rotation's 1 / sqrt(D), the fixed point and the codes' 16
-    const float f = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * (top / 32512.0f) *
-                    (BITS == 4 ? 0.0625f : 1.0f);
-    const uint64_t bad = __ballot(!fine);
-    if (seg == 0) qscale[16 * t + r] = (bad >> (lane & 48)) & 0xFFFFu ? __uint_as_float(0x7FC00000u) : fmaxf(f, 1e-37f);
-    __syncthreads();
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int m = 0; m < KM; ++m)
-        q[t][p][m] = *reinterpret_cast<const v4i*>(&sh.q[p][col][quad * (D / 4) + 16 * m]);
-    qf[t] = a.scale < 0.0f ? -qscale[16 * t + col] : qscale[16 * t + col];
   }
-  int end[QT];                                        // tokens this lane's row sees
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int i = (tile * ROWS + 16 * t + col) / a.group;
-    end[t] = i >= s.n ? 0 : a.causal ? s.kv - s.n + i + 1 : s.kv;
-  }
-
-  v4f o[QT][E];
-  float base[QT], l[QT], vmax = 0x1p-126f, vnorm = 0x1p126f;
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    base[t] = kUnset;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[t][i] = (v4f){0, 0, 0, 0};
-  }
-
   auto page_of = [&](int j) { return __builtin_amdgcn_readfirstlane(j < c1 ? pages[(j >> log2p) - page0] : -1); };
   // Token 4 r + quad of a group of 16 is the one whose score ends up in register r of the lanes of `quad`, so a value
   // read of register r covers 4 neighbouring rows.  The keys' codes are laid down in operand order, 16 bytes a lane.
@@ -261,11 +217,6 @@ __global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_de
           dma16(a.c.vc + (u ? r1 : r0) * R::kRow + m * 1024, voff, to + (u * (R::kLoads / 2) + m) * 1024);
     }
   };
-  // Direct loads return in order: waiting for a half leaves in flight what was issued after it.
-  constexpr int kNK = R::kLoads + 1, kNV = R::kLoads;
-
-  __syncthreads();                                     // the ring takes the place of the staged queries
-  constexpr int kStride = kStep * kWaves, S = R::kStages;
   int j0 = c0 + kStep * wave, stage = 0;
 #pragma unroll
   for (int n = 0; n < S; ++n)
@@ -273,6 +224,71 @@ __global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_de
       load_keys(j0 + n * kStride, n);
       load_values(j0 + n * kStride, n);
     }
+
+  // ---- the rotated queries, as two int8 planes, while the first steps arrive
+  if (wave < 4) {
+    if (S == 2 && j0 + kStride < c1) wait_vmcnt<2 * (kNK + kNV)>();
+    else if (j0 < c1) wait_vmcnt<kNK + kNV>();
+    else wait_vmcnt<0>();
+    compiler_fence();
+    const int r = tid / 16, seg = tid % 16;            // 16 rows, E elements a lane
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      char* mine = qbuf[wave] + (4 * t + r % 4) * 2 * D;
+      const int i = (tile * ROWS + 16 * t + r) / a.group;
+      float x[E];
+      load_row<E>(reinterpret_cast<const uint16_t*>(mine) + seg * E, a.bf16, x);
+      if (i >= s.n) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.0f;
+      }
+      rotate_row<D>(x, seg);
+      float top = 0.0f;
+      bool fine = true;
+#pragma unroll
+      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e])), fine = fine & (fabsf(x[e]) < INFINITY);
+      top = warp_max16(top);
+      const float to = top > 0.0f ? 32512.0f / top : 0.0f;
+      wave_lds_sync();                                 // the row's lanes have read it
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int at = query_place<D, BITS>(seg * E + e), n = (int)rintf(x[e] * to), hi = (n + 128) >> 8;
+        mine[at] = (char)hi;
+        mine[D + at] = (char)(n - (hi << 8));
+      }
+      // sm_scale, the rotation's 1 / sqrt(D), the fixed point and the codes' 16
+      const float f = a.scale * kv_rsqrt(D) * 1.44269504088896340736f * (top / 32512.0f) * (BITS == 4 ? 0.0625f : 1.0f);
+      const uint64_t bad = __ballot(!fine);
+      if (seg == 0) qscale[16 * t + r] = (bad >> (lane & 48)) & 0xFFFFu ? __uint_as_float(0x7FC00000u) : f;
+    }
+  }
+  lds_barrier();
+  v4i q[QT][2][KM];
+  float qf[QT];
+  int end[QT];                                        // tokens this lane's row sees
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int m = 0; m < KM; ++m)
+        q[t][p][m] = *reinterpret_cast<const v4i*>(qbuf[col / 4] + (4 * t + col % 4) * 2 * D + p * D + quad * (D / 4) + 16 * m);
+    qf[t] = qscale[16 * t + col];
+    const int i = (tile * ROWS + 16 * t + col) / a.group;
+    end[t] = i >= s.n ? 0 : a.causal ? s.kv - s.n + i + 1 : s.kv;
+  }
+
+  v4f o[QT][E];
+  float base[QT], l[QT], vmax = 0x1p-126f, vnorm = 0x1p126f;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    base[t] = kUnset;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[t][i] = (v4f){0, 0, 0, 0};
+  }
+
+  // Direct loads return in order: waiting for a half leaves in flight what was issued after it.
   for (; j0 < c1; j0 += kStride, stage = S == 1 ? 0 : stage ^ 1) {
     const bool more = j0 + kStride < c1, refill = j0 + S * kStride < c1;
     const char* here_k = ring + stage * R::kStage;
@@ -462,14 +478,14 @@ __global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_de
     __syncthreads();
     float top = kLowest;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) top = fmaxf(top, stat[v][col][0]);
+    for (int v = 0; v < WAVES; ++v) top = fmaxf(top, stat[v][col][0]);
     const float mine = __builtin_amdgcn_exp2f((base[t] == kUnset ? kLowest : kWeightBits - base[t]) - top) * vmax;
-    const int r = tid / 16, seg = tid % 16;
+    const int r = tid / 16 % 16, seg = tid % 16;       // the first four wavefronts finish the rows
     float rtop = kLowest, sum = 0.0f, out[E];
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) rtop = fmaxf(rtop, stat[v][r][0]);
+    for (int v = 0; v < WAVES; ++v) rtop = fmaxf(rtop, stat[v][r][0]);
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) sum += __builtin_amdgcn_exp2f(stat[v][r][0] - rtop) * stat[v][r][1];
+    for (int v = 0; v < WAVES; ++v) sum += __builtin_amdgcn_exp2f(stat[v][r][0] - rtop) * stat[v][r][1];
 #pragma unroll
     for (int p = 0; p < E / PASS; ++p) {
       if (p) __syncthreads();
@@ -480,14 +496,17 @@ __global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_de
           sh.o[wave][col][PASS * (4 * quad + e) + i] =
               o[t][PASS * p + i][e] * (BITS == 4 && i % 2 ? mine * 0.0625f : mine);
       __syncthreads();
+      if (wave < 4) {
 #pragma unroll
-      for (int i = 0; i < PASS; ++i) {
-        float z = 0.0f;
+        for (int i = 0; i < PASS; ++i) {
+          float z = 0.0f;
 #pragma unroll
-        for (int v = 0; v < kWaves; ++v) z += sh.o[v][r][PASS * seg + i];
-        out[PASS * p + i] = z;
+          for (int v = 0; v < WAVES; ++v) z += sh.o[v][r][PASS * seg + i];
+          out[PASS * p + i] = z;
+        }
       }
     }
+    if (wave >= 4) continue;
     const int rr = 16 * t + r;
     if (sp.splits > 1) {
       if (rr < rows) {
@@ -513,12 +532,14 @@ __global__ __launch_bounds__(64 * kWaves, kv_decode_wgs(D, BITS, QT)) void kv_de
   }
 }
 
-// Joins the splits of each row: segments of 16 lanes take the splits in turn,
-// E elements a lane, then one segment rotates the row back.
+// Joins the splits of each row: `segs` segments of 16 lanes take the splits in
+// turn, E elements a lane, 16 splits of a segment at a time (their maxima and
+// sums a lane each, so that the partial rows load without waiting for one
+// another); then one segment rotates the row back.
 template <int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int segs) {
   constexpr int E = D / 16;
-  __shared__ float part[16][D + 4];
+  __shared__ __align__(16) float part[16][D + 4];
   __shared__ float stat[16][2];
   const int sub = threadIdx.x / 16, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
   const KvSeq s = kv_sequence(a, b);
@@ -538,18 +559,36 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int 
   float m = kLowest, l = 0.0f, x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = 0.0f;
-  for (int z = sub % segs; z < n; z += segs) {
-    const int64_t at = sp.row(b, h, tile, z, rr);
-    const float mz = sp.ml[2 * at], lz = sp.ml[2 * at + 1];
-    v4f o[E / 4];
-#pragma unroll
-    for (int e = 0; e < E / 4; ++e) o[e] = *reinterpret_cast<const v4f*>(sp.o + at * D + seg * E + 4 * e);
-    const float next = fmaxf(m, mz), keep = __builtin_amdgcn_exp2f(m - next), add = __builtin_amdgcn_exp2f(mz - next);
+  for (int z0 = sub % segs; z0 < n; z0 += 16 * segs) {
+    const int z = z0 + seg * segs;                     // this lane's split
+    float mz = kLowest, lz = 0.0f;
+    if (z < n) {
+      const int64_t at = sp.row(b, h, tile, z, rr);
+      mz = sp.ml[2 * at];
+      lz = sp.ml[2 * at + 1];
+    }
+    const float next = fmaxf(m, warp_max16(mz)), keep = __builtin_amdgcn_exp2f(m - next);
+    const float w = __builtin_amdgcn_exp2f(mz - next);
     m = next;
-    l = l * keep + lz * add;
+    l = l * keep + lz * w;                             // summed over the lanes below
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = x[e] * keep + o[e / 4][e % 4] * add;
+    for (int e = 0; e < E; ++e) x[e] *= keep;
+    const int count = (n - z0 + segs - 1) / segs;
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+      if (k >= count) break;
+      const float wk = __shfl(w, k, 16);
+      const float* o = sp.o + sp.row(b, h, tile, z0 + k * segs, rr) * D + seg * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const v4f y = *reinterpret_cast<const v4f*>(o + e);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) x[e + g] += y[g] * wk;
+      }
+    }
   }
+#pragma unroll
+  for (int k = 1; k < 16; k <<= 1) l += __shfl_xor(l, k);
   if (seg == 0) {
     stat[sub][0] = m;
     stat[sub][1] = l;
@@ -574,23 +613,29 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int 
   store_row<E>(a.o + ((s.first + i) * a.q_heads + h * a.group + row - i * a.group) * D + seg * E, a.bf16, x);
 }
 
-template <int D, int BITS, int QT>
+template <int D, int BITS, int QT, int WAVES>
 hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
   KvSplit sp = p.split;
   sp.o = static_cast<float*>(workspace);
   sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
-  kv_decode_kernel<D, BITS, QT><<<dim3(sp.splits * sp.tiles, a.c.heads, a.batch), 64 * kWaves, 0, stream>>>(a, sp);
+  kv_decode_kernel<D, BITS, QT, WAVES>
+      <<<dim3(sp.splits * sp.tiles, a.c.heads, a.batch), 64 * WAVES, 0, stream>>>(a, sp);
   if (hipError_t e = hipGetLastError()) return e;
   return sp.splits > 1 ? launch_kv_join(a, sp, stream) : hipSuccess;
 }
 
 template <int D, int BITS>
 hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
-  return p.split.rows == 16 ? run<D, BITS, 1>(a, p, workspace, stream) : run<D, BITS, 2>(a, p, workspace, stream);
+  if (p.waves > 4) return run<D, BITS, 1, kv_decode_wide(D)>(a, p, workspace, stream);
+  return p.split.rows == 16 ? run<D, BITS, 1, 4>(a, p, workspace, stream) : run<D, BITS, 2, 4>(a, p, workspace, stream);
 }
 
 }  // namespace
 
+// One workgroup per sequence, key head and tile of rows where these fill the
+// card.  Where they do not: up to 2048 tokens one workgroup of 16 wavefronts
+// (8 for heads of 256) walks them all, which saves the join's launch; longer
+// ones are split so that the chunks fill the card once, in workgroups of 4.
 KvPlan kv_decode_plan(const KvAttn& a) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_q * a.group;
@@ -599,17 +644,22 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   s.tiles = (int)((rows + s.rows - 1) / s.rows);
   s.kept = (int)(rows < s.rows ? rows : s.rows);
   s.heads = a.c.heads;
+  p.waves = 4;
   const int64_t base = (int64_t)s.tiles * a.c.heads * a.batch;
-  const int64_t slots = 256 * kv_decode_wgs(a.c.head_dim, a.c.bits, s.rows / 16);   // resident on 256 CUs
+  const int64_t slots = 256 * kv_decode_wgs(a.c.head_dim, s.rows / 16, 4);   // resident on 256 CUs
   int64_t splits = slots / base;
-  const int64_t most = (a.max_kv + 255) / 256, least = ((int64_t)a.max_kv + kChunkMax - 1) / kChunkMax;
+  if (s.rows == 16 && splits > 1 && a.max_kv > 128 && a.max_kv <= 2048) {
+    p.waves = kv_decode_wide(a.c.head_dim);
+    splits = 1;
+  }
+  const int64_t most = ((int64_t)a.max_kv + 255) / 256, least = ((int64_t)a.max_kv + kChunkMax - 1) / kChunkMax;
   if (splits > most) splits = most;
   if (splits < least) splits = least;
   if (splits < 1) splits = 1;
   const int64_t chunk = (a.max_kv + splits - 1) / splits;
   s.chunk = (int)((chunk + 127) / 128 * 128);
   if (s.chunk < 128) s.chunk = 128;
-  s.splits = (int)((a.max_kv + s.chunk - 1) / s.chunk);
+  s.splits = (int)(((int64_t)a.max_kv + s.chunk - 1) / s.chunk);
   if (s.splits < 1) s.splits = 1;
   p.parts = s.splits > 1 ? base * s.splits * s.kept : 0;
   p.bytes = (size_t)p.parts * (a.c.head_dim + 2) * 4;

@@ -102,23 +102,22 @@ class KVCache:
                    torch.zeros(shape, dtype=torch.float32, device=device))
 
 
-class _on:
-    """Makes the tensor's GPU current for the call (nothing to do when it is)."""
+# The current stream's handle by device number; torch.cuda.current_stream(dev)
+# builds a Python object around it (2.8 us of a call's 9, against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("dev", "was")
 
-    def __init__(self, device: torch.device):
-        self.dev = device.index
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.dev:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.was != self.dev:
-            torch.cuda.set_device(self.was)
+def _call(fn, name: str, device: torch.device, *args) -> None:
+    """fn(*args, stream) with the device current, on its current stream."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(status, name)
 
 
 def _rows(t: torch.Tensor, cache: KVCache, heads: Optional[int], name: str) -> Tuple[torch.Tensor, int, int]:
@@ -158,9 +157,8 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         raise ValueError("k and v must have one shape and dtype")
     if slots.shape != k.shape[:1]:
         raise ValueError(f"slots must be [{k.shape[0]}], got {list(slots.shape)}")
-    with _on(cache.device) as stream:
-        _check(_lib().convrot_kv_append(cache._ref, k.data_ptr(), k_token, k_head, v.data_ptr(), v_token, v_head,
-                                        _DTYPES[k.dtype], slots.data_ptr(), k.shape[0], stream), "convrot_kv_append")
+    _call(_lib().convrot_kv_append, "convrot_kv_append", cache.device, cache._ref, k.data_ptr(), k_token, k_head,
+          v.data_ptr(), v_token, v_head, _DTYPES[k.dtype], slots.data_ptr(), k.shape[0])
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float16,
@@ -175,16 +173,14 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
         raise ValueError("slots must be one-dimensional")
     shape = (slots.shape[0], cache.heads, cache.head_dim)
     if out is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        k, v = torch.empty((2, *shape), dtype=dtype, device=cache.device).unbind(0)
     else:
         k, v = out
         for t in (k, v):
             if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != cache.device:
                 raise ValueError(f"out must be two contiguous {dtype} tensors {list(shape)} on {cache.device}")
-    with _on(cache.device) as stream:
-        _check(_lib().convrot_kv_read(cache._ref, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                                      _DTYPES[dtype], stream), "convrot_kv_read")
+    _call(_lib().convrot_kv_read, "convrot_kv_read", cache.device, cache._ref, slots.data_ptr(), shape[0],
+          k.data_ptr(), v.data_ptr(), _DTYPES[dtype])
     return k, v
 
 
@@ -230,7 +226,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, kv_lens: 
     if max_kv is None:
         max_kv = width * cache.page_size
     if out is None:
-        out = torch.empty((tokens, q_heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
     elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != q.device:
         raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
     need = kv_workspace_bytes(cache, tokens, q_heads, batch, max_q, max_kv)
@@ -238,11 +234,9 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, kv_lens: 
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != q.device:
         raise TypeError("workspace must be a contiguous uint8 tensor on q's device")
-    with _on(cache.device) as stream:
-        _check(_lib().convrot_kv_attention(
-            cache._ref, q.data_ptr(), q_token, q_head, _DTYPES[q.dtype], tokens, q_heads, table.data_ptr(), width,
-            batch, kv_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), max_q, max_kv,
-            1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-            stream), "convrot_kv_attention")
+    _call(_lib().convrot_kv_attention, "convrot_kv_attention", cache.device, cache._ref, q.data_ptr(), q_token,
+          q_head, _DTYPES[q.dtype], tokens, q_heads, table.data_ptr(), width, batch, kv_lens.data_ptr(),
+          None if q_start is None else q_start.data_ptr(), max_q, max_kv,
+          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return out
