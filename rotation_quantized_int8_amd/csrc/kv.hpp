@@ -38,11 +38,21 @@ struct KvAttn {
   int64_t T;
   int64_t width;
   int batch, q_heads, group;
+  uint32_t group_mul;     // row / group = row * group_mul >> group_shift, for row < 2^31
+  int group_shift;
   int each_q;
   int max_q, max_kv;
   float scale;            // sm_scale
   int causal, bf16;
 };
+
+// The query that a row (query, head in group) belongs to.  With l = ceil(log2
+// group), group_shift = 31 + l and group_mul = floor(2^group_shift / group) + 1
+// (below 2^32), the product overshoots 2^group_shift row / group by at most
+// row < 2^31 <= 2^group_shift / group, so the quotient is exact.
+__device__ __forceinline__ int kv_query_of(const KvAttn& a, int row) {
+  return (int)((uint64_t)(uint32_t)row * a.group_mul >> a.group_shift);
+}
 
 hipError_t launch_kv_append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16, const int64_t* slots,
                             int64_t T, hipStream_t stream);

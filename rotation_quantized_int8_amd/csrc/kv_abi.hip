@@ -82,6 +82,9 @@ KvAttn attention_args(const convrot_kv_cache* c, int64_t T, int64_t q_heads, int
   a.batch = (int)batch;
   a.q_heads = (int)q_heads;
   a.group = (int)(q_heads / c->heads);
+  a.group_shift = 31;
+  while ((1 << (a.group_shift - 31)) < a.group) ++a.group_shift;
+  a.group_mul = (uint32_t)((1ull << a.group_shift) / (uint64_t)a.group + 1);
   a.max_q = (int)(max_q < T ? max_q : T);
   a.max_kv = (int)max_kv;
   return a;

@@ -42,6 +42,39 @@ hipError_t launch_kv_prompt(const KvAttn& a, const KvPlan& p, void* workspace, h
 // The finished rows from the splits' partial ones.
 hipError_t launch_kv_join(const KvAttn& a, const KvSplit& sp, hipStream_t stream);
 
+// Maximum, and sum, with the lane whose number differs in bit 4 (and in bit 5):
+// the two results of a lane swap of v with itself are the pair's two values.
+__device__ __forceinline__ float pair32(float v, float& other) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  other = __uint_as_float(r[1]);
+  return __uint_as_float(r[0]);
+}
+__device__ __forceinline__ float pair16(float v, float& other) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  other = __uint_as_float(r[1]);
+  return __uint_as_float(r[0]);
+}
+__device__ __forceinline__ float max32(float v) {
+  float w;
+  v = pair32(v, w);
+  return fmaxf(v, w);
+}
+__device__ __forceinline__ float max16_32(float v) {
+  float w;
+  v = pair16(v, w);
+  return max32(fmaxf(v, w));
+}
+__device__ __forceinline__ float sum32(float v) {
+  float w;
+  v = pair32(v, w);
+  return v + w;
+}
+__device__ __forceinline__ float sum16_32(float v) {
+  float w;
+  v = pair16(v, w);
+  return sum32(v + w);
+}
+
 // The value of the lane whose number in its 16-lane row differs in bit BIT.
 template <int BIT>
 __device__ __forceinline__ float row_swap(float v) {

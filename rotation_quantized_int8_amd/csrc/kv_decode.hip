@@ -130,7 +130,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   constexpr int E = D / 16;                    // elements of a lane's output tiles, and of a rotation lane
   constexpr int KM = D / 64;                   // matrix steps of a score
   constexpr int ROWS = 16 * QT;
-  constexpr int PASS = WAVES > 4 ? 2 : E < 8 ? E : 8;   // elements of a row segment joined at once
+  constexpr int PASS = E < 8 ? E : 8;   // elements of a row segment joined at once
   constexpr int PITCH = 16 * PASS + 4;
   constexpr int S = R::kStages, kStride = kStep * WAVES;
   constexpr int kNK = R::kLoads + 1, kNV = R::kLoads;    // direct loads of a step's keys (and scales), and values
@@ -160,8 +160,8 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   const int rows = s.n * a.group - tile * ROWS;      // valid rows from this tile on
   if (rows <= 0) return;
   // the tokens that the tile's last and first row see
-  const int last = a.causal ? s.kv - s.n + (tile * ROWS + (rows < ROWS ? rows : ROWS) - 1) / a.group + 1 : s.kv;
-  const int first = a.causal ? s.kv - s.n + tile * ROWS / a.group + 1 : s.kv;
+  const int last = a.causal ? s.kv - s.n + kv_query_of(a, tile * ROWS + (rows < ROWS ? rows : ROWS) - 1) + 1 : s.kv;
+  const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * ROWS) + 1 : s.kv;
   const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
   if (c1 <= c0 && split > 0) return;                 // the join leaves it out by the same rule
   __syncthreads();
@@ -173,7 +173,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     for (int n = 0; n < QBYTES / 1024; ++n) {
       const int off = n * 1024 + lane * 16, lr = off / (2 * D);
       const int row = tile * ROWS + 16 * (lr / 4) + 4 * wave + lr % 4;
-      const int i = row / a.group, head = h * a.group + row - i * a.group;
+      const int i = kv_query_of(a, row), head = h * a.group + row - i * a.group;
       const bool in = lr < QROWS && i < s.n;
       dma16(a.q.p + (in ? (s.first + i) * a.q.token + head * a.q.head + off % (2 * D) / 2 : 0),
             __builtin_amdgcn_readfirstlane(to + n * 1024));
@@ -235,7 +235,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       char* mine = qbuf[wave] + (4 * t + r % 4) * 2 * D;
-      const int i = (tile * ROWS + 16 * t + r) / a.group;
+      const int i = kv_query_of(a, tile * ROWS + 16 * t + r);
       float x[E];
       load_row<E>(reinterpret_cast<const uint16_t*>(mine) + seg * E, a.bf16, x);
       if (i >= s.n) {
@@ -250,11 +250,31 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
       top = warp_max16(top);
       const float to = top > 0.0f ? 32512.0f / top : 0.0f;
       wave_lds_sync();                                 // the row's lanes have read it
+      // n = 256 hi + lo with lo in [-128, 127]: lo is the low byte of n, hi the second of n + 128
+      uint32_t n[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int at = query_place<D, BITS>(seg * E + e), n = (int)rintf(x[e] * to), hi = (n + 128) >> 8;
-        mine[at] = (char)hi;
-        mine[D + at] = (char)(n - (hi << 8));
+      for (int e = 0; e < E; ++e) n[e] = (uint32_t)(int)rintf(x[e] * to);
+      auto bytes = [](uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3, uint32_t sel) {   // one byte of each
+        return __builtin_amdgcn_perm(b1, b0, sel) | __builtin_amdgcn_perm(b3, b2, sel) << 16;
+      };
+#pragma unroll
+      for (int e = 0; e < E; e += BITS == 4 ? 8 : 4) {   // neighbours in the operand: every second element of 8, or 4
+#pragma unroll
+        for (int par = 0; par < (BITS == 4 ? 2 : 1); ++par) {
+          constexpr int step = BITS == 4 ? 2 : 1;
+          // a lane of 4 elements (D = 64) holds half of such an 8
+          if constexpr (BITS == 4 && E == 4) {
+            const int at = query_place<D, BITS>(seg * E + par);
+            *reinterpret_cast<uint16_t*>(mine + at) = (uint16_t)__builtin_amdgcn_perm(n[par + 2] + 128, n[par] + 128, 0x0C0C0501u);
+            *reinterpret_cast<uint16_t*>(mine + D + at) = (uint16_t)__builtin_amdgcn_perm(n[par + 2], n[par], 0x0C0C0400u);
+          } else {
+            const int at = query_place<D, BITS>(seg * E + e + par);
+            const uint32_t* m = n + e + par;
+            *reinterpret_cast<uint32_t*>(mine + at) =
+                bytes(m[0] + 128, m[step] + 128, m[2 * step] + 128, m[3 * step] + 128, 0x0C0C0501u);
+            *reinterpret_cast<uint32_t*>(mine + D + at) = bytes(m[0], m[step], m[2 * step], m[3 * step], 0x0C0C0400u);
+          }
+        }
       }
       // sm_scale, the rotation's 1 / sqrt(D), the fixed point and the codes' 16
       const float f = a.scale * kv_rsqrt(D) * 1.44269504088896340736f * (top / 32512.0f) * (BITS == 4 ? 0.0625f : 1.0f);
@@ -274,7 +294,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
       for (int m = 0; m < KM; ++m)
         q[t][p][m] = *reinterpret_cast<const v4i*>(qbuf[col / 4] + (4 * t + col % 4) * 2 * D + p * D + quad * (D / 4) + 16 * m);
     qf[t] = qscale[16 * t + col];
-    const int i = (tile * ROWS + 16 * t + col) / a.group;
+    const int i = kv_query_of(a, tile * ROWS + 16 * t + col);
     end[t] = i >= s.n ? 0 : a.causal ? s.kv - s.n + i + 1 : s.kv;
   }
 
@@ -361,8 +381,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) most = fmaxf(most, vs[u][r]);
     if (__any(most > vmax)) {
-      most = fmaxf(most, __shfl_xor(most, 16));
-      most = fmaxf(most, __shfl_xor(most, 32));
+      most = max16_32(most);
       // twice the power of two above the largest: room for it to double
       const uint32_t e = (__float_as_uint(most) >> 23) + 2u;
       const float next = __uint_as_float(__builtin_amdgcn_readfirstlane((e < 254u ? e : 254u) << 23));
@@ -403,8 +422,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             best = fmaxf(best, whole | seen(t, u, r) ? (float)sc[t][u][r] * (ks[u][r] * qf[t]) : kLowest);
-        best = fmaxf(best, __shfl_xor(best, 16));
-        best = fmaxf(best, __shfl_xor(best, 32));
+        best = max16_32(best);
         const float next = fminf(base[t], kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base[t]);
         l[t] *= by;
 #pragma unroll
@@ -468,8 +486,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   // ---- join the wavefronts, 16 rows at a time
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    l[t] += __shfl_xor(l[t], 16);
-    l[t] += __shfl_xor(l[t], 32);
+    l[t] = sum16_32(l[t]);
     __syncthreads();
     if (quad == 0) {
       stat[wave][col][0] = base[t] == kUnset ? kLowest : kWeightBits - base[t];
@@ -496,15 +513,27 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
           sh.o[wave][col][PASS * (4 * quad + e) + i] =
               o[t][PASS * p + i][e] * (BITS == 4 && i % 2 ? mine * 0.0625f : mine);
       __syncthreads();
-      if (wave < 4) {
+      // four wavefronts sum four; with more, each group of four its own, and then the first four the groups
+      const int g = wave / 4;
+      v4f z[PASS / 4];
 #pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-          float z = 0.0f;
+      for (int i = 0; i < PASS / 4; ++i) {
+        z[i] = (v4f){0, 0, 0, 0};
 #pragma unroll
-          for (int v = 0; v < WAVES; ++v) z += sh.o[v][r][PASS * seg + i];
-          out[PASS * p + i] = z;
-        }
+        for (int v = 0; v < 4; ++v) z[i] += *reinterpret_cast<const v4f*>(&sh.o[4 * g + v][r][PASS * seg + 4 * i]);
       }
+      if constexpr (WAVES > 4) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PASS / 4; ++i) *reinterpret_cast<v4f*>(&sh.o[g][r][PASS * seg + 4 * i]) = z[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PASS / 4; ++i)
+#pragma unroll
+          for (int v = 1; v < WAVES / 4; ++v) z[i] += *reinterpret_cast<const v4f*>(&sh.o[v][r][PASS * seg + 4 * i]);
+      }
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) out[PASS * p + i] = z[i / 4][i % 4];
     }
     if (wave >= 4) continue;
     const int rr = 16 * t + r;
@@ -525,7 +554,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
       for (int i = 0; i < E; ++i) out[i] = sum == 0.0f ? 0.0f : out[i] * by;
       rotate_row<D>(out, seg);
       if (rr < rows) {
-        const int row = tile * ROWS + rr, i = row / a.group, head = h * a.group + row - i * a.group;
+        const int row = tile * ROWS + rr, i = kv_query_of(a, row), head = h * a.group + row - i * a.group;
         store_row<E>(a.o + ((s.first + i) * a.q_heads + head) * D + seg * E, a.bf16, out);
       }
     }
@@ -544,7 +573,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int 
   const int sub = threadIdx.x / 16, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
   const KvSeq s = kv_sequence(a, b);
   const int row = blockIdx.x * (16 / segs) + sub / segs;     // of the sequence's rows with this key head
-  const int i = row / a.group;
+  const int i = kv_query_of(a, row);
   const bool valid = i < s.n;
   const int tile = row / sp.rows, rr = row - tile * sp.rows;
   // the splits that the row's tile ran: up to the last token its last row sees
@@ -552,7 +581,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int 
   if (a.causal) {
     int r1 = (tile + 1) * sp.rows - 1;
     r1 = r1 < s.n * a.group ? r1 : s.n * a.group - 1;
-    last = s.kv - s.n + r1 / a.group + 1;
+    last = s.kv - s.n + kv_query_of(a, r1) + 1;
   }
   int n = (last + sp.chunk - 1) / sp.chunk;
   n = valid ? (n < 1 ? 1 : n < sp.splits ? n : sp.splits) : 0;

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   const int rows = s.n * a.group - tile * kRows;
   if (rows <= 0) return;
   const int c0 = split * sp.chunk;
-  const int last = a.causal ? s.kv - s.n + (tile * kRows + (rows < kRows ? rows : kRows) - 1) / a.group + 1 : s.kv;
+  const int last = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + (rows < kRows ? rows : kRows) - 1) + 1 : s.kv;
   const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
   if (c1 <= c0 && split > 0) return;
 
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
     float top = 0.0f;
 #pragma unroll
     for (int t = 0; t < kPass; ++t) {
-      const int row = tile * kRows + 16 * t + r, i = row / a.group, head = h * a.group + row - i * a.group;
+      const int row = tile * kRows + 16 * t + r, i = kv_query_of(a, row), head = h * a.group + row - i * a.group;
 #pragma unroll
       for (int e = 0; e < E; ++e) x[t][e] = 0.0f;
       if (i < s.n) load_row<E>(a.q.p + (s.first + i) * a.q.token + head * a.q.head + seg * E, a.bf16, x[t]);
@@ -299,9 +299,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   };
 
   // ---- the steps
-  const int myrow = tile * kRows + 32 * wave + col, myquery = myrow / a.group;
+  const int myrow = tile * kRows + 32 * wave + col, myquery = kv_query_of(a, myrow);
   const int end = myquery >= s.n ? 0 : a.causal ? s.kv - s.n + myquery + 1 : s.kv;
-  const int first = a.causal ? s.kv - s.n + (tile * kRows + 32 * wave) / a.group + 1 : s.kv;   // the wavefront's first row
+  const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + 32 * wave) + 1 : s.kv;   // the wavefront's first row
   v16f o[P::kTiles];
   float base = kUnset, l = 0.0f, vnow = 0x1p-126f;
 #pragma unroll
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
 #pragma unroll
           for (int i = 0; i < 4; ++i) best = fmaxf(best, whole | seen(kt, r + i) ? p[kt][r + i] * ks[i] : kLowest);
         }
-      best = fmaxf(best, __shfl_xor(best, 32));
+      best = max32(best);
       const float next = fminf(base, kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base);
       l *= by;
 #pragma unroll
@@ -419,7 +419,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
 
   // ---- a lane holds half a row: rotate it back (every bit of (tile, register) and the half-wave is a bit of the
   // element's number), or leave it to the join
-  l += __shfl_xor(l, 32);
+  l = sum32(l);
   if (myquery >= s.n || 32 * wave + col >= rows) return;
   // element of (tile t, register r): row = 8 (r / 4) + 4 hi + r % 4, unit = row % kUnits, e = t * kSpread + row / kUnits
   auto unit_of = [&](int r) { return (8 * (r / 4) + 4 * hi + r % 4) % P::kUnits; };
@@ -456,8 +456,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
       }
 #pragma unroll
   for (int i = 0; i < P::kTiles * 16; ++i) {
-    const float other = __shfl_xor(x[i], 32);
-    x[i] = hi ? other - x[i] : x[i] + other;
+    float second;
+    const float one = pair32(x[i], second);
+    x[i] = hi ? one - second : one + second;
   }
   const int head = h * a.group + myrow - myquery * a.group;
   uint16_t* dst = a.o + ((s.first + myquery) * a.q_heads + head) * D;
