@@ -36,6 +36,9 @@ __device__ __forceinline__ void dma16(const void* gptr, uint32_t lds) {
 
 // The same from a wave-uniform base plus a 32-bit byte offset per lane.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  const uint64_t b = (uint64_t)base;   // into scalar registers, where the compiler keeps it in vector ones
+  base = (const void*)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b));
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }

@@ -19,11 +19,13 @@
 //                   weights never leave their lane; a lane loads, for each of
 //                   its 8 tokens, the D / 16 codes of its own D / 16 elements
 //                   and interleaves pairs of tokens by byte permutes.
-// W = p scale', normalised by a power of two M >= every scale' seen so far,
-// and p = 2^(score - m + 8), so fp16 keeps weights down to 2^-32 of the
-// largest.  m is raised only when a weight passes 2^15, so most steps neither
-// reduce over lanes nor rescale, and no maximum is needed before the
-// exponential.
+// W = p scale' with p = 2^(score - m + 8) and m the running maximum of
+// score + log2 scale', so fp16 keeps weights down to 2^-32 of the largest.
+// m is raised only when a weight passes 2^15, so most steps neither reduce
+// over lanes nor rescale, and no maximum is needed before the exponential.
+// The values' codes enter with an offset of 8 (see value_operands), which
+// costs the outputs 2^-24 of 8 sum W against a mean that is smaller than it
+// by sqrt(tokens) at worst: below fp16's own rounding up to 10^6 even tokens.
 //
 // What bounds it: HBM (each cached row is read once for all rows of its key
 // head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
@@ -44,6 +46,8 @@ constexpr int kStep = 32;                     // tokens a wavefront takes at onc
 constexpr int kChunkMax = 4096;               // tokens of a workgroup at most (its page numbers are kept in LDS)
 constexpr float kWeightBits = 8.0f;           // p = 2^(score - m + 8)
 constexpr float kMostWeight = 32768.0f;       // m is raised past this weight
+constexpr float kLeastScale = 0x1p-80f;       // a value's scale in the maximum, at least
+constexpr float kMostSum = 0x1p92f;           // and past this sum of a step: only values of almost 0 get there
 constexpr float kUnset = 1e30f;               // 8 - m of a row that has seen no token
 constexpr float kLowest = -1e30f;             // its m
 
@@ -95,7 +99,10 @@ __device__ __forceinline__ constexpr int query_place(int d) {
 }
 
 // O^T operands of output tiles i .. i + 3: of 8 tokens' words, four half pairs
-// a tile.  With 4-bit codes the odd tiles hold 16 c.
+// a tile.  A code enters as the fp16 number whose bits are c + 8 (c + 128 for
+// 8 bits), the subnormal (c + 8) 2^-24, and the sum of the weights times the
+// offset is taken off at the end: a mask and an exclusive or make the
+// operand.  With 4-bit codes the odd tiles hold 16 (c + 8).
 template <int D, int BITS>
 __device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Ring<D, BITS>::kValueWords], int i,
                                                v4u (&f)[4]) {
@@ -104,21 +111,15 @@ __device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Ring<D,
     const uint32_t* a = v[p / 2][2 * (p % 2)];
     const uint32_t* b = v[p / 2][2 * (p % 2) + 1];
     if constexpr (BITS == 4) {
-      const uint32_t x = __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u) ^ 0x88888888u;
-      const uint32_t y = x >> 8;
-      // 1024 + (c + 8) and 1024 + 16 (c + 8)
-      const h2 one = {(_Float16)1032.0f, (_Float16)1032.0f}, sixteen = {(_Float16)1152.0f, (_Float16)1152.0f};
-      f[0][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - one);
-      f[1][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) - sixteen);
-      f[2][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x000F000Fu) | 0x64006400u) - one);
-      f[3][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (y & 0x00F000F0u) | 0x64006400u) - sixteen);
+      const uint32_t x = __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u), y = x >> 8;
+      f[0][p] = (x & 0x000F000Fu) ^ 0x00080008u;
+      f[1][p] = (x & 0x00F000F0u) ^ 0x00800080u;
+      f[2][p] = (y & 0x000F000Fu) ^ 0x00080008u;
+      f[3][p] = (y & 0x00F000F0u) ^ 0x00800080u;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t x = __builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)e * 0x00010001u);
-        const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};   // 1024 + (c + 128)
-        f[e][p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (x ^ 0x64806480u)) - off);
-      }
+      for (int e = 0; e < 4; ++e)
+        f[e][p] = __builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)e * 0x00010001u) ^ 0x00800080u;
     }
   }
 }
@@ -190,8 +191,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     const int p = page_of(j);
     return (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
   };
-  auto load_keys = [&](int j, int stage) {             // and all scales
-    const int64_t r0 = group_row(j), r1 = group_row(j + 16);
+  auto load_keys = [&](int64_t r0, int64_t r1, int stage) {   // of the groups with these first rows, and all scales
     const uint32_t to = __builtin_amdgcn_readfirstlane(ring0 + stage * R::kStage);
     if constexpr (R::kRow < 64) {
       dma16(a.c.kc + (lane < 32 ? r0 : r1) * R::kRow + lane % 32 * 16, to);
@@ -204,8 +204,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     }
     dma4((lane < 32 ? a.c.ks : a.c.vs) + (lane & 16 ? r1 : r0) + turned, to + 2 * R::kHalf);
   };
-  auto load_values = [&](int j, int stage) {
-    const int64_t r0 = group_row(j), r1 = group_row(j + 16);
+  auto load_values = [&](int64_t r0, int64_t r1, int stage) {
     const uint32_t to = __builtin_amdgcn_readfirstlane(ring0 + stage * R::kStage + R::kHalf);
     if constexpr (R::kRow < 64) {
       dma16(a.c.vc + (lane < 32 ? r0 : r1) * R::kRow + lane % 32 * 16, to);
@@ -221,8 +220,9 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
   for (int n = 0; n < S; ++n)
     if (j0 + n * kStride < c1) {
-      load_keys(j0 + n * kStride, n);
-      load_values(j0 + n * kStride, n);
+      const int64_t r0 = group_row(j0 + n * kStride), r1 = group_row(j0 + n * kStride + 16);
+      load_keys(r0, r1, n);
+      load_values(r0, r1, n);
     }
 
   // ---- the rotated queries, as two int8 planes, while the first steps arrive
@@ -299,11 +299,13 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   }
 
   v4f o[QT][E];
-  float base[QT], l[QT], vmax = 0x1p-126f, vnorm = 0x1p126f;
+  v4f weight[QT];                                      // sum of the rounded weights (four times the same)
+  float base[QT], l[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     base[t] = kUnset;
     l[t] = 0.0f;
+    weight[t] = (v4f){0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < E; ++i) o[t][i] = (v4f){0, 0, 0, 0};
   }
@@ -311,6 +313,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   // Direct loads return in order: waiting for a half leaves in flight what was issued after it.
   for (; j0 < c1; j0 += kStride, stage = S == 1 ? 0 : stage ^ 1) {
     const bool more = j0 + kStride < c1, refill = j0 + S * kStride < c1;
+    int64_t next0 = 0, next1 = 0;
     const char* here_k = ring + stage * R::kStage;
     const char* here_v = here_k + R::kHalf;
     const char* here_s = here_v + R::kHalf;
@@ -362,8 +365,10 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
         for (int r = 0; r < 4; ++r) sc[t][u][r] = (sc[t][u][r] << 8) + lo[t][r];
     }
     if (refill) {
+      next0 = group_row(j0 + S * kStride);
+      next1 = group_row(j0 + S * kStride + 16);
       __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the reads are done
-      load_keys(j0 + S * kStride, stage);
+      load_keys(next0, next1, stage);
     }
 
     // ---- weights
@@ -373,75 +378,55 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          vs[u][r] = here[u] & (j0 + 16 * u + 4 * r + quad < c1) ? vs[u][r] : 0.0f;
+          vs[u][r] = (here[u] & (j0 + 16 * u + 4 * r + quad < c1)) ? vs[u][r] : 0.0f;
     }
-    float most = vmax;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) most = fmaxf(most, vs[u][r]);
-    if (__any(most > vmax)) {
-      most = max16_32(most);
-      // twice the power of two above the largest: room for it to double
-      const uint32_t e = (__float_as_uint(most) >> 23) + 2u;
-      const float next = __uint_as_float(__builtin_amdgcn_readfirstlane((e < 254u ? e : 254u) << 23));
-      const float by = vmax / next;
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[t][i] *= by;
-      vmax = next;
-      vnorm = 1.0f / next;
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) vs[u] *= vnorm;
-
     v8h w[QT];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      float p[8];
+      float p[8], x[8], sum;
       auto weigh = [&]() {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            p[4 * u + r] = __builtin_amdgcn_exp2f(__fmaf_rn((float)sc[t][u][r], ks[u][r] * qf[t], base[t]));
+        for (int e = 0; e < 8; ++e) {
+          const int u = e / 4, r = e % 4;
+          p[e] = __builtin_amdgcn_exp2f(__fmaf_rn((float)sc[t][u][r], ks[u][r] * qf[t], base[t]));
+        }
         if (!whole) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) p[e] = seen(t, e / 4, e % 4) ? p[e] : 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = p[e] * vs[e / 4][e % 4];
+        if (!whole) {   // a token that another row sees may have a NaN scale
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = p[e] == 0.0f ? 0.0f : x[e];
+        }
+        sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       };
       weigh();
-      float top = p[0];
+      float top = x[0];
 #pragma unroll
-      for (int e = 1; e < 8; ++e) top = fmaxf(top, p[e]);
-      if (__any(top > kMostWeight)) {                 // raise the maximum
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+      if (__any((top > kMostWeight) | (sum > kMostSum) | (base[t] == kUnset))) {   // raise the maximum
         float best = kLowest;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            best = fmaxf(best, whole | seen(t, u, r) ? (float)sc[t][u][r] * (ks[u][r] * qf[t]) : kLowest);
+        for (int e = 0; e < 8; ++e) {
+          const int u = e / 4, r = e % 4;
+          const float z = (float)sc[t][u][r] * (ks[u][r] * qf[t]) + __builtin_amdgcn_logf(fmaxf(vs[u][r], kLeastScale));
+          best = fmaxf(best, (whole | seen(t, u, r)) ? z : kLowest);
+        }
         best = max16_32(best);
         const float next = fminf(base[t], kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base[t]);
         l[t] *= by;
+        weight[t] *= by;
 #pragma unroll
         for (int i = 0; i < E; ++i) o[t][i] *= by;
         base[t] = next;
         weigh();
       }
-      l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      l[t] += sum;
       v4u packed;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int u = e / 2, r = 2 * (e % 2);
-        float wa = p[2 * e] * vs[u][r], wb = p[2 * e + 1] * vs[u][r + 1];
-        if (!whole) {   // a token that another row sees may have a NaN scale
-          wa = p[2 * e] == 0.0f ? 0.0f : wa;
-          wb = p[2 * e + 1] == 0.0f ? 0.0f : wb;
-        }
-        packed[e] = pack_f16x2_rn(wa, wb);
-      }
+      for (int e = 0; e < 4; ++e) packed[e] = pack_f16x2_rn(x[2 * e], x[2 * e + 1]);
       w[t] = __builtin_bit_cast(v8h, packed);
     }
 
@@ -467,6 +452,9 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
           for (int i = 0; i < 4; ++i) vw[u][r][i] = x[i];
         }
       }
+    const v8h ones = {1, 1, 1, 1, 1, 1, 1, 1};
+#pragma unroll
+    for (int t = 0; t < QT; ++t) weight[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, w[t], weight[t], 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < E; i += 4) {
       v4u f[4];
@@ -479,7 +467,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     }
     if (refill) {
       __builtin_amdgcn_s_waitcnt(0xC07F);
-      load_values(j0 + S * kStride, stage);
+      load_values(next0, next1, stage);
     }
   }
 
@@ -496,7 +484,8 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     float top = kLowest;
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) top = fmaxf(top, stat[v][col][0]);
-    const float mine = __builtin_amdgcn_exp2f((base[t] == kUnset ? kLowest : kWeightBits - base[t]) - top) * vmax;
+    const float mine = __builtin_amdgcn_exp2f((base[t] == kUnset ? kLowest : kWeightBits - base[t]) - top);
+    const float offset = weight[t][0] * (BITS == 4 ? -8.0f : -128.0f);
     const int r = tid / 16 % 16, seg = tid % 16;       // the first four wavefronts finish the rows
     float rtop = kLowest, sum = 0.0f, out[E];
 #pragma unroll
@@ -511,7 +500,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i)
           sh.o[wave][col][PASS * (4 * quad + e) + i] =
-              o[t][PASS * p + i][e] * (BITS == 4 && i % 2 ? mine * 0.0625f : mine);
+              __fmaf_rn(o[t][PASS * p + i][e], BITS == 4 && i % 2 ? 0x1p20f : 0x1p24f, offset) * mine;
       __syncthreads();
       // four wavefronts sum four; with more, each group of four its own, and then the first four the groups
       const int g = wave / 4;

@@ -365,7 +365,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
         for (int r = 0; r < 16; r += 4) {
           const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) best = fmaxf(best, whole | seen(kt, r + i) ? p[kt][r + i] * ks[i] : kLowest);
+          for (int i = 0; i < 4; ++i) best = fmaxf(best, (whole | seen(kt, r + i)) ? p[kt][r + i] * ks[i] : kLowest);
         }
       best = max32(best);
       const float next = fminf(base, kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base);
