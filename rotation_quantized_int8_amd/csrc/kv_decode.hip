@@ -550,21 +550,33 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   }
 }
 
-// Joins the splits of each row: `segs` segments of 16 lanes take the splits in
+// Joins the splits of each row: SEGS segments of 16 lanes take the splits in
 // turn, E elements a lane, 16 splits of a segment at a time (their maxima and
 // sums a lane each, so that the partial rows load without waiting for one
-// another); then one segment rotates the row back.
-template <int D>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int segs) {
-  constexpr int E = D / 16;
-  __shared__ __align__(16) float part[16][D + 4];
-  __shared__ float stat[16][2];
-  const int sub = threadIdx.x / 16, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
-  const KvSeq s = kv_sequence(a, b);
-  const int row = blockIdx.x * (16 / segs) + sub / segs;     // of the sequence's rows with this key head
-  const int i = kv_query_of(a, row);
-  const bool valid = i < s.n;
+// another); the four segments of a wavefront are summed by lane swaps, the
+// wavefronts through LDS, and the row is rotated back.  What counts is the
+// chain of loads, not the bytes: 4, 16 or 64 segments, so that a segment has
+// few splits.
+template <int D, int SEGS>
+__global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn a, KvSplit sp) {
+  constexpr int E = D / 16, WAVES = SEGS / 4;          // wavefronts of a row
+  __shared__ __align__(16) float part[WAVES][D];
+  __shared__ float stat[WAVES][2];
+  const int sub = threadIdx.x / 16 % SEGS, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
+  const int row = SEGS == 4 ? blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;   // of the sequence's with this key head
   const int tile = row / sp.rows, rr = row - tile * sp.rows;
+  if (tile >= sp.tiles || rr >= sp.kept) return;
+  // the first 16 splits' maxima and sums, without waiting for the sequence's lengths
+  const int64_t at = sp.row(b, h, tile, 0, rr);
+  int z = sub + seg * SEGS;                            // this lane's split
+  float mz = kLowest, lz = 0.0f;
+  if (z < sp.splits) {
+    mz = sp.ml[2 * (at + (int64_t)z * sp.kept)];
+    lz = sp.ml[2 * (at + (int64_t)z * sp.kept) + 1];
+  }
+  const KvSeq s = kv_sequence(a, b);
+  const int i = kv_query_of(a, row);
+  if (i >= s.n) return;                                // uniform in a wavefront, and where wavefronts meet
   // the splits that the row's tile ran: up to the last token its last row sees
   int last = s.kv;
   if (a.causal) {
@@ -573,30 +585,32 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int 
     last = s.kv - s.n + kv_query_of(a, r1) + 1;
   }
   int n = (last + sp.chunk - 1) / sp.chunk;
-  n = valid ? (n < 1 ? 1 : n < sp.splits ? n : sp.splits) : 0;
+  n = n < 1 ? 1 : n < sp.splits ? n : sp.splits;
   float m = kLowest, l = 0.0f, x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = 0.0f;
-  for (int z0 = sub % segs; z0 < n; z0 += 16 * segs) {
-    const int z = z0 + seg * segs;                     // this lane's split
-    float mz = kLowest, lz = 0.0f;
-    if (z < n) {
-      const int64_t at = sp.row(b, h, tile, z, rr);
-      mz = sp.ml[2 * at];
-      lz = sp.ml[2 * at + 1];
+  for (int z0 = sub; z0 < n; z0 += 16 * SEGS) {
+    if (z0 != sub) {
+      z = z0 + seg * SEGS;
+      if (z < n) {
+        mz = sp.ml[2 * (at + (int64_t)z * sp.kept)];
+        lz = sp.ml[2 * (at + (int64_t)z * sp.kept) + 1];
+      }
     }
+    mz = z < n ? mz : kLowest;
+    lz = z < n ? lz : 0.0f;
     const float next = fmaxf(m, warp_max16(mz)), keep = __builtin_amdgcn_exp2f(m - next);
-    const float w = __builtin_amdgcn_exp2f(mz - next);
+    const float w = z < n ? __builtin_amdgcn_exp2f(mz - next) : 0.0f;
     m = next;
     l = l * keep + lz * w;                             // summed over the lanes below
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= keep;
-    const int count = (n - z0 + segs - 1) / segs;
+    const int count = (n - z0 + SEGS - 1) / SEGS;
 #pragma unroll 4
     for (int k = 0; k < 16; ++k) {
       if (k >= count) break;
       const float wk = __shfl(w, k, 16);
-      const float* o = sp.o + sp.row(b, h, tile, z0 + k * segs, rr) * D + seg * E;
+      const float* o = sp.o + (at + (int64_t)(z0 + k * SEGS) * sp.kept) * D + seg * E;
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
         const v4f y = *reinterpret_cast<const v4f*>(o + e);
@@ -607,28 +621,46 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn a, KvSplit sp, int 
   }
 #pragma unroll
   for (int k = 1; k < 16; k <<= 1) l += __shfl_xor(l, k);
-  if (seg == 0) {
-    stat[sub][0] = m;
-    stat[sub][1] = l;
-  }
+  float top = max16_32(m), by = __builtin_amdgcn_exp2f(m - top), sum = sum16_32(l * by);
 #pragma unroll
-  for (int e = 0; e < E; ++e) part[sub][seg * E + e] = x[e];
-  __syncthreads();
-  if (sub % segs || !valid) return;
-  float top = kLowest, sum = 0.0f;
-  for (int z = 0; z < segs; ++z) top = fmaxf(top, stat[sub + z][0]);
+  for (int e = 0; e < E; ++e) x[e] = sum16_32(x[e] * by);
+  if constexpr (WAVES > 1) {
+    const int wave = threadIdx.x / 64;
+    if (sub % 4 == 0) {
+      if (seg == 0) {
+        stat[wave][0] = top;
+        stat[wave][1] = sum;
+      }
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.0f;
-  for (int z = 0; z < segs; ++z) {
-    const float by = __builtin_amdgcn_exp2f(stat[sub + z][0] - top);
-    sum += by * stat[sub + z][1];
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<v4f*>(&part[wave][seg * E + e]) = (v4f){x[e], x[e + 1], x[e + 2], x[e + 3]};
+    }
+    __syncthreads();
+    if (wave) return;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] += by * part[sub + z][seg * E + e];
+    for (int v = 0; v < WAVES; ++v) top = fmaxf(top, stat[v][0]);
+    sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.0f;
+#pragma unroll
+    for (int v = 0; v < WAVES; v += 4) {
+      by = __builtin_amdgcn_exp2f(stat[v + sub][0] - top);
+      sum += stat[v + sub][1] * by;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const v4f y = *reinterpret_cast<const v4f*>(&part[v + sub][seg * E + e]);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) x[e + g] += y[g] * by;
+      }
+    }
+    sum = sum16_32(sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = sum16_32(x[e]);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] * (kv_rsqrt(D) / sum);
   rotate_row<D>(x, seg);
-  store_row<E>(a.o + ((s.first + i) * a.q_heads + h * a.group + row - i * a.group) * D + seg * E, a.bf16, x);
+  if (sub % 4 == 0) store_row<E>(a.o + ((s.first + i) * a.q_heads + h * a.group + row - i * a.group) * D + seg * E, a.bf16, x);
 }
 
 template <int D, int BITS, int QT, int WAVES>
@@ -684,15 +716,22 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   return p;
 }
 
-hipError_t launch_kv_join(const KvAttn& a, const KvSplit& sp, hipStream_t stream) {
-  int segs = 1;
-  while (segs < 16 && segs < sp.splits) segs *= 2;
-  const unsigned per = 16 / segs, rows = (unsigned)a.max_q * a.group;
-  const dim3 grid((rows + per - 1) / per, a.c.heads, a.batch);
-  if (a.c.head_dim == 64) kv_join_kernel<64><<<grid, 256, 0, stream>>>(a, sp, segs);
-  else if (a.c.head_dim == 128) kv_join_kernel<128><<<grid, 256, 0, stream>>>(a, sp, segs);
-  else kv_join_kernel<256><<<grid, 256, 0, stream>>>(a, sp, segs);
+namespace {
+
+template <int D>
+hipError_t join(const KvAttn& a, const KvSplit& sp, hipStream_t stream) {
+  const unsigned rows = (unsigned)a.max_q * a.group;
+  if (sp.splits <= 4) kv_join_kernel<D, 4><<<dim3((rows + 3) / 4, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
+  else if (sp.splits <= 32) kv_join_kernel<D, 16><<<dim3(rows, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
+  else kv_join_kernel<D, 64><<<dim3(rows, a.c.heads, a.batch), 1024, 0, stream>>>(a, sp);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_join(const KvAttn& a, const KvSplit& sp, hipStream_t stream) {
+  return a.c.head_dim == 64 ? join<64>(a, sp, stream)
+         : a.c.head_dim == 128 ? join<128>(a, sp, stream) : join<256>(a, sp, stream);
 }
 
 hipError_t launch_kv_decode(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
