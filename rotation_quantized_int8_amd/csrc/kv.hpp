@@ -54,6 +54,13 @@ __device__ __forceinline__ int kv_query_of(const KvAttn& a, int row) {
   return (int)((uint64_t)(uint32_t)row * a.group_mul >> a.group_shift);
 }
 
+// The multiplier and shift of such a division, 1 <= d < 2^31.
+inline void kv_divider(uint32_t d, uint32_t* mul, int* shift) {
+  *shift = 31;
+  while ((1ull << (*shift - 31)) < d) ++*shift;
+  *mul = (uint32_t)((1ull << *shift) / d + 1);
+}
+
 hipError_t launch_kv_append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16, const int64_t* slots,
                             int64_t T, hipStream_t stream);
 hipError_t launch_kv_read(const KvCache& c, const int64_t* slots, int64_t T, uint16_t* K, uint16_t* V, bool bf16,
@@ -80,26 +87,28 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
   return bf16 ? (uint32_t)f32_to_bf16_rn(a) | ((uint32_t)f32_to_bf16_rn(b) << 16) : pack_f16x2_rn(a, b);
 }
 
-// The queries and tokens of sequence b, made safe: rows [first, first + n) lie
+// The queries and tokens of a sequence, made safe: rows [first, first + n) lie
 // in [0, T), and 0 <= kv <= max_kv.
 struct KvSeq {
   int64_t first;
   int n, kv;
 };
-__device__ __forceinline__ KvSeq kv_sequence(const KvAttn& a, int b) {
+__device__ __forceinline__ KvSeq kv_safe(const KvAttn& a, int64_t from, int64_t to, int kv) {
   KvSeq s;
+  from = from < 0 ? 0 : from > a.T ? a.T : from;
+  to = to < from ? from : to > a.T ? a.T : to;
+  s.first = from;
+  s.n = to - from > a.max_q ? a.max_q : (int)(to - from);
+  s.kv = kv < 0 ? 0 : kv > a.max_kv ? a.max_kv : kv;
+  return s;
+}
+__device__ __forceinline__ KvSeq kv_sequence(const KvAttn& a, int b) {
   int64_t from = (int64_t)b * a.each_q, to = from + a.each_q;
   if (a.q_start) {
     from = a.q_start[b];
     to = a.q_start[b + 1];
   }
-  from = from < 0 ? 0 : from > a.T ? a.T : from;
-  to = to < from ? from : to > a.T ? a.T : to;
-  s.first = from;
-  s.n = to - from > a.max_q ? a.max_q : (int)(to - from);
-  const int kv = a.kv_lens[b];
-  s.kv = kv < 0 ? 0 : kv > a.max_kv ? a.max_kv : kv;
-  return s;
+  return kv_safe(a, from, to, a.kv_lens[b]);
 }
 
 }  // namespace convrot

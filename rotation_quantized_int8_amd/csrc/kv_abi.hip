@@ -70,7 +70,7 @@ bool dtype_ok(int dtype) { return dtype == CONVROT_DTYPE_F16 || dtype == CONVROT
 bool attention_sizes_ok(const convrot_kv_cache* c, int64_t T, int64_t q_heads, int64_t batch, int64_t max_q,
                         int64_t max_kv) {
   return T >= 0 && T <= kInt && batch >= 0 && batch <= 65535 && q_heads >= 1 && q_heads <= 65535 &&
-         q_heads % c->heads == 0 && max_q >= 0 && max_q <= kInt && max_kv >= 0 && max_kv <= kInt - 4096 &&
+         q_heads % c->heads == 0 && max_q >= 0 && max_q <= kInt && max_kv >= 0 && max_kv <= (1 << 30) &&
          max_q * (q_heads / c->heads) <= kInt - 4096;
 }
 
@@ -82,9 +82,7 @@ KvAttn attention_args(const convrot_kv_cache* c, int64_t T, int64_t q_heads, int
   a.batch = (int)batch;
   a.q_heads = (int)q_heads;
   a.group = (int)(q_heads / c->heads);
-  a.group_shift = 31;
-  while ((1 << (a.group_shift - 31)) < a.group) ++a.group_shift;
-  a.group_mul = (uint32_t)((1ull << a.group_shift) / (uint64_t)a.group + 1);
+  kv_divider((uint32_t)a.group, &a.group_mul, &a.group_shift);
   a.max_q = (int)(max_q < T ? max_q : T);
   a.max_kv = (int)max_kv;
   return a;

@@ -8,16 +8,23 @@
 namespace convrot {
 
 // How a call is split: the rows (query, head in group) of one key head in
-// tiles of `rows`, the tokens in `splits` chunks.  With more than one split
-// the partial outputs go through the workspace: row() numbers them.
+// tiles of `rows`, the tokens of a sequence in chunks.  A unit is one chunk of
+// one sequence.  With balance = 0 every sequence has `splits` units of `chunk`
+// tokens (those past its end are idle).  Otherwise the chunk follows from the
+// lengths on the device (kv_units), so that the units of all sequences are
+// about `balance` per head and tile, and unit numbers run through the
+// sequences; `units` bounds them.  Where a sequence may have several units the
+// partial outputs go through the workspace: row() numbers them.
 struct KvSplit {
   int rows, tiles, kept;     // kept: rows of a tile that can be valid
   int splits, chunk;
-  int heads;
+  int balance, units;
+  uint32_t balance_mul;      // division by `balance`, as KvAttn's by the group
+  int balance_shift;
   float* o;                  // [.., D], unnormalised, rotated basis
   float* ml;                 // [.., 2]: maximum (log2 units) and sum
-  __device__ __forceinline__ int64_t row(int b, int h, int tile, int split, int r) const {
-    return ((((int64_t)b * heads + h) * tiles + tile) * splits + split) * kept + r;
+  __device__ __forceinline__ int64_t row(int h, int tile, int unit, int r) const {
+    return (((int64_t)h * tiles + tile) * units + unit) * kept + r;
   }
 };
 struct KvPlan {
@@ -73,6 +80,98 @@ __device__ __forceinline__ float sum16_32(float v) {
   float w;
   v = pair16(v, w);
   return sum32(v + w);
+}
+
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, true);    // row_shr 1, 2, 4, 8
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, true);    // the row before, into rows 1 and 3
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, true);    // the first half, into the second
+  return x;
+}
+
+// The units of a balanced call (at most 256 sequences), the same in every
+// wavefront of every workgroup: a chunk of `chunk` tokens, a multiple of 128,
+// and sequence `b` has units first .. first + n - 1 (n at least 1).  Asked for
+// the sequence of a unit (b < 0) or for a sequence; b < 0 on return: no such
+// unit.  The chunk starts at the mean that gives `balance` units and, where
+// there are at least twice as many units as sequences, grows until the units
+// are no more than that, so that they all run at once.  A lane looks at WORDS
+// sequences.
+struct KvUnits {
+  int b, first, n, chunk;
+  KvSeq seq;
+};
+
+template <int WORDS>
+__device__ __forceinline__ KvUnits kv_units_of(const KvAttn& a, const KvSplit& sp, int b, int unit) {
+  const int lane = threadIdx.x % 64;
+  uint32_t blocks[WORDS], n[WORDS], sum[WORDS], mine = 0;
+  int kv[WORDS], from[WORDS], to[WORDS];
+#pragma unroll
+  for (int k = 0; k < WORDS; ++k) {
+    const int i = 64 * k + lane;
+    const bool in = i < a.batch;
+    kv[k] = in ? a.kv_lens[i] : 0;
+    from[k] = a.q_start && in ? a.q_start[i] : 0;
+    to[k] = a.q_start && in ? a.q_start[i + 1] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < WORDS; ++k) {
+    kv[k] = kv[k] < 0 ? 0 : kv[k] > a.max_kv ? a.max_kv : kv[k];
+    blocks[k] = ((uint32_t)kv[k] + 127) / 128;
+    mine += blocks[k];
+  }
+  const uint32_t total = __builtin_amdgcn_readlane(wave_scan(mine), 63), want = (uint32_t)sp.balance;
+  // ceil(total / want): at most 2^31 blocks, the multiplier as for the group
+  uint32_t chunk = (uint32_t)((uint64_t)(total + want - 1) * sp.balance_mul >> sp.balance_shift);
+  chunk = chunk < 2 ? 2 : chunk;
+  for (;;) {
+    // ceil(blocks / chunk) in fp32 (blocks < 2^23): the quotient by the reciprocal is off by one at most
+    const float inverse = __builtin_amdgcn_rcpf((float)chunk);
+    uint32_t before = 0;
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) {
+      uint32_t need = (uint32_t)((float)blocks[k] * inverse);
+      need = need * chunk > blocks[k] ? need - 1 : need;
+      need = need * chunk < blocks[k] ? need + 1 : need;
+      need = need * chunk < blocks[k] ? need + 1 : need;
+      n[k] = 64 * k + lane < a.batch ? (need < 1 ? 1 : need) : 0;
+      sum[k] = before + wave_scan(n[k]);
+      before = __builtin_amdgcn_readlane(sum[k], 63);
+    }
+    if (before <= want || 2 * (uint32_t)a.batch > want) break;
+    chunk += chunk < 8 ? 1 : chunk / 8;
+  }
+  KvUnits u{-1, 0, 0, (int)chunk * 128, {0, 0, 0}};
+#pragma unroll
+  for (int k = WORDS - 1; k >= 0; --k) {
+    int at = -1;
+    if (b < 0) {
+      const uint64_t past = __ballot((64 * k + lane < a.batch) & (sum[k] > (uint32_t)unit));
+      if (past) at = __builtin_ctzll(past);
+    } else if (b / 64 == k) {
+      at = b % 64;
+    }
+    if (at >= 0) {
+      u.b = 64 * k + at;
+      u.n = __builtin_amdgcn_readlane(n[k], at);
+      u.first = __builtin_amdgcn_readlane(sum[k], at) - u.n;
+      int64_t f = (int64_t)u.b * a.each_q, t = f + a.each_q;
+      if (a.q_start) {
+        f = (int)__builtin_amdgcn_readlane(from[k], at);
+        t = (int)__builtin_amdgcn_readlane(to[k], at);
+      }
+      u.seq = kv_safe(a, f, t, __builtin_amdgcn_readlane(kv[k], at));
+    }
+  }
+  return u;
+}
+__device__ __forceinline__ KvUnits kv_units(const KvAttn& a, const KvSplit& sp, int b, int unit) {
+  return a.batch <= 64 ? kv_units_of<1>(a, sp, b, unit) : kv_units_of<4>(a, sp, b, unit);
 }
 
 // The value of the lane whose number in its 16-lane row differs in bit BIT.

@@ -43,7 +43,6 @@ namespace {
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
 constexpr int kStep = 32;                     // tokens a wavefront takes at once
-constexpr int kChunkMax = 4096;               // tokens of a workgroup at most (its page numbers are kept in LDS)
 constexpr float kWeightBits = 8.0f;           // p = 2^(score - m + 8)
 constexpr float kMostWeight = 32768.0f;       // m is raised past this weight
 constexpr float kLeastScale = 0x1p-80f;       // a value's scale in the maximum, at least
@@ -144,28 +143,50 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   __shared__ __align__(16) char qbuf[4][QBYTES];       // the rows as loaded, then each as its two int8 planes
   __shared__ float qscale[ROWS];
   __shared__ float stat[WAVES][16][2];
-  __shared__ int pages[kChunkMax / CONVROT_KV_PAGE_MIN + 1];
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 16, quad = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int split = blockIdx.x % sp.splits, tile = blockIdx.x / sp.splits;
-  const int c0 = split * sp.chunk, log2p = a.c.page_log2, page0 = c0 >> log2p;
-
-  // the chunk's page numbers, without waiting for the sequence's length
-  for (int i = tid; i <= sp.chunk >> log2p && page0 + i < a.width; i += 64 * WAVES) {
-    const int p = a.table[(int64_t)b * a.width + page0 + i];
-    pages[i] = p >= 0 && p < a.c.pages ? p : -1;
+  const int h = blockIdx.y, log2p = a.c.page_log2;
+  int b = blockIdx.z, unit, split, tile, c0, chunk = sp.chunk;
+  KvSeq s;
+  bool alone = sp.splits == 1;                         // the sequence's only unit writes the output itself
+  if (sp.balance) {
+    unit = blockIdx.x % sp.units;
+    tile = blockIdx.x / sp.units;
+    const KvUnits u = kv_units(a, sp, -1, unit);
+    if (u.b < 0) return;
+    b = u.b;
+    split = unit - u.first;
+    chunk = u.chunk;
+    alone = u.n == 1;
+    s = u.seq;
+  } else {
+    split = blockIdx.x % sp.splits;
+    tile = blockIdx.x / sp.splits;
+    unit = b * sp.splits + split;
   }
-  const KvSeq s = kv_sequence(a, b);
+  c0 = split * chunk;
+
+  // The page numbers of the wavefront's next 64 steps, one a lane (two groups of 16 tokens a step), without waiting
+  // for the sequence's length.
+  int pages[2];
+  auto find_pages = [&](int step) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t i = (c0 + kStep * wave + kStride * (step + lane) + 16 * u) >> log2p;
+      const int p = i < a.width ? a.table[b * a.width + i] : -1;
+      pages[u] = p < a.c.pages ? p : -1;
+    }
+  };
+  find_pages(0);
+  if (!sp.balance) s = kv_sequence(a, b);
   const int rows = s.n * a.group - tile * ROWS;      // valid rows from this tile on
   if (rows <= 0) return;
   // the tokens that the tile's last and first row see
   const int last = a.causal ? s.kv - s.n + kv_query_of(a, tile * ROWS + (rows < ROWS ? rows : ROWS) - 1) + 1 : s.kv;
   const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * ROWS) + 1 : s.kv;
-  const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
+  const int c1 = last < c0 + chunk ? last : c0 + chunk;
   if (c1 <= c0 && split > 0) return;                 // the join leaves it out by the same rule
-  __syncthreads();
 
   // ---- direct loads: the query rows, then the first steps
   if (wave < 4) {
@@ -180,16 +201,23 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
             __builtin_amdgcn_readfirstlane(to + n * 1024));
     }
   }
-  auto page_of = [&](int j) { return __builtin_amdgcn_readfirstlane(j < c1 ? pages[(j >> log2p) - page0] : -1); };
   // Token 4 r + quad of a group of 16 is the one whose score ends up in register r of the lanes of `quad`, so a value
   // read of register r covers 4 neighbouring rows.  The keys' codes are laid down in operand order, 16 bytes a lane.
   const int turned = 4 * (col % 4) + col / 4;          // token of the lane's key codes, and of its scale
   const uint32_t koff = R::kRow < 64 ? 0 : turned * R::kRow + quad * 16, voff = lane * 16;
   char* ring = sh.ring[wave];
   const uint32_t ring0 = (uint32_t)(uintptr_t)(lds_ptr_t)ring;
-  auto group_row = [&](int j) {
-    const int p = page_of(j);
-    return (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
+  uint32_t present = 0;                                // bits 2 stage + u: the group's page is there
+  int64_t row0, row1;
+  // first rows of a step's two groups (of page 0 where there is none)
+  auto find_rows = [&](int step, int stage) {
+    const int j = c0 + kStep * wave + kStride * step;
+    const int p0 = __builtin_amdgcn_readlane(pages[0], step % 64);
+    const int p1 = j + 16 < c1 ? __builtin_amdgcn_readlane(pages[1], step % 64) : -1;
+    const int mask = (1 << log2p) - 1;
+    row0 = (((int64_t)(p0 < 0 ? 0 : p0) * a.c.heads + h) << log2p) + (j & mask);
+    row1 = (((int64_t)(p1 < 0 ? 0 : p1) * a.c.heads + h) << log2p) + (j + 16 & mask);
+    present = (present & ~(3u << 2 * stage)) | ((p0 >= 0) | (p1 >= 0) << 1) << 2 * stage;
   };
   auto load_keys = [&](int64_t r0, int64_t r1, int stage) {   // of the groups with these first rows, and all scales
     const uint32_t to = __builtin_amdgcn_readfirstlane(ring0 + stage * R::kStage);
@@ -216,13 +244,13 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
           dma16(a.c.vc + (u ? r1 : r0) * R::kRow + m * 1024, voff, to + (u * (R::kLoads / 2) + m) * 1024);
     }
   };
-  int j0 = c0 + kStep * wave, stage = 0;
+  int j0 = c0 + kStep * wave, step = 0, stage = 0;
 #pragma unroll
   for (int n = 0; n < S; ++n)
     if (j0 + n * kStride < c1) {
-      const int64_t r0 = group_row(j0 + n * kStride), r1 = group_row(j0 + n * kStride + 16);
-      load_keys(r0, r1, n);
-      load_values(r0, r1, n);
+      find_rows(n, n);
+      load_keys(row0, row1, n);
+      load_values(row0, row1, n);
     }
 
   // ---- the rotated queries, as two int8 planes, while the first steps arrive
@@ -311,9 +339,8 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   }
 
   // Direct loads return in order: waiting for a half leaves in flight what was issued after it.
-  for (; j0 < c1; j0 += kStride, stage = S == 1 ? 0 : stage ^ 1) {
+  for (; j0 < c1; j0 += kStride, ++step, stage = S == 1 ? 0 : stage ^ 1) {
     const bool more = j0 + kStride < c1, refill = j0 + S * kStride < c1;
-    int64_t next0 = 0, next1 = 0;
     const char* here_k = ring + stage * R::kStage;
     const char* here_v = here_k + R::kHalf;
     const char* here_s = here_v + R::kHalf;
@@ -341,7 +368,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
       ks[u] = *reinterpret_cast<const v4f*>(here_s + 64 * u + 16 * quad);
       vs[u] = *reinterpret_cast<const v4f*>(here_s + 128 + 64 * u + 16 * quad);
     }
-    const bool here[2] = {page_of(j0) >= 0, page_of(j0 + 16) >= 0};   // false past c1 too
+    const bool here[2] = {(present >> 2 * stage & 1) != 0, (present >> 2 * stage & 2) != 0};   // false past c1 too
     const bool whole = j0 + kStep <= first && here[0] && here[1];
     // ---- scores; the next keys load as soon as these are used
     v4i sc[QT][2];
@@ -365,10 +392,10 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
         for (int r = 0; r < 4; ++r) sc[t][u][r] = (sc[t][u][r] << 8) + lo[t][r];
     }
     if (refill) {
-      next0 = group_row(j0 + S * kStride);
-      next1 = group_row(j0 + S * kStride + 16);
+      if ((step + S) % 64 == 0) find_pages(step + S);
+      find_rows(step + S, stage);
       __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the reads are done
-      load_keys(next0, next1, stage);
+      load_keys(row0, row1, stage);
     }
 
     // ---- weights
@@ -467,7 +494,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     }
     if (refill) {
       __builtin_amdgcn_s_waitcnt(0xC07F);
-      load_values(next0, next1, stage);
+      load_values(row0, row1, stage);
     }
   }
 
@@ -526,9 +553,9 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     }
     if (wave >= 4) continue;
     const int rr = 16 * t + r;
-    if (sp.splits > 1) {
+    if (!alone) {
       if (rr < rows) {
-        const int64_t at = sp.row(b, h, tile, split, rr);
+        const int64_t at = sp.row(h, tile, unit, rr);
         float* dst = sp.o + at * D + seg * E;
 #pragma unroll
         for (int i = 0; i < E; i += 4) *reinterpret_cast<v4f*>(dst + i) = (v4f){out[i], out[i + 1], out[i + 2], out[i + 3]};
@@ -566,15 +593,22 @@ __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn
   const int row = SEGS == 4 ? blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;   // of the sequence's with this key head
   const int tile = row / sp.rows, rr = row - tile * sp.rows;
   if (tile >= sp.tiles || rr >= sp.kept) return;
+  int first = b * sp.splits, n = sp.splits, chunk = sp.chunk;
+  KvSeq s;
+  if (sp.balance) {
+    const KvUnits u = kv_units(a, sp, b, 0);
+    first = u.first, n = u.n, chunk = u.chunk, s = u.seq;
+    if (n == 1) return;                                // written by its only unit
+  }
   // the first 16 splits' maxima and sums, without waiting for the sequence's lengths
-  const int64_t at = sp.row(b, h, tile, 0, rr);
+  const int64_t at = sp.row(h, tile, first, rr);
   int z = sub + seg * SEGS;                            // this lane's split
   float mz = kLowest, lz = 0.0f;
-  if (z < sp.splits) {
+  if (z < n) {
     mz = sp.ml[2 * (at + (int64_t)z * sp.kept)];
     lz = sp.ml[2 * (at + (int64_t)z * sp.kept) + 1];
   }
-  const KvSeq s = kv_sequence(a, b);
+  if (!sp.balance) s = kv_sequence(a, b);
   const int i = kv_query_of(a, row);
   if (i >= s.n) return;                                // uniform in a wavefront, and where wavefronts meet
   // the splits that the row's tile ran: up to the last token its last row sees
@@ -584,8 +618,8 @@ __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn
     r1 = r1 < s.n * a.group ? r1 : s.n * a.group - 1;
     last = s.kv - s.n + kv_query_of(a, r1) + 1;
   }
-  int n = (last + sp.chunk - 1) / sp.chunk;
-  n = n < 1 ? 1 : n < sp.splits ? n : sp.splits;
+  const int ran = last > 0 ? (last - 1) / chunk + 1 : 1;
+  n = ran < n ? ran : n;
   float m = kLowest, l = 0.0f, x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = 0.0f;
@@ -668,8 +702,8 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
   KvSplit sp = p.split;
   sp.o = static_cast<float*>(workspace);
   sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
-  kv_decode_kernel<D, BITS, QT, WAVES>
-      <<<dim3(sp.splits * sp.tiles, a.c.heads, a.batch), 64 * WAVES, 0, stream>>>(a, sp);
+  const dim3 grid(sp.balance ? sp.units * sp.tiles : sp.splits * sp.tiles, a.c.heads, sp.balance ? 1 : a.batch);
+  kv_decode_kernel<D, BITS, QT, WAVES><<<grid, 64 * WAVES, 0, stream>>>(a, sp);
   if (hipError_t e = hipGetLastError()) return e;
   return sp.splits > 1 ? launch_kv_join(a, sp, stream) : hipSuccess;
 }
@@ -682,10 +716,13 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
 
 }  // namespace
 
-// One workgroup per sequence, key head and tile of rows where these fill the
-// card.  Where they do not: up to 2048 tokens one workgroup of 16 wavefronts
-// (8 for heads of 256) walks them all, which saves the join's launch; longer
-// ones are split so that the chunks fill the card once, in workgroups of 4.
+// A short context (and a batch that fills the card several times over with
+// contexts that are not long) takes one workgroup per sequence, key head and
+// tile of rows, and no join; where these would leave CUs idle, of 16
+// wavefronts (8 for heads of 256).  Otherwise the tokens of all sequences are
+// cut into units that fill the card once (measured on 32 sequences of up to
+// 8192 tokens: twice as many units 51 us, four times as many 58 us, against
+// 45 us: starting and joining a unit costs about as much as 500 tokens).
 KvPlan kv_decode_plan(const KvAttn& a) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_q * a.group;
@@ -693,25 +730,34 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   s.rows = rows <= 16 ? 16 : 32;
   s.tiles = (int)((rows + s.rows - 1) / s.rows);
   s.kept = (int)(rows < s.rows ? rows : s.rows);
-  s.heads = a.c.heads;
   p.waves = 4;
-  const int64_t base = (int64_t)s.tiles * a.c.heads * a.batch;
+  s.splits = 1;
+  s.chunk = a.max_kv < 128 ? 128 : (a.max_kv + 127) / 128 * 128;
+  s.units = a.batch;
+  const int64_t heads = (int64_t)s.tiles * a.c.heads, base = heads * a.batch;
   const int64_t slots = 256 * kv_decode_wgs(a.c.head_dim, s.rows / 16, 4);   // resident on 256 CUs
-  int64_t splits = slots / base;
-  if (s.rows == 16 && splits > 1 && a.max_kv > 128 && a.max_kv <= 2048) {
+  if (a.max_kv <= 256) return p;
+  if (a.max_kv <= 1024 && base <= 256 && s.rows == 16) {
     p.waves = kv_decode_wide(a.c.head_dim);
-    splits = 1;
+    return p;
   }
-  const int64_t most = ((int64_t)a.max_kv + 255) / 256, least = ((int64_t)a.max_kv + kChunkMax - 1) / kChunkMax;
-  if (splits > most) splits = most;
-  if (splits < least) splits = least;
-  if (splits < 1) splits = 1;
-  const int64_t chunk = (a.max_kv + splits - 1) / splits;
-  s.chunk = (int)((chunk + 127) / 128 * 128);
-  if (s.chunk < 128) s.chunk = 128;
-  s.splits = (int)(((int64_t)a.max_kv + s.chunk - 1) / s.chunk);
-  if (s.splits < 1) s.splits = 1;
-  p.parts = s.splits > 1 ? base * s.splits * s.kept : 0;
+  if (base >= 4 * slots && a.max_kv <= 8192) return p;
+  if (a.batch <= 256) {
+    const int64_t want = slots / heads;
+    s.balance = (int)(want < a.batch ? a.batch : want);
+    kv_divider((uint32_t)s.balance, &s.balance_mul, &s.balance_shift);
+    s.units = 2 * (int64_t)a.batch <= s.balance ? s.balance : s.balance + a.batch;
+    const int64_t most = (int64_t)a.batch * ((a.max_kv + 255) / 256);   // chunks have 256 tokens at least
+    if (s.units > most) s.units = (int)most;
+    s.splits = (a.max_kv + 255) / 256;                                  // a sequence's units at most
+    if (s.splits > s.units) s.splits = s.units;
+  } else {
+    if (a.max_kv <= 8192) return p;
+    s.chunk = 4096;
+    s.splits = (a.max_kv + s.chunk - 1) / s.chunk;
+    s.units = a.batch * s.splits;
+  }
+  p.parts = heads * s.units * s.kept;
   p.bytes = (size_t)p.parts * (a.c.head_dim + 2) * 4;
   return p;
 }

@@ -425,7 +425,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   auto unit_of = [&](int r) { return (8 * (r / 4) + 4 * hi + r % 4) % P::kUnits; };
   auto e_of = [&](int t, int r) { return t * P::kSpread + 8 * (r / 4) / P::kUnits; };
   if (sp.splits > 1) {
-    const int64_t at = sp.row(b, h, tile, split, 32 * wave + col);
+    const int64_t at = sp.row(h, tile, b * sp.splits + split, 32 * wave + col);
     float* dst = sp.o + at * D;
 #pragma unroll
     for (int t = 0; t < P::kTiles; ++t)
@@ -503,7 +503,6 @@ KvPlan kv_prompt_plan(const KvAttn& a) {
   s.rows = kRows;
   s.tiles = (int)((rows + kRows - 1) / kRows);
   s.kept = (int)(rows < kRows ? rows : kRows);
-  s.heads = a.c.heads;
   const int64_t base = (int64_t)s.tiles * a.c.heads * a.batch;
   int64_t splits = (512 + base - 1) / base;
   const int64_t most = (a.max_kv + 511) / 512;
@@ -514,6 +513,7 @@ KvPlan kv_prompt_plan(const KvAttn& a) {
   if (s.chunk < kStep) s.chunk = kStep;
   s.splits = (int)(((int64_t)a.max_kv + s.chunk - 1) / s.chunk);
   if (s.splits < 1) s.splits = 1;
+  s.units = (int)(a.batch * s.splits);
   p.parts = s.splits > 1 ? base * s.splits * s.kept : 0;
   p.bytes = (size_t)p.parts * (a.c.head_dim + 2) * 4;
   return p;
