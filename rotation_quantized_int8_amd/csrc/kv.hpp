@@ -79,12 +79,12 @@ __device__ __forceinline__ float in16_f32(uint32_t bits) {
   else return __half2float(__ushort_as_half((uint16_t)bits));
 }
 
-__device__ __forceinline__ uint32_t out16(float f, bool bf16) {
-  return bf16 ? f32_to_bf16_rn(f) : __half_as_ushort(__float2half_rn(f));
-}
-// Two fp32 values to 16 bits each, packed low then high.
-__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
-  return bf16 ? (uint32_t)f32_to_bf16_rn(a) | ((uint32_t)f32_to_bf16_rn(b) << 16) : pack_f16x2_rn(a, b);
+// Two fp32 values to bf16, each rounded once to nearest even, packed low then
+// high (one v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_bf16x2_rn(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){as_fp32(a), as_fp32(b)}, b2));
 }
 
 // The queries and tokens of a sequence, made safe: rows [first, first + n) lie

@@ -222,18 +222,25 @@ __device__ __forceinline__ void load_row(const uint16_t* p, bool bf16, float (&x
       for (int j = 0; j < 4; ++j) w[4 * i + j] = r[j];
     }
   }
+  if (bf16) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const uint32_t b = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-    x[i] = bf16 ? in16_f32<true>(b) : in16_f32<false>(b);
+    for (int i = 0; i < E; ++i) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = in16_f32<false>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
   }
 }
 
 template <int E>
 __device__ __forceinline__ void store_row(uint16_t* p, bool bf16, const float (&x)[E]) {
   uint32_t w[E / 2];
+  if (bf16) {
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) w[i] = pack16(x[2 * i], x[2 * i + 1], bf16);
+    for (int i = 0; i < E / 2; ++i) w[i] = pack_bf16x2_rn(x[2 * i], x[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) w[i] = pack_f16x2_rn(x[2 * i], x[2 * i + 1]);
+  }
   if constexpr (E == 4) {
     *reinterpret_cast<v2u*>(p) = (v2u){w[0], w[1]};
   } else {

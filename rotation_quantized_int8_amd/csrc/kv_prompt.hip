@@ -32,9 +32,11 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;
-constexpr int kStep = 64;                     // tokens of a step
+constexpr int kStep = 16 * kWaves;            // tokens of a step: each wavefront decodes a group of 16
 constexpr float kWeightBits = 8.0f;
 constexpr float kMostWeight = 32768.0f;
+constexpr float kLeastScale = 0x1p-80f;       // as in the single-token kernel
+constexpr float kMostSum = 0x1p92f;
 constexpr float kUnset = 1e30f;               // base of a row that has seen no token
 constexpr float kLowest = -1e30f;             // its maximum
 
@@ -43,46 +45,48 @@ __device__ __forceinline__ uint32_t less(uint32_t x, float by) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) - off);
 }
 
-// Eight codes as fp16 operands of the keys.  4 bits: elements 0 4 1 5 2 6 3 7,
-// the odd ones times 16; 8 bits: in order.
+// Eight codes as fp16 operands of the keys: the subnormals (c + 8) 2^-24 (with
+// 8 bits (c + 128) 2^-24), made by a mask and an exclusive or; what the offset
+// adds to a score is the row's own constant, taken off by the accumulator's
+// start.  4 bits: elements 0 4 1 5 2 6 3 7, the odd ones times 16; 8 bits: in
+// order.
 template <int BITS>
 __device__ __forceinline__ v4u key_halves(const uint32_t* w) {
   v4u f;
   if constexpr (BITS == 4) {
-    const uint32_t x = w[0] ^ 0x88888888u, y = x >> 8;
-    f[0] = less((x & 0x000F000Fu) | 0x64006400u, 1032.0f);
-    f[1] = less((x & 0x00F000F0u) | 0x64006400u, 1152.0f);
-    f[2] = less((y & 0x000F000Fu) | 0x64006400u, 1032.0f);
-    f[3] = less((y & 0x00F000F0u) | 0x64006400u, 1152.0f);
+    const uint32_t x = w[0], y = x >> 8;
+    f[0] = (x & 0x000F000Fu) ^ 0x00080008u;
+    f[1] = (x & 0x00F000F0u) ^ 0x00800080u;
+    f[2] = (y & 0x000F000Fu) ^ 0x00080008u;
+    f[3] = (y & 0x00F000F0u) ^ 0x00800080u;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      f[i] = less(__builtin_amdgcn_perm(0, w[i / 2], i % 2 ? 0x0C030C02u : 0x0C010C00u) ^ 0x64806480u, 1152.0f);
+      f[i] = __builtin_amdgcn_perm(0, w[i / 2], i % 2 ? 0x0C030C02u : 0x0C010C00u) ^ 0x00800080u;
   }
   return f;
 }
-
-// Element of its unit of 8 that half j of a key operand holds, and the factor
+// Where element e of its unit of 8 stands in a key operand, and the factor
 // that its code enters with.
 template <int BITS>
-__device__ __forceinline__ constexpr int key_element(int j) {
-  return BITS == 8 ? j : j / 2 + 4 * (j % 2);
-}
+__device__ __forceinline__ constexpr int key_place(int e) { return BITS == 8 ? e : 2 * (e % 4) + e / 4; }
 template <int BITS>
 __device__ __forceinline__ constexpr float key_factor(int e) { return BITS == 4 && e % 2 ? 16.0f : 1.0f; }
 
 // Element i of the unit for two tokens a and b, as a half pair (4 bits: the
-// odd elements times 16).
+// odd elements times 16).  1024 + (c + 8) and the like, less its offset: the
+// sum of the weights would have to be formed per wavefront, where this
+// subtraction is shared by all four.
 template <int BITS>
 __device__ __forceinline__ void value_halves(const uint32_t* a, const uint32_t* b, uint32_t (&f)[8]) {
   if constexpr (BITS == 4) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      const uint32_t x = __builtin_amdgcn_perm(b[0], a[0], i ? 0x07060302u : 0x05040100u) ^ 0x88888888u, y = x >> 8;
-      f[i] = less((x & 0x000F000Fu) | 0x64006400u, 1032.0f);
-      f[i + 1] = less((x & 0x00F000F0u) | 0x64006400u, 1152.0f);
-      f[i + 2] = less((y & 0x000F000Fu) | 0x64006400u, 1032.0f);
-      f[i + 3] = less((y & 0x00F000F0u) | 0x64006400u, 1152.0f);
+      const uint32_t x = __builtin_amdgcn_perm(b[0], a[0], i ? 0x07060302u : 0x05040100u), y = x >> 8;
+      f[i] = less((x & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
+      f[i + 1] = less((x & 0x00F000F0u) ^ 0x64806480u, 1152.0f);
+      f[i + 2] = less((y & 0x000F000Fu) ^ 0x64086408u, 1032.0f);
+      f[i + 3] = less((y & 0x00F000F0u) ^ 0x64806480u, 1152.0f);
     }
   } else {
 #pragma unroll
@@ -100,10 +104,10 @@ struct Prompt {
   static constexpr int kSteps = D / 16;                // matrix steps of a score
   static constexpr int kTiles = D / 32;                // output tiles
   static constexpr int kSpread = 256 / D;              // elements of a unit that share an output tile
-  // decoding: a key task is 16 bytes of one token's row, a value task one unit of 4 tokens
-  static constexpr int kKeyTasks = kStep * kRow / 16, kValueTasks = kStep / 4 * kUnits;
-  static constexpr int kKeyEach = (kKeyTasks + kThreads - 1) / kThreads;
-  static constexpr int kValueEach = (kValueTasks + kThreads - 1) / kThreads;
+  // A wavefront's group of 16 tokens: 16-byte pieces of the keys' rows, and units of 4 tokens of the values'.
+  static constexpr int kPieces = kRow, kTasks = 4 * kUnits;
+  static constexpr int kKeyEach = kPieces < 64 ? 1 : kPieces / 64;
+  static constexpr int kValueEach = kTasks < 64 ? 1 : kTasks / 64;
   static constexpr int kBuffer = kStep * D * 2;        // bytes of a step's keys, and of its values
   static constexpr int kQPitch = D * 2 + 16;
   static constexpr int kBytes = 4 * kBuffer > kRows * kQPitch ? 4 * kBuffer : kRows * kQPitch;
@@ -115,9 +119,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   constexpr int E = D / 16;
   extern __shared__ __align__(16) char lds[];          // keys [2], values [2]; first the queries
   __shared__ __align__(16) float kscale[2][kStep], vscale[2][kStep];
-  __shared__ __align__(16) int absent[2][4];
-  __shared__ float vtop[2];
-  __shared__ float qtop[kWaves];
+  __shared__ __align__(16) int absent[2][kWaves];
+  __shared__ float qtop[kWaves], qoffset[kRows];
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 32, hi = lane / 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -128,75 +131,49 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   const int rest = blockIdx.x / a.c.heads;
   const int split = rest % sp.splits, tile = sp.tiles - 1 - rest / sp.splits;
   const int log2p = a.c.page_log2;
+  const int c0 = split * sp.chunk;
 
   const KvSeq s = kv_sequence(a, b);
   const int rows = s.n * a.group - tile * kRows;
   if (rows <= 0) return;
-  const int c0 = split * sp.chunk;
   const int last = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + (rows < kRows ? rows : kRows) - 1) + 1 : s.kv;
   const int c1 = last < c0 + sp.chunk ? last : c0 + sp.chunk;
   if (c1 <= c0 && split > 0) return;
 
-  // ---- raw codes and scales of a step, prefetched into registers
-  struct Raw {
-    v4u k[P::kKeyEach];
-    uint32_t v[P::kValueEach][4][P::kUnit / 4];
-    float scale;
-    int page;                                          // of the scale's token
-  } raw;
-  const int pages = a.c.pages;
-  auto page_of = [&](int j) {
-    const int p = j < c1 ? a.table[(int64_t)b * a.width + (j >> log2p)] : -1;
-    return p >= 0 && p < pages ? p : -1;
+  // ---- raw codes and scales of the wavefront's next group, in registers.  Its page numbers of 64 steps are held a
+  // lane each; the group's first row is uniform.
+  v4u rawk[P::kKeyEach];
+  uint32_t rawv[P::kValueEach][4][P::kUnit / 4];
+  float raws;
+  int pages, present = 0;
+  auto find_pages = [&](int step) {
+    const int64_t j = c0 + (int64_t)kStep * (step + lane) + 16 * wave;
+    const int p = j < c1 ? a.table[b * a.width + (j >> log2p)] : -1;
+    pages = p < a.c.pages ? p : -1;
   };
-  auto row_of = [&](int j, int p) {
-    return (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
-  };
-  int kp[P::kKeyEach], vp[P::kValueEach], scp;         // pages of the next step's tokens
-  auto find = [&](int j0) {
+  const uint32_t koff = lane % 16 * P::kRow + lane / 16 % (P::kRow / 16) * 16;
+  auto load = [&](int step) {
+    if (step % 64 == 0) find_pages(step);
+    const int j = c0 + kStep * step + 16 * wave, p = __builtin_amdgcn_readlane(pages, step % 64);
+    present = p >= 0;
+    const int64_t row = (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
+    const uint8_t* kbase = a.c.kc + row * P::kRow;
+    const uint8_t* vbase = a.c.vc + row * P::kRow;
 #pragma unroll
-    for (int i = 0; i < P::kKeyEach; ++i) {
-      const int task = tid + i * kThreads;
-      kp[i] = page_of(j0 + task / P::kRow * 16 + task % 16);
-    }
-#pragma unroll
-    for (int i = 0; i < P::kValueEach; ++i) vp[i] = page_of(j0 + (tid + i * kThreads) / P::kUnits * 4);
-    scp = page_of(j0 + tid % kStep);
-  };
-  // a key task is the 16-byte piece task / 16 % (row / 16) of token task % 16 of a group of 16 tokens (row tasks a
-  // group), so that 16 lanes write neighbouring operands
-  auto load = [&](int j0) {
-#pragma unroll
-    for (int i = 0; i < P::kKeyEach; ++i) {
-      const int task = tid + i * kThreads;
-      if (P::kKeyTasks % kThreads == 0 || task < P::kKeyTasks) {
-        const int j = j0 + task / P::kRow * 16 + task % 16, piece = task / 16 % (P::kRow / 16);
-        raw.k[i] = *reinterpret_cast<const v4u*>(a.c.kc + row_of(j, kp[i]) * P::kRow + piece * 16);
-      }
-    }
+    for (int i = 0; i < P::kKeyEach; ++i) rawk[i] = *reinterpret_cast<const v4u*>(kbase + (koff + i * 64));
 #pragma unroll
     for (int i = 0; i < P::kValueEach; ++i) {
-      const int task = tid + i * kThreads;
-      if (P::kValueTasks % kThreads == 0 || task < P::kValueTasks) {
-        const int j = j0 + task / P::kUnits * 4, unit = task % P::kUnits;
-        const uint8_t* p = a.c.vc + row_of(j, vp[i]) * P::kRow + unit * P::kUnit;
+      const int task = (lane + 64 * i) % P::kTasks;
+      const uint32_t off = task / P::kUnits * 4 * P::kRow + task % P::kUnits * P::kUnit;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int w = 0; w < P::kUnit / 4; ++w)
-            raw.v[i][t][w] = reinterpret_cast<const uint32_t*>(p + t * P::kRow)[w];
-      }
+        for (int w = 0; w < P::kUnit / 4; ++w)
+          rawv[i][t][w] = reinterpret_cast<const uint32_t*>(vbase + (off + t * P::kRow))[w];
     }
-    if (tid < 2 * kStep) {
-      const int j = j0 + tid % kStep;
-      raw.page = j < c1 ? scp : -1;
-      raw.scale = (tid < kStep ? a.c.ks : a.c.vs)[row_of(j, scp)];
-    }
+    raws = (lane < 16 ? a.c.ks : a.c.vs)[row + lane % 16];
   };
-
-  find(c0);
-  load(c0);
-  find(c0 + kStep);
+  if (c1 > c0) load(0);
 
   // ---- the rotated queries as fp16, in the element order of the key operands
   float common;                                        // what a score's product is multiplied by, without the key's scale
@@ -212,6 +189,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
 #pragma unroll
       for (int e = 0; e < E; ++e) x[t][e] = 0.0f;
       if (i < s.n) load_row<E>(a.q.p + (s.first + i) * a.q.token + head * a.q.head + seg * E, a.bf16, x[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < kPass; ++t) {
       rotate_row<D>(x[t], seg);
 #pragma unroll
       for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[t][e]) < INFINITY ? fabsf(x[t][e]) : 0.0f);
@@ -222,20 +202,27 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, qtop[w]);
     // 2^e above the largest, so that the queries enter below 1
-    const uint32_t e = (__float_as_uint(top) >> 23) + 1u;
-    const float unit = __uint_as_float((e < 1u ? 1u : e > 253u ? 253u : e) << 23);
+    const uint32_t e2 = (__float_as_uint(top) >> 23) + 1u;
+    const float unit = __uint_as_float((e2 < 1u ? 1u : e2 > 253u ? 253u : e2) << 23);
     const float by = (a.scale < 0.0f ? -1.0f : 1.0f) / unit;
-    common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit;
+    // sm_scale, the rotation's 1 / sqrt(D), log2 e, the queries' unit and the codes' 2^-24
+    common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit * 0x1p24f;
 #pragma unroll
     for (int t = 0; t < kPass; ++t) {
       _Float16* dst = reinterpret_cast<_Float16*>(lds + (16 * t + r) * P::kQPitch);
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const int d = seg * E + i, e8 = d % 8;
-        // where element e8 of its unit stands in the operand
-        const int at = BITS == 8 ? e8 : 2 * (e8 % 4) + e8 / 4;
-        dst[d / 8 * 8 + at] = (_Float16)(x[t][i] * (by / key_factor<BITS>(e8)));
+        const int d = seg * E + i, e8 = E == 4 ? seg % 2 * 4 + i : i % 8;
+        const float factor = BITS == 4 && i % 2 ? 16.0f : 1.0f;
+        const _Float16 y = (_Float16)(x[t][i] * (by / factor));
+        sum += (float)y * factor;
+        dst[d / 8 * 8 + key_place<BITS>(e8)] = y;
       }
+      // what the codes' offset adds to the row's scores
+#pragma unroll
+      for (int k = 1; k < 16; k <<= 1) sum += __shfl_xor(sum, k);
+      if (seg == 0) qoffset[16 * t + r] = sum * (BITS == 4 ? -8.0f * 0x1p-24f : -128.0f * 0x1p-24f);
     }
     __syncthreads();
     const char* mine = lds + (32 * wave + col) * P::kQPitch;
@@ -243,58 +230,51 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
     for (int k = 0; k < P::kSteps; ++k) q[k] = *reinterpret_cast<const v8h*>(mine + (2 * k + hi) * 16);
     __syncthreads();
   }
+  v16f start;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) start[r] = qoffset[32 * wave + col];
 
   char* kbuf = lds;
   char* vbuf = lds + 2 * P::kBuffer;
-  float vmax = 0x1p-126f;                              // of the scales written so far (kept by wave 1)
-  auto decode = [&](int buf) {
+  auto decode = [&](int buf, int step) {
+    if (P::kPieces >= 64 || lane < P::kPieces) {
+      char* dst = kbuf + buf * P::kBuffer + ((wave / 2) * P::kSteps * 64 + wave % 2 * 16 + lane % 16) * 16;
 #pragma unroll
-    for (int i = 0; i < P::kKeyEach; ++i) {
-      const int task = tid + i * kThreads;
-      if (P::kKeyTasks % kThreads == 0 || task < P::kKeyTasks) {
-        const int j = task / P::kRow * 16 + task % 16, piece = task / 16 % (P::kRow / 16);
+      for (int i = 0; i < P::kKeyEach; ++i)
 #pragma unroll
         for (int n = 0; n < 16 / P::kUnit; ++n) {
-          const int unit = piece * (16 / P::kUnit) + n;
           uint32_t w[P::kUnit / 4];
 #pragma unroll
-          for (int z = 0; z < P::kUnit / 4; ++z) w[z] = raw.k[i][n * (P::kUnit / 4) + z];
-          *reinterpret_cast<v4u*>(kbuf + buf * P::kBuffer +
-                                  (((j / 32) * P::kSteps + unit / 2) * 64 + unit % 2 * 32 + j % 32) * 16) =
-              key_halves<BITS>(w);
+          for (int z = 0; z < P::kUnit / 4; ++z) w[z] = rawk[i][n * (P::kUnit / 4) + z];
+          // unit of the row; operand unit / 2, half-wave unit % 2
+          const int unit = (4 * i + lane / 16 % (P::kRow / 16)) * (16 / P::kUnit) + n;
+          *reinterpret_cast<v4u*>(dst + (unit / 2 * 64 + unit % 2 * 32) * 16) = key_halves<BITS>(w);
         }
-      }
     }
+    if (P::kTasks >= 64 || lane < P::kTasks) {
 #pragma unroll
-    for (int i = 0; i < P::kValueEach; ++i) {
-      const int task = tid + i * kThreads;
-      if (P::kValueTasks % kThreads == 0 || task < P::kValueTasks) {
-        const int j = task / P::kUnits * 4, unit = task % P::kUnits;
+      for (int i = 0; i < P::kValueEach; ++i) {
+        const int task = lane + 64 * i, quad = task / P::kUnits, unit = task % P::kUnits;
         uint32_t f01[8], f23[8];
-        value_halves<BITS>(raw.v[i][0], raw.v[i][1], f01);
-        value_halves<BITS>(raw.v[i][2], raw.v[i][3], f23);
-        // tokens 16 u + 8 half + 4 g + 0..3: step u, lanes of half-wave g, the operand's half `half`
-        const int u = j / 16, half = j / 8 % 2, g = j / 4 % 2;
+        value_halves<BITS>(rawv[i][0], rawv[i][1], f01);
+        value_halves<BITS>(rawv[i][2], rawv[i][3], f23);
+        // tokens 16 wave + 8 half + 4 g + 0..3: operand `wave`, lanes of half-wave g, its half `half`
+        const int half = quad / 2, g = quad % 2;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int t = e / P::kSpread, row = e % P::kSpread * P::kUnits + unit;
-          *reinterpret_cast<v2u*>(vbuf + buf * P::kBuffer + ((t * 4 + u) * 64 + g * 32 + row) * 16 + half * 8) =
+          *reinterpret_cast<v2u*>(vbuf + buf * P::kBuffer + ((t * kWaves + wave) * 64 + g * 32 + row) * 16 + half * 8) =
               (v2u){f01[e], f23[e]};
         }
       }
     }
-    if (wave == 0) {
-      kscale[buf][lane] = raw.scale * common;
-      if (lane % 16 == 0) absent[buf][lane / 16] = raw.page < 0;
-    } else if (wave == 1) {
-      const float v = raw.page < 0 ? 0.0f : raw.scale;
-      if (__any(v > vmax)) {
-        float most = wave_max64(fmaxf(v, vmax));
-        const uint32_t e = (__float_as_uint(most) >> 23) + 2u;   // room for the largest to double
-        vmax = __uint_as_float((e < 254u ? e : 254u) << 23);
-      }
-      vscale[buf][lane] = v * (1.0f / vmax);
-      if (lane == 0) vtop[buf] = vmax;
+    if (lane < 16) {
+      kscale[buf][16 * wave + lane] = raws * common;
+    } else if (lane < 32) {
+      const int j = c0 + kStep * step + 16 * wave + lane - 16;
+      vscale[buf][16 * wave + lane - 16] = j < c1 && present ? raws : 0.0f;
+    } else if (lane == 32) {
+      absent[buf][wave] = !present;
     }
   };
 
@@ -303,70 +283,69 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   const int end = myquery >= s.n ? 0 : a.causal ? s.kv - s.n + myquery + 1 : s.kv;
   const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + 32 * wave) + 1 : s.kv;   // the wavefront's first row
   v16f o[P::kTiles];
-  float base = kUnset, l = 0.0f, vnow = 0x1p-126f;
+  float base = kUnset, l = 0.0f;
 #pragma unroll
   for (int t = 0; t < P::kTiles; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
 
-  auto use = [&](int buf, int j0) {
-    const float v = vtop[buf];
-    if (v != vnow) {
-      const float by = vnow / v;
+  auto score = [&](int buf, int kt) {
+    v16f z = start;
 #pragma unroll
-      for (int t = 0; t < P::kTiles; ++t) o[t] *= by;
-      vnow = v;
+    for (int k = 0; k < P::kSteps; ++k) {
+      const v8h c = *reinterpret_cast<const v8h*>(kbuf + buf * P::kBuffer + ((kt * P::kSteps + k) * 64 + lane) * 16);
+      z = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[k], z, 0, 0, 0);
     }
-    const v4i gone = *reinterpret_cast<const v4i*>(absent[buf]);
-    const bool whole = __builtin_amdgcn_readfirstlane(j0 + kStep <= first && !(gone[0] | gone[1] | gone[2] | gone[3]));
-    v16f p[2];                                         // scores, then weights
-    auto score = [&]() {
+    return z;
+  };
+  // the 32 tokens from j on, whose products with the queries are z: weights, then outputs
+  auto use = [&](int buf, int kt, int j, v16f z) {
+    const v2u gone = *reinterpret_cast<const v2u*>(&absent[buf][2 * kt]);
+    const bool whole = __builtin_amdgcn_readfirstlane((j + 32 <= first) & !(gone[0] | gone[1]));
+    auto seen = [&](int r) { return (j + 8 * (r / 4) + 4 * hi + r % 4 < end) & !gone[r / 8]; };
+    float sum, top;
+    auto weigh = [&]() {                               // z becomes the weights times the values' scales
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
+      for (int r = 0; r < 16; r += 4) {
+        const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) p[kt][r] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < P::kSteps; ++k) {
-          const v8h c = *reinterpret_cast<const v8h*>(kbuf + buf * P::kBuffer + ((kt * P::kSteps + k) * 64 + lane) * 16);
-          p[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[k], p[kt], 0, 0, 0);
-        }
+        for (int i = 0; i < 4; ++i) z[r + i] = __builtin_amdgcn_exp2f(__fmaf_rn(z[r + i], ks[i], base));
       }
-    };
-    auto seen = [&](int kt, int r) {
-      return (j0 + 32 * kt + 8 * (r / 4) + 4 * hi + r % 4 < end) & !gone[2 * kt + r / 8];
-    };
-    auto weigh = [&]() {
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[kt][r + i] = __builtin_amdgcn_exp2f(__fmaf_rn(p[kt][r + i], ks[i], base));
-        }
       if (!whole) {
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) p[kt][r] = seen(kt, r) ? p[kt][r] : 0.0f;
+        for (int r = 0; r < 16; ++r) z[r] = seen(r) ? z[r] : 0.0f;
       }
-    };
-    score();
-    weigh();
-    float most = fmaxf(p[0][0], p[1][0]);
+      sum = 0.0f;
 #pragma unroll
-    for (int r = 1; r < 16; ++r) most = fmaxf(fmaxf(most, p[0][r]), p[1][r]);
-    if (__any(most > kMostWeight)) {                   // rare: form the scores again
-      score();
+      for (int r = 0; r < 16; r += 4) sum += (z[r] + z[r + 1]) + (z[r + 2] + z[r + 3]);
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
+        if (!whole) {                                  // a NaN scale that another row sees
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vs[i] = z[r + i] == 0.0f ? 0.0f : vs[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[r + i] *= vs[i];
+      }
+      top = z[0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
+    };
+    weigh();
+    if (__any((top > kMostWeight) | (sum > kMostSum) | (base == kUnset))) {   // raise the maximum (rare)
+      z = score(buf, kt);
       float best = kLowest;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+      for (int r = 0; r < 16; r += 4) {
+        const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
+        const v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) best = fmaxf(best, (whole | seen(kt, r + i)) ? p[kt][r + i] * ks[i] : kLowest);
+        for (int i = 0; i < 4; ++i) {
+          const float y = z[r + i] * ks[i] + __builtin_amdgcn_logf(fmaxf(vs[i], kLeastScale));
+          best = fmaxf(best, (whole | seen(r + i)) ? y : kLowest);
         }
+      }
       best = max32(best);
       const float next = fminf(base, kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base);
       l *= by;
@@ -375,44 +354,31 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
       base = next;
       weigh();
     }
-    v4u w[4];
+    l += sum;
+    v4u w[2];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
-        l += (p[kt][r] + p[kt][r + 1]) + (p[kt][r + 2] + p[kt][r + 3]);
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = p[kt][r + i] * vs[i];
-          if (!whole) x[i] = p[kt][r + i] == 0.0f ? 0.0f : x[i];   // a token that another row sees may have a NaN scale
-        }
-        w[2 * kt + r / 8][r % 8 / 2] = pack_f16x2_rn(x[0], x[1]);
-        w[2 * kt + r / 8][r % 8 / 2 + 1] = pack_f16x2_rn(x[2], x[3]);
-      }
+    for (int r = 0; r < 16; r += 2) w[r / 8][r % 8 / 2] = pack_f16x2_rn(z[r], z[r + 1]);
 #pragma unroll
     for (int t = 0; t < P::kTiles; ++t)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const v8h c = *reinterpret_cast<const v8h*>(vbuf + buf * P::kBuffer + ((t * 4 + u) * 64 + lane) * 16);
+      for (int u = 0; u < 2; ++u) {
+        const v8h c = *reinterpret_cast<const v8h*>(vbuf + buf * P::kBuffer + ((t * kWaves + 2 * kt + u) * 64 + lane) * 16);
         o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, __builtin_bit_cast(v8h, w[u]), o[t], 0, 0, 0);
       }
   };
 
   if (c1 > c0) {
-    decode(0);
-    load(c0 + kStep);
-    find(c0 + 2 * kStep);
+    decode(0, 0);
+    if (c0 + kStep < c1) load(1);
     __syncthreads();
-    int buf = 0;
-    for (int j = c0; j < c1; j += kStep, buf ^= 1) {
+    int buf = 0, step = 0;
+    for (int j = c0; j < c1; j += kStep, buf ^= 1, ++step) {
       if (j + kStep < c1) {
-        decode(buf ^ 1);
-        load(j + 2 * kStep);
-        find(j + 3 * kStep);
+        decode(buf ^ 1, step + 1);
+        if (j + 2 * kStep < c1) load(step + 2);
       }
-      use(buf, j);
+      use(buf, 0, j, score(buf, 0));
+      use(buf, 1, j + 32, score(buf, 1));
       __syncthreads();
     }
   }
@@ -424,27 +390,43 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   // element of (tile t, register r): row = 8 (r / 4) + 4 hi + r % 4, unit = row % kUnits, e = t * kSpread + row / kUnits
   auto unit_of = [&](int r) { return (8 * (r / 4) + 4 * hi + r % 4) % P::kUnits; };
   auto e_of = [&](int t, int r) { return t * P::kSpread + 8 * (r / 4) / P::kUnits; };
+  float x[P::kTiles * 16];
+  const float by = sp.splits > 1 ? 1.0f : l == 0.0f ? 0.0f : kv_rsqrt(D) / l;
+#pragma unroll
+  for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      x[16 * t + r] = l == 0.0f ? 0.0f : o[t][r] * (BITS == 4 && e_of(t, r) % 2 ? by * 0.0625f : by);
+  // the lane's units, 8 elements each
+  auto units = [&](auto&& store) {
+#pragma unroll
+    for (int n = 0; n < 2 * P::kTiles; ++n) {
+      float y[8];
+      int unit = 0;
+#pragma unroll
+      for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (r % 4 + 4 * (r / 4 % (P::kUnits / 8)) == n) {
+            y[e_of(t, r)] = x[16 * t + r];
+            unit = unit_of(r);
+          }
+      store(unit, y);
+    }
+  };
   if (sp.splits > 1) {
     const int64_t at = sp.row(h, tile, b * sp.splits + split, 32 * wave + col);
     float* dst = sp.o + at * D;
-#pragma unroll
-    for (int t = 0; t < P::kTiles; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        dst[8 * unit_of(r) + e_of(t, r)] = o[t][r] * (vnow * (BITS == 4 && e_of(t, r) % 2 ? 0.0625f : 1.0f));
+    units([&](int unit, float (&y)[8]) {
+      *reinterpret_cast<v4f*>(dst + 8 * unit) = (v4f){y[0], y[1], y[2], y[3]};
+      *reinterpret_cast<v4f*>(dst + 8 * unit + 4) = (v4f){y[4], y[5], y[6], y[7]};
+    });
     if (hi == 0) {
       sp.ml[2 * at] = base == kUnset ? kLowest : kWeightBits - base;
       sp.ml[2 * at + 1] = l;
     }
     return;
   }
-  const float by = l == 0.0f ? 0.0f : kv_rsqrt(D) * vnow / l;
-  float x[P::kTiles * 16];
-#pragma unroll
-  for (int t = 0; t < P::kTiles; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      x[16 * t + r] = l == 0.0f ? 0.0f : o[t][r] * (BITS == 4 && e_of(t, r) % 2 ? by * 0.0625f : by);
 #pragma unroll
   for (int k = 1; k < P::kTiles * 16; k <<= 1)
 #pragma unroll
@@ -462,23 +444,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   }
   const int head = h * a.group + myrow - myquery * a.group;
   uint16_t* dst = a.o + ((s.first + myquery) * a.q_heads + head) * D;
-  // registers of one unit: its 8 elements are (t, r) with e = 0..7
-#pragma unroll
-  for (int n = 0; n < 2 * P::kTiles; ++n) {            // units of this lane
-    float y[8];
-    int unit = 0;
-#pragma unroll
-    for (int t = 0; t < P::kTiles; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int nr = r % 4 + 4 * (r / 4 % (P::kUnits / 8));
-        if (nr == n) {
-          y[e_of(t, r)] = x[16 * t + r];
-          unit = unit_of(r);
-        }
-      }
-    store_row<8>(dst + 8 * unit, a.bf16, y);
-  }
+  units([&](int unit, float (&y)[8]) { store_row<8>(dst + 8 * unit, a.bf16, y); });
 }
 
 template <int D, int BITS>

@@ -199,21 +199,18 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* 
     if constexpr (L > 4) stage_i16<2>(v, lane);
     if (r >= rows) continue;
     v4u* dst = reinterpret_cast<v4u*>(out + r * D + lane * 32);
+    // element e of the lane is in half e / gap % 2 of v[e / (2 gap) * gap + e % gap]
+    uint32_t w[16];
+    auto at = [&](int e) { return __fmul_rn((float)v[e / (2 * gap) * gap + e % gap][e / gap % 2], f); };
+    if (bf16) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v4u w;
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2_rn(at(2 * i), at(2 * i + 1));
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int i = 8 * j + 2 * e + z;   // element of the lane
-          x[z] = __fmul_rn((float)v[i / (2 * gap) * gap + i % gap][i / gap % 2], f);
-        }
-        w[e] = pack16(x[0], x[1], bf16);
-      }
-      dst[j] = w;
+      for (int i = 0; i < 16; ++i) w[i] = pack_f16x2_rn(at(2 * i), at(2 * i + 1));
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[j] = (v4u){w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
   }
 }
 
