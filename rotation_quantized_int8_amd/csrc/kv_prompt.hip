@@ -15,10 +15,10 @@
 // operand layout of W^T up to an order of the tokens that C_v^T is stored in.
 // The rotated queries are rounded to fp16 after a power of two common to the
 // workgroup; it, sm_scale and log2 e are multiplied into the keys' scales, so
-// a weight is exp2(fma(S, scale_j, base_row)): one operation, its exponential
-// and the product with the value's scale, against 2 D / 32 matrix operations
-// of 8 passes for 32 elements of S.  The running maximum is raised only when
-// a weight passes 2^15 (they start at 2^8 for the largest).
+// a weight is exp2(fma(S, scale_j, base_row)): one operation, its exponential,
+// its share of the sum and the product with the value's scale.  The running
+// maximum is raised only when a weight could pass 2^15 (they start at 2^8 for
+// the largest).
 
 #include "kv_core.hpp"
 #include "launch.hpp"
@@ -28,6 +28,7 @@ namespace {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
@@ -45,40 +46,12 @@ __device__ __forceinline__ uint32_t less(uint32_t x, float by) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) - off);
 }
 
-// Eight codes as fp16 operands of the keys: the subnormals (c + 8) 2^-24 (with
-// 8 bits (c + 128) 2^-24), made by a mask and an exclusive or; what the offset
-// adds to a score is the row's own constant, taken off by the accumulator's
-// start.  4 bits: elements 0 4 1 5 2 6 3 7, the odd ones times 16; 8 bits: in
-// order.
+// The eight elements of unit (8 codes) a next to those of unit b, as half
+// pairs (4 bits: the odd elements times 16): 1024 + (c + 8) and the like by a
+// mask and an exclusive or, less 1032.  Two units of one token make a key
+// operand, one unit of two tokens a value operand.
 template <int BITS>
-__device__ __forceinline__ v4u key_halves(const uint32_t* w) {
-  v4u f;
-  if constexpr (BITS == 4) {
-    const uint32_t x = w[0], y = x >> 8;
-    f[0] = (x & 0x000F000Fu) ^ 0x00080008u;
-    f[1] = (x & 0x00F000F0u) ^ 0x00800080u;
-    f[2] = (y & 0x000F000Fu) ^ 0x00080008u;
-    f[3] = (y & 0x00F000F0u) ^ 0x00800080u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = __builtin_amdgcn_perm(0, w[i / 2], i % 2 ? 0x0C030C02u : 0x0C010C00u) ^ 0x00800080u;
-  }
-  return f;
-}
-// Where element e of its unit of 8 stands in a key operand, and the factor
-// that its code enters with.
-template <int BITS>
-__device__ __forceinline__ constexpr int key_place(int e) { return BITS == 8 ? e : 2 * (e % 4) + e / 4; }
-template <int BITS>
-__device__ __forceinline__ constexpr float key_factor(int e) { return BITS == 4 && e % 2 ? 16.0f : 1.0f; }
-
-// Element i of the unit for two tokens a and b, as a half pair (4 bits: the
-// odd elements times 16).  1024 + (c + 8) and the like, less its offset: the
-// sum of the weights would have to be formed per wavefront, where this
-// subtraction is shared by all four.
-template <int BITS>
-__device__ __forceinline__ void value_halves(const uint32_t* a, const uint32_t* b, uint32_t (&f)[8]) {
+__device__ __forceinline__ void halves(const uint32_t* a, const uint32_t* b, uint32_t (&f)[8]) {
   if constexpr (BITS == 4) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
@@ -109,18 +82,17 @@ struct Prompt {
   static constexpr int kKeyEach = kPieces < 64 ? 1 : kPieces / 64;
   static constexpr int kValueEach = kTasks < 64 ? 1 : kTasks / 64;
   static constexpr int kBuffer = kStep * D * 2;        // bytes of a step's keys, and of its values
-  static constexpr int kQPitch = D * 2 + 16;
-  static constexpr int kBytes = 4 * kBuffer > kRows * kQPitch ? 4 * kBuffer : kRows * kQPitch;
+  static constexpr int kBytes = 4 * kBuffer;
 };
 
 template <int D, int BITS>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(KvAttn a, KvSplit sp) {
   using P = Prompt<D, BITS>;
-  constexpr int E = D / 16;
-  extern __shared__ __align__(16) char lds[];          // keys [2], values [2]; first the queries
+  extern __shared__ __align__(16) char lds[];          // keys [2], values [2]
   __shared__ __align__(16) float kscale[2][kStep], vscale[2][kStep];
   __shared__ __align__(16) int absent[2][kWaves];
-  __shared__ float qtop[kWaves], qoffset[kRows];
+  __shared__ __align__(16) float vtop[2][kWaves];      // largest value scale of each group
+  __shared__ float qtop[kWaves];
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 32, hi = lane / 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -175,64 +147,82 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   };
   if (c1 > c0) load(0);
 
-  // ---- the rotated queries as fp16, in the element order of the key operands
+  // ---- the rotated queries as fp16.  The rotation is a matrix product too: W (+-1, exact) times the rows, whose
+  // result layout is, in pairs of registers, the operand layout of the scores: lane (column = row, hi), step k, holds
+  // elements 4 hi .. 4 hi + 3 of units 2 k and 2 k + 1, alternating.
+  const int myrow = tile * kRows + 32 * wave + col, myquery = kv_query_of(a, myrow);
   float common;                                        // what a score's product is multiplied by, without the key's scale
   v8h q[P::kSteps];
   {
-    constexpr int kPass = kRows / 16;
-    float x[kPass][E];
-    const int r = tid / 16, seg = tid % 16;
+    v16f x[P::kTiles];
+#pragma unroll
+    for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[t][r] = 0.0f;
+    // W's operand of tile t, step k: the sign of element (m, d), m = 32 t + col, d = 16 k + 8 hi + j, is the parity of
+    // m & d = that of (col & 7) & j, of (col >> 3 & hi & 1), of (col >> 4) & k & 1 and of t & (k >> 1)
+    const uint32_t one = a.bf16 ? 0x3F80u : 0x3C00u;
+    v4u w[2][2];                                       // by k & 1, and negated
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = (uint32_t)__builtin_popcount(col & 7 & 2 * i), up = (uint32_t)__builtin_popcount(col & 7 & (2 * i + 1));
+      const uint32_t pair = one * 0x00010001u ^ (lo & 1) << 15 ^ (up & 1) << 31;
+      w[0][0][i] = pair ^ (col >> 3 & hi & 1 ? 0x80008000u : 0u);
+      w[1][0][i] = w[0][0][i] ^ (col >> 4 ? 0x80008000u : 0u);
+      w[0][1][i] = w[0][0][i] ^ 0x80008000u;
+      w[1][1][i] = w[1][0][i] ^ 0x80008000u;
+    }
+    const bool in = myquery < s.n;
+    const uint16_t* src = a.q.p + (in ? (s.first + myquery) * a.q.token + (h * a.group + myrow - myquery * a.group) * a.q.head : 0);
+    v4u raw[P::kSteps];
+#pragma unroll
+    for (int k = 0; k < P::kSteps; ++k) {
+      raw[k] = *reinterpret_cast<const v4u*>(src + 8 * (2 * k + hi));
+      if (!in) raw[k] = (v4u){0, 0, 0, 0};
+    }
+    if (a.bf16) {
+#pragma unroll
+      for (int k = 0; k < P::kSteps; ++k)
+#pragma unroll
+        for (int t = 0; t < P::kTiles; ++t)
+          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, w[k & 1][__builtin_popcount(t & k >> 1) & 1]),
+                                                         __builtin_bit_cast(v8b, raw[k]), x[t], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < P::kSteps; ++k)
+#pragma unroll
+        for (int t = 0; t < P::kTiles; ++t)
+          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, w[k & 1][__builtin_popcount(t & k >> 1) & 1]),
+                                                        __builtin_bit_cast(v8h, raw[k]), x[t], 0, 0, 0);
+    }
     float top = 0.0f;
 #pragma unroll
-    for (int t = 0; t < kPass; ++t) {
-      const int row = tile * kRows + 16 * t + r, i = kv_query_of(a, row), head = h * a.group + row - i * a.group;
+    for (int t = 0; t < P::kTiles; ++t)
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[t][e] = 0.0f;
-      if (i < s.n) load_row<E>(a.q.p + (s.first + i) * a.q.token + head * a.q.head + seg * E, a.bf16, x[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < kPass; ++t) {
-      rotate_row<D>(x[t], seg);
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[t][e]) < INFINITY ? fabsf(x[t][e]) : 0.0f);
-    }
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[t][r]));
+    top = top < INFINITY ? top : 0.0f;                 // (a row with an infinity or a NaN has no finite element)
     top = wave_max64(top);
     if (lane == 0) qtop[wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, qtop[w]);
+    for (int v = 0; v < kWaves; ++v) top = fmaxf(top, qtop[v]);
     // 2^e above the largest, so that the queries enter below 1
     const uint32_t e2 = (__float_as_uint(top) >> 23) + 1u;
     const float unit = __uint_as_float((e2 < 1u ? 1u : e2 > 253u ? 253u : e2) << 23);
-    const float by = (a.scale < 0.0f ? -1.0f : 1.0f) / unit;
-    // sm_scale, the rotation's 1 / sqrt(D), log2 e, the queries' unit and the codes' 2^-24
-    common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit * 0x1p24f;
+    const float by = (a.scale < 0.0f ? -1.0f : 1.0f) / unit, odd = BITS == 4 ? by * 0.0625f : by;
+    // sm_scale, the rotation's 1 / sqrt(D), log2 e and the queries' unit
+    common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit;
 #pragma unroll
-    for (int t = 0; t < kPass; ++t) {
-      _Float16* dst = reinterpret_cast<_Float16*>(lds + (16 * t + r) * P::kQPitch);
-      float sum = 0.0f;
+    for (int k = 0; k < P::kSteps; ++k) {
+      v4u y;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int d = seg * E + i, e8 = E == 4 ? seg % 2 * 4 + i : i % 8;
-        const float factor = BITS == 4 && i % 2 ? 16.0f : 1.0f;
-        const _Float16 y = (_Float16)(x[t][i] * (by / factor));
-        sum += (float)y * factor;
-        dst[d / 8 * 8 + key_place<BITS>(e8)] = y;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * (k % 2) + i;
+        y[i] = pack_f16x2_rn(x[k / 2][r] * (i % 2 ? odd : by), x[k / 2][r + 4] * (i % 2 ? odd : by));
       }
-      // what the codes' offset adds to the row's scores
-#pragma unroll
-      for (int k = 1; k < 16; k <<= 1) sum += __shfl_xor(sum, k);
-      if (seg == 0) qoffset[16 * t + r] = sum * (BITS == 4 ? -8.0f * 0x1p-24f : -128.0f * 0x1p-24f);
+      q[k] = __builtin_bit_cast(v8h, y);
     }
-    __syncthreads();
-    const char* mine = lds + (32 * wave + col) * P::kQPitch;
-#pragma unroll
-    for (int k = 0; k < P::kSteps; ++k) q[k] = *reinterpret_cast<const v8h*>(mine + (2 * k + hi) * 16);
-    __syncthreads();
   }
-  v16f start;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) start[r] = qoffset[32 * wave + col];
 
   char* kbuf = lds;
   char* vbuf = lds + 2 * P::kBuffer;
@@ -242,13 +232,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
 #pragma unroll
       for (int i = 0; i < P::kKeyEach; ++i)
 #pragma unroll
-        for (int n = 0; n < 16 / P::kUnit; ++n) {
-          uint32_t w[P::kUnit / 4];
+        for (int n = 0; n < 16 / P::kUnit; n += 2) {
+          uint32_t w[16 / 4], f[8];
 #pragma unroll
-          for (int z = 0; z < P::kUnit / 4; ++z) w[z] = rawk[i][n * (P::kUnit / 4) + z];
-          // unit of the row; operand unit / 2, half-wave unit % 2
-          const int unit = (4 * i + lane / 16 % (P::kRow / 16)) * (16 / P::kUnit) + n;
-          *reinterpret_cast<v4u*>(dst + (unit / 2 * 64 + unit % 2 * 32) * 16) = key_halves<BITS>(w);
+          for (int z = 0; z < 4; ++z) w[z] = rawk[i][z];
+          halves<BITS>(w + n * (P::kUnit / 4), w + (n + 1) * (P::kUnit / 4), f);
+          const int step2 = ((4 * i + lane / 16 % (P::kRow / 16)) * (16 / P::kUnit) + n) / 2;
+          *reinterpret_cast<v4u*>(dst + step2 * 1024) = (v4u){f[0], f[1], f[2], f[3]};
+          *reinterpret_cast<v4u*>(dst + step2 * 1024 + 512) = (v4u){f[4], f[5], f[6], f[7]};
         }
     }
     if (P::kTasks >= 64 || lane < P::kTasks) {
@@ -256,8 +247,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
       for (int i = 0; i < P::kValueEach; ++i) {
         const int task = lane + 64 * i, quad = task / P::kUnits, unit = task % P::kUnits;
         uint32_t f01[8], f23[8];
-        value_halves<BITS>(rawv[i][0], rawv[i][1], f01);
-        value_halves<BITS>(rawv[i][2], rawv[i][3], f23);
+        halves<BITS>(rawv[i][0], rawv[i][1], f01);
+        halves<BITS>(rawv[i][2], rawv[i][3], f23);
         // tokens 16 wave + 8 half + 4 g + 0..3: operand `wave`, lanes of half-wave g, its half `half`
         const int half = quad / 2, g = quad % 2;
 #pragma unroll
@@ -268,18 +259,20 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
         }
       }
     }
+    const int j = c0 + kStep * step + 16 * wave + lane % 16;
+    const float v = (j < c1) & (present != 0) ? raws : 0.0f, most = warp_max16(v);
     if (lane < 16) {
       kscale[buf][16 * wave + lane] = raws * common;
     } else if (lane < 32) {
-      const int j = c0 + kStep * step + 16 * wave + lane - 16;
-      vscale[buf][16 * wave + lane - 16] = j < c1 && present ? raws : 0.0f;
-    } else if (lane == 32) {
-      absent[buf][wave] = !present;
+      vscale[buf][16 * wave + lane - 16] = v;
+      if (lane == 16) {
+        vtop[buf][wave] = most;
+        absent[buf][wave] = !present;
+      }
     }
   };
 
   // ---- the steps
-  const int myrow = tile * kRows + 32 * wave + col, myquery = kv_query_of(a, myrow);
   const int end = myquery >= s.n ? 0 : a.causal ? s.kv - s.n + myquery + 1 : s.kv;
   const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + 32 * wave) + 1 : s.kv;   // the wavefront's first row
   v16f o[P::kTiles];
@@ -290,7 +283,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
     for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
 
   auto score = [&](int buf, int kt) {
-    v16f z = start;
+    v16f z;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z[r] = 0.0f;
 #pragma unroll
     for (int k = 0; k < P::kSteps; ++k) {
       const v8h c = *reinterpret_cast<const v8h*>(kbuf + buf * P::kBuffer + ((kt * P::kSteps + k) * 64 + lane) * 16);
@@ -303,7 +298,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
     const v2u gone = *reinterpret_cast<const v2u*>(&absent[buf][2 * kt]);
     const bool whole = __builtin_amdgcn_readfirstlane((j + 32 <= first) & !(gone[0] | gone[1]));
     auto seen = [&](int r) { return (j + 8 * (r / 4) + 4 * hi + r % 4 < end) & !gone[r / 8]; };
-    float sum, top;
+    const float* vmost = &vtop[buf][2 * kt];
+    float sum;
     auto weigh = [&]() {                               // z becomes the weights times the values' scales
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
@@ -328,12 +324,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[r + i] *= vs[i];
       }
-      top = z[0];
-#pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
     };
     weigh();
-    if (__any((top > kMostWeight) | (sum > kMostSum) | (base == kUnset))) {   // raise the maximum (rare)
+    // raise the maximum (rare) where a weight might pass 2^15; a row that has seen no token has an infinite sum
+    if (__any((sum * fmaxf(vmost[0], vmost[1]) > kMostWeight) | (sum > kMostSum))) {
       z = score(buf, kt);
       float best = kLowest;
 #pragma unroll
