@@ -583,14 +583,15 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 // another); the four segments of a wavefront are summed by lane swaps, the
 // wavefronts through LDS, and the row is rotated back.  What counts is the
 // chain of loads, not the bytes: 4, 16 or 64 segments, so that a segment has
-// few splits.
+// few splits; one where the rows alone fill the card.
 template <int D, int SEGS>
 __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn a, KvSplit sp) {
-  constexpr int E = D / 16, WAVES = SEGS / 4;          // wavefronts of a row
+  constexpr int E = D / 16, WAVES = SEGS < 4 ? 1 : SEGS / 4;   // wavefronts of a row
+  constexpr int PER = SEGS == 64 ? 1 : 16 / SEGS;      // rows of a workgroup
   __shared__ __align__(16) float part[WAVES][D];
   __shared__ float stat[WAVES][2];
   const int sub = threadIdx.x / 16 % SEGS, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
-  const int row = SEGS == 4 ? blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;   // of the sequence's with this key head
+  const int row = blockIdx.x * PER + threadIdx.x / 16 / SEGS % PER;   // of the sequence's with this key head
   const int tile = row / sp.rows, rr = row - tile * sp.rows;
   if (tile >= sp.tiles || rr >= sp.kept) return;
   int first = b * sp.splits, n = sp.splits, chunk = sp.chunk;
@@ -655,14 +656,19 @@ __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn
   }
 #pragma unroll
   for (int k = 1; k < 16; k <<= 1) l += __shfl_xor(l, k);
-  float top = max16_32(m), by = __builtin_amdgcn_exp2f(m - top), sum = sum16_32(l * by);
+  float sum = l;
+  if constexpr (SEGS > 1) {
+    const float top = max16_32(m), by = __builtin_amdgcn_exp2f(m - top);
+    sum = sum16_32(l * by);
+    m = top;
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = sum16_32(x[e] * by);
+    for (int e = 0; e < E; ++e) x[e] = sum16_32(x[e] * by);
+  }
   if constexpr (WAVES > 1) {
     const int wave = threadIdx.x / 64;
     if (sub % 4 == 0) {
       if (seg == 0) {
-        stat[wave][0] = top;
+        stat[wave][0] = m;
         stat[wave][1] = sum;
       }
 #pragma unroll
@@ -672,13 +678,13 @@ __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn
     __syncthreads();
     if (wave) return;
 #pragma unroll
-    for (int v = 0; v < WAVES; ++v) top = fmaxf(top, stat[v][0]);
+    for (int v = 0; v < WAVES; ++v) m = fmaxf(m, stat[v][0]);
     sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.0f;
 #pragma unroll
     for (int v = 0; v < WAVES; v += 4) {
-      by = __builtin_amdgcn_exp2f(stat[v + sub][0] - top);
+      const float by = __builtin_amdgcn_exp2f(stat[v + sub][0] - m);
       sum += stat[v + sub][1] * by;
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
@@ -767,7 +773,9 @@ namespace {
 template <int D>
 hipError_t join(const KvAttn& a, const KvSplit& sp, hipStream_t stream) {
   const unsigned rows = (unsigned)a.max_q * a.group;
-  if (sp.splits <= 4) kv_join_kernel<D, 4><<<dim3((rows + 3) / 4, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
+  const int64_t all = (int64_t)rows * a.c.heads * a.batch;
+  if (sp.splits <= 16 && all >= 16384) kv_join_kernel<D, 1><<<dim3((rows + 15) / 16, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
+  else if (sp.splits <= 4) kv_join_kernel<D, 4><<<dim3((rows + 3) / 4, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
   else if (sp.splits <= 32) kv_join_kernel<D, 16><<<dim3(rows, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
   else kv_join_kernel<D, 64><<<dim3(rows, a.c.heads, a.batch), 1024, 0, stream>>>(a, sp);
   return hipGetLastError();
