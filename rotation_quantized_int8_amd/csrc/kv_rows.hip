@@ -1,10 +1,11 @@
 // Writing rows into the rotated, quantised key/value cache and reading them
 // back (convrot_kv_append, convrot_kv_read).
 //
-// A row of D elements is held by D / 32 neighbouring lanes, 32 contiguous
-// elements each: of the log2 D butterfly stages of the rotation, five run in
-// a lane's registers and the last one to three between lanes, by DPP
-// permutations inside a 16-lane row (no LDS).
+// A row of D elements is held by L = D / 32 neighbouring lanes, four chunks of
+// 8 elements each, chunk j L + lane: the lanes of a row touch neighbouring
+// 16 bytes on its 16-bit side.  Of the log2 D butterfly stages of the
+// rotation, five run in a lane's registers and the other one to three between
+// lanes, by DPP permutations inside a 16-lane row (no LDS).
 //
 // Both kernels are bound by HBM: a row costs 2 D bytes on its 16-bit side and
 // D bits / 8 + 4 in the cache, against about log2 D additions an element.
@@ -98,9 +99,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, Kv
     if (slot >= c.slots) slot = -1;
     v4u raw[4] = {};
     if (slot >= 0) {
-      const v4u* src = reinterpret_cast<const v4u*>(in.p + t * in.token + h * in.head + lane * 32);
+      const v4u* src = reinterpret_cast<const v4u*>(in.p + t * in.token + h * in.head) + lane;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) raw[j] = src[j];
+      for (int j = 0; j < 4; ++j) raw[j] = src[j * L];
     }
     double v[32];
 #pragma unroll
@@ -136,10 +137,12 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, Kv
     codes32<BITS>(u, finite ? s : 0.0f, w);
     if (slot < 0) continue;
     const int64_t row = ((slot >> c.page_log2) * c.heads + h << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
-    v4u* dst = reinterpret_cast<v4u*>(codes + row * (D * BITS / 8) + lane * (4 * BITS));
+    uint8_t* dst = codes + row * (D * BITS / 8) + lane * BITS;   // 8 codes are BITS bytes
 #pragma unroll
-    for (int j = 0; j < BITS / 4; ++j)
-      dst[j] = finite ? (v4u){w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]} : (v4u){0, 0, 0, 0};
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(dst + j * L * BITS) = finite ? w[j] : 0;
+      else *reinterpret_cast<v2u*>(dst + j * L * BITS) = finite ? (v2u){w[2 * j], w[2 * j + 1]} : (v2u){0, 0};
+    }
     if (lane == 0) scales[row] = finite ? __fmul_rn(s, kv_rsqrt(D)) : __uint_as_float(0x7FC00000u);
   }
 }
@@ -165,9 +168,16 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* 
     float f = 0.0f;
     if (slot >= 0) {
       const int64_t row = ((slot >> c.page_log2) * c.heads + h << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
-      const v4u* src = reinterpret_cast<const v4u*>(codes + row * (D * BITS / 8) + lane * (4 * BITS));
+      const uint8_t* src = codes + row * (D * BITS / 8) + lane * BITS;   // 8 codes are BITS bytes
 #pragma unroll
-      for (int j = 0; j < BITS / 4; ++j) raw[j] = src[j];
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (BITS == 4) {
+          raw[0][j] = *reinterpret_cast<const uint32_t*>(src + j * L * BITS);
+        } else {
+          const v2u y = *reinterpret_cast<const v2u*>(src + j * L * BITS);
+          raw[j / 2][2 * j % 4] = y[0], raw[j / 2][2 * j % 4 + 1] = y[1];
+        }
+      }
       f = __fmul_rn(scales[row], kv_rsqrt(D));
     }
     // v[i] holds two elements `gap` apart
@@ -198,7 +208,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* 
     if constexpr (L > 2) stage_i16<1>(v, lane);
     if constexpr (L > 4) stage_i16<2>(v, lane);
     if (r >= rows) continue;
-    v4u* dst = reinterpret_cast<v4u*>(out + r * D + lane * 32);
+    v4u* dst = reinterpret_cast<v4u*>(out + r * D) + lane;
     // element e of the lane is in half e / gap % 2 of v[e / (2 gap) * gap + e % gap]
     uint32_t w[16];
     auto at = [&](int e) { return __fmul_rn((float)v[e / (2 * gap) * gap + e % gap][e / gap % 2], f); };
@@ -210,7 +220,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* 
       for (int i = 0; i < 16; ++i) w[i] = pack_f16x2_rn(at(2 * i), at(2 * i + 1));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dst[j] = (v4u){w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+    for (int j = 0; j < 4; ++j) dst[j * L] = (v4u){w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
   }
 }
 
