@@ -10,6 +10,24 @@ typedef short v2s __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
+// Division by a number the host knows: n / d = n * mul >> shift for n < 2^31.
+// With l = ceil(log2 d), shift = 31 + l and mul = floor(2^shift / d) + 1 (below
+// 2^32), the product overshoots 2^shift n / d by at most n < 2^31 <= 2^shift /
+// d, so the quotient is exact.
+struct KvDivider {
+  uint32_t mul;
+  int shift;
+};
+inline KvDivider kv_divider(uint32_t d) {
+  KvDivider v{0, 31};
+  while ((1ull << (v.shift - 31)) < d) ++v.shift;
+  v.mul = (uint32_t)((1ull << v.shift) / d + 1);
+  return v;
+}
+__device__ __forceinline__ uint32_t kv_divide(uint32_t n, KvDivider d) {
+  return (uint32_t)((uint64_t)n * d.mul >> d.shift);
+}
+
 struct KvCache {
   uint8_t* kc;      // codes [pages, heads, page, D bits / 8]
   float* ks;        // scales [pages, heads, page]
@@ -38,28 +56,15 @@ struct KvAttn {
   int64_t T;
   int64_t width;
   int batch, q_heads, group;
-  uint32_t group_mul;     // row / group = row * group_mul >> group_shift, for row < 2^31
-  int group_shift;
+  KvDivider by_group;
   int each_q;
   int max_q, max_kv;
   float scale;            // sm_scale
   int causal, bf16;
 };
 
-// The query that a row (query, head in group) belongs to.  With l = ceil(log2
-// group), group_shift = 31 + l and group_mul = floor(2^group_shift / group) + 1
-// (below 2^32), the product overshoots 2^group_shift row / group by at most
-// row < 2^31 <= 2^group_shift / group, so the quotient is exact.
-__device__ __forceinline__ int kv_query_of(const KvAttn& a, int row) {
-  return (int)((uint64_t)(uint32_t)row * a.group_mul >> a.group_shift);
-}
-
-// The multiplier and shift of such a division, 1 <= d < 2^31.
-inline void kv_divider(uint32_t d, uint32_t* mul, int* shift) {
-  *shift = 31;
-  while ((1ull << (*shift - 31)) < d) ++*shift;
-  *mul = (uint32_t)((1ull << *shift) / d + 1);
-}
+// The query that a row (query, head in group) belongs to.
+__device__ __forceinline__ int kv_query_of(const KvAttn& a, int row) { return (int)kv_divide((uint32_t)row, a.by_group); }
 
 hipError_t launch_kv_append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16, const int64_t* slots,
                             int64_t T, hipStream_t stream);

@@ -82,7 +82,7 @@ KvAttn attention_args(const convrot_kv_cache* c, int64_t T, int64_t q_heads, int
   a.batch = (int)batch;
   a.q_heads = (int)q_heads;
   a.group = (int)(q_heads / c->heads);
-  kv_divider((uint32_t)a.group, &a.group_mul, &a.group_shift);
+  a.by_group = kv_divider((uint32_t)a.group);
   a.max_q = (int)(max_q < T ? max_q : T);
   a.max_kv = (int)max_kv;
   return a;

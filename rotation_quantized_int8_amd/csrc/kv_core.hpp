@@ -19,8 +19,7 @@ struct KvSplit {
   int rows, tiles, kept;     // kept: rows of a tile that can be valid
   int splits, chunk;
   int balance, units;
-  uint32_t balance_mul;      // division by `balance`, as KvAttn's by the group
-  int balance_shift;
+  KvDivider by_balance;
   float* o;                  // [.., D], unnormalised, rotated basis
   float* ml;                 // [.., 2]: maximum (log2 units) and sum
   __device__ __forceinline__ int64_t row(int h, int tile, int unit, int r) const {
@@ -126,8 +125,7 @@ __device__ __forceinline__ KvUnits kv_units_of(const KvAttn& a, const KvSplit& s
     mine += blocks[k];
   }
   const uint32_t total = __builtin_amdgcn_readlane(wave_scan(mine), 63), want = (uint32_t)sp.balance;
-  // ceil(total / want): at most 2^31 blocks, the multiplier as for the group
-  uint32_t chunk = (uint32_t)((uint64_t)(total + want - 1) * sp.balance_mul >> sp.balance_shift);
+  uint32_t chunk = kv_divide(total + want - 1, sp.by_balance);   // (2^31 blocks of 128 tokens do not fit the card)
   chunk = chunk < 2 ? 2 : chunk;
   for (;;) {
     // ceil(blocks / chunk) in fp32 (blocks < 2^23): the quotient by the reciprocal is off by one at most

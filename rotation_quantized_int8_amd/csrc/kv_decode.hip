@@ -751,7 +751,7 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   if (a.batch <= 256) {
     const int64_t want = slots / heads;
     s.balance = (int)(want < a.batch ? a.batch : want);
-    kv_divider((uint32_t)s.balance, &s.balance_mul, &s.balance_shift);
+    s.by_balance = kv_divider((uint32_t)s.balance);
     s.units = 2 * (int64_t)a.batch <= s.balance ? s.balance : s.balance + a.batch;
     const int64_t most = (int64_t)a.batch * ((a.max_kv + 255) / 256);   // chunks have 256 tokens at least
     if (s.units > most) s.units = (int)most;

@@ -85,17 +85,17 @@ __device__ __forceinline__ void codes32(const float (&u)[32], float s, uint32_t 
 // of them has at most 48 significand bits).
 template <int D, int BITS, bool BF16>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, KvRows vr,
-                                                        const int64_t* __restrict__ slots, int rows) {
+                                                        const int64_t* __restrict__ slots, int rows, KvDivider by_heads) {
   constexpr int L = D / 32;
   const KvRows in = blockIdx.y ? vr : kr;
   uint8_t* codes = blockIdx.y ? c.vc : c.kc;
   float* scales = blockIdx.y ? c.vs : c.ks;
   const int lane = threadIdx.x % L;
   const int per = 256 / L;
-  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
-    const int64_t r = base + threadIdx.x / L;
-    const int t = (int)(r / c.heads), h = (int)(r - (int64_t)t * c.heads);
-    int64_t slot = r < rows ? slots[t] : -1;
+  for (uint32_t base = blockIdx.x * per; base < (uint32_t)rows; base += gridDim.x * per) {
+    const uint32_t r = base + threadIdx.x / L;          // below 2^31 + 2^21
+    const int t = (int)kv_divide(r, by_heads), h = (int)(r - (uint32_t)t * c.heads);
+    int64_t slot = r < (uint32_t)rows ? slots[t] : -1;
     if (slot >= c.slots) slot = -1;
     v4u raw[4] = {};
     if (slot >= 0) {
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, Kv
 // 32512, so it is exact.
 template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* __restrict__ slots, int rows,
-                                                      uint16_t* ko, uint16_t* vo, int bf16) {
+                                                      KvDivider by_heads, uint16_t* ko, uint16_t* vo, int bf16) {
   constexpr int L = D / 32;
   const bool second = blockIdx.y || !ko;
   const uint8_t* codes = second ? c.vc : c.kc;
@@ -159,10 +159,10 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* 
   uint16_t* out = second ? vo : ko;
   const int lane = threadIdx.x % L;
   const int per = 256 / L;
-  for (int64_t base = (int64_t)blockIdx.x * per; base < rows; base += (int64_t)gridDim.x * per) {
-    const int64_t r = base + threadIdx.x / L;
-    const int t = (int)(r / c.heads), h = (int)(r - (int64_t)t * c.heads);
-    int64_t slot = r < rows ? slots[t] : -1;
+  for (uint32_t base = blockIdx.x * per; base < (uint32_t)rows; base += gridDim.x * per) {
+    const uint32_t r = base + threadIdx.x / L;          // below 2^31 + 2^21
+    const int t = (int)kv_divide(r, by_heads), h = (int)(r - (uint32_t)t * c.heads);
+    int64_t slot = r < (uint32_t)rows ? slots[t] : -1;
     if (slot >= c.slots) slot = -1;
     v4u raw[BITS / 4] = {};
     float f = 0.0f;
@@ -207,8 +207,8 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* 
     stage_i16<0>(v, lane);
     if constexpr (L > 2) stage_i16<1>(v, lane);
     if constexpr (L > 4) stage_i16<2>(v, lane);
-    if (r >= rows) continue;
-    v4u* dst = reinterpret_cast<v4u*>(out + r * D) + lane;
+    if (r >= (uint32_t)rows) continue;
+    v4u* dst = reinterpret_cast<v4u*>(out + (int64_t)r * D) + lane;
     // element e of the lane is in half e / gap % 2 of v[e / (2 gap) * gap + e % gap]
     uint32_t w[16];
     auto at = [&](int e) { return __fmul_rn((float)v[e / (2 * gap) * gap + e % gap][e / gap % 2], f); };
@@ -236,8 +236,8 @@ hipError_t append(const KvCache& c, const KvRows& k, const KvRows& v, bool bf16,
                   hipStream_t stream) {
   const int rows = (int)(T * c.heads);
   const dim3 grid(row_grid(rows, D), 2);
-  if (bf16) kv_append_kernel<D, BITS, true><<<grid, 256, 0, stream>>>(c, k, v, slots, rows);
-  else kv_append_kernel<D, BITS, false><<<grid, 256, 0, stream>>>(c, k, v, slots, rows);
+  if (bf16) kv_append_kernel<D, BITS, true><<<grid, 256, 0, stream>>>(c, k, v, slots, rows, kv_divider((uint32_t)c.heads));
+  else kv_append_kernel<D, BITS, false><<<grid, 256, 0, stream>>>(c, k, v, slots, rows, kv_divider((uint32_t)c.heads));
   return hipGetLastError();
 }
 
@@ -246,7 +246,7 @@ hipError_t read(const KvCache& c, const int64_t* slots, int64_t T, uint16_t* K, 
                 hipStream_t stream) {
   const int rows = (int)(T * c.heads);
   const dim3 grid(row_grid(rows, D), K && V ? 2 : 1);
-  kv_read_kernel<D, BITS><<<grid, 256, 0, stream>>>(c, slots, rows, K, V, bf16);
+  kv_read_kernel<D, BITS><<<grid, 256, 0, stream>>>(c, slots, rows, kv_divider((uint32_t)c.heads), K, V, bf16);
   return hipGetLastError();
 }
 
