@@ -298,6 +298,9 @@ ATTENTION = [
     ([70, 90], [170, 90], 1, 5, 256, 8, BF16, 16, True),
     ([255, 17], [255, 1000], 1, 4, 128, 8, F16, 256, True),
     ([48], [6000], 1, 2, 128, 4, F16, 16, True),          # few rows, a long context: split
+    # enough rows of 128 for workgroups of 256, lengths that leave tiles and groups of 16 part empty
+    ([512, 499, 3, 290], [600, 499, 300, 777], 8, 4, 128, 4, BF16, 32, True),
+    ([400, 513], [450, 100], 16, 4, 128, 8, F16, 16, False),
     # states of another length
     ([100, 64], [77, 1], 2, 1, 128, 4, F16, 16, False),
     ([1, 1, 5], [77, 513, 0], 2, 4, 64, 4, BF16, 32, False),
@@ -321,6 +324,97 @@ def test_attention(case):
     tight = cr.kv_attention(cache, q, table, lens, q_start=_starts(q_lens), max_q=max(q_lens), max_kv=max(kv_lens),
                             causal=causal)
     _check_attention(cache, q, table, q_lens, kv_lens, causal, tight, tell="tight bounds")
+
+
+@pytest.mark.parametrize("batch", [63, 64, 65, 130, 256])
+def test_attention_of_many_sequences(batch):
+    """Units cut over all sequences: idle ones, short ones, a few long ones."""
+    _say("many sequences", batch)
+    g = _gen(batch, 11)
+    kv_lens = [int(x) for x in torch.randint(0, 90, (batch,), generator=g)]
+    kv_lens[0], kv_lens[batch // 2], kv_lens[-1], kv_lens[1] = 3000, 1700, 700, 0
+    cache = _random_cache(g, sum(-(-m // 16) for m in kv_lens), 16, 2, 64, 4)
+    table, lens = _sequences(g, cache, kv_lens)
+    q = torch.randn((batch, 6, 64), generator=g).half().to(DEV)
+    got = cr.kv_attention(cache, q, table, lens)
+    _check_attention(cache, q, table, [1] * batch, kv_lens, True, got)
+    # some sequences without a query, some with two
+    q_lens = [int(x) for x in torch.randint(0, 3, (batch,), generator=g)]
+    q = torch.randn((sum(q_lens), 6, 64), generator=g).half().to(DEV)
+    got = cr.kv_attention(cache, q, table, lens, q_start=_starts(q_lens), max_q=2)
+    _check_attention(cache, q, table, q_lens, kv_lens, True, got)
+
+
+def test_attention_of_more_sequences_than_are_balanced():
+    """Over 256 sequences and a wide table: fixed chunks of 4096 tokens."""
+    _say("300 sequences")
+    g = _gen(12)
+    kv_lens = [int(x) for x in torch.randint(0, 40, (300,), generator=g)]
+    kv_lens[7] = 9001
+    cache = _random_cache(g, sum(-(-m // 16) for m in kv_lens), 16, 1, 64, 8)
+    table, lens = _sequences(g, cache, kv_lens)
+    q = torch.randn((300, 3, 64), generator=g).bfloat16().to(DEV)
+    got = cr.kv_attention(cache, q, table, lens)
+    _check_attention(cache, q, table, [1] * 300, kv_lens, True, got)
+
+
+@pytest.mark.parametrize("n,m,heads,d", [(1, 9001, 1024, 64), (3, 8700, 1100, 128), (40, 5003, 1600, 64),
+                                         (36, 4500, 1100, 128), (33, 4300, 600, 256)])
+def test_attention_walks_long_contexts_alone(n, m, heads, d):
+    """So many heads that one workgroup walks a context past its 64 remembered pages; three heads are compared."""
+    _say("long and alone", n, m, heads, d)
+    g = _gen(n, m)
+    page, pages = 16, -(-m // 16)
+    dev = torch.Generator(device=DEV)
+    dev.manual_seed(m)
+    shape = (pages, heads, page)
+    cache = cr.KVCache(*(f() for _ in range(2) for f in (
+        lambda: torch.randint(0, 256, (*shape, d // 2), dtype=torch.uint8, device=DEV, generator=dev),
+        lambda: torch.rand(shape, device=DEV, generator=dev) * 0.1)))
+    for codes in (cache.k_codes, cache.v_codes):       # codes of -8 are not written by kv_append
+        codes[(codes & 0xF) == 8] = 0
+        codes[(codes >> 4) == 8] = 0
+    table, lens = _sequences(g, cache, [m])
+    q = torch.randn((n, heads, d), generator=g).half().to(DEV)
+    got = cr.kv_attention(cache, q, table, lens, max_kv=m)
+    some = torch.tensor([0, heads // 2 + 1, heads - 1])
+    part = cr.KVCache(*(t[:, some].contiguous() for t in (cache.k_codes, cache.k_scale, cache.v_codes, cache.v_scale)))
+    _check_attention(part, q[:, some], table, [n], [m], True, got[:, some])
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_attention_value_rows_of_all_sizes(rows, bits):
+    """Values of zero under the largest weight, and values whose scales span fp32."""
+    _say("value sizes", rows, bits)
+    m, d = 400, 64
+    g = _gen(rows, bits)
+    k, v = _values(g, (m, 1, d), BF16), _values(g, (m, 1, d), BF16)
+    table = torch.arange(25, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([m], dtype=torch.int32, device=DEV)
+    q = torch.randn((rows, 1, d), generator=g).bfloat16().to(DEV)
+    slots = torch.arange(m, device=DEV)
+    for change in ("sink", "first tiles zero", "all zero", "tiny", "large", "rising"):
+        kk, vv = k.clone(), v.clone()
+        if change == "sink":                            # its score is far above the others, its value is zero
+            kk[0] = q[0, 0].cpu() * 30
+            vv[0] = 0
+        elif change == "first tiles zero":
+            vv[:200] = 0
+        elif change == "all zero":
+            vv[:] = 0
+        elif change == "tiny":
+            vv *= 2.0 ** -60
+        elif change == "large":
+            vv *= 2.0 ** 60
+        else:
+            vv *= torch.exp2(torch.linspace(-70, 60, m))[:, None, None].bfloat16()
+        cache = cr.KVCache.empty(25, 16, 1, d, bits, DEV)
+        cr.kv_append(cache, kk.to(DEV), vv.to(DEV), slots)
+        got = cr.kv_attention(cache, q, table, lens)
+        _check_attention(cache, q, table, [rows], [m], True, got, tell=change)
+        if change == "all zero":
+            assert not got.any()
 
 
 @pytest.mark.parametrize("n,m", [(1, 5000), (20, 700), (150, 700)])
