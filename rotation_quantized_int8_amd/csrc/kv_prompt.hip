@@ -14,7 +14,10 @@
 // A lane owns one row (column lane % 32); the result layout of S^T is the
 // operand layout of W^T up to an order of the tokens that C_v^T is stored in.
 // The rotated queries are rounded to fp16 after a power of two common to the
-// workgroup; it, sm_scale and log2 e are multiplied into the keys' scales, so
+// workgroup.  For fp16 rows the remainder, rounded again, takes a second
+// product into the same accumulator: left out, it would cost the outputs
+// twice their own rounding (measured: 4.1e-4 against 2.1e-4, with it 2.8e-4);
+// next to the rounding of a bf16 output it is nothing.  The unit, sm_scale and log2 e are multiplied into the keys' scales, so
 // a weight is exp2(fma(S, scale_j, base_row)): one operation, its exponential,
 // its share of the sum and the product with the value's scale.  The running
 // maximum is raised only when a weight could pass 2^15 (they start at 2^8 for
@@ -83,7 +86,7 @@ struct Prompt {
   static constexpr int kBytes = 4 * kBuffer;
 };
 
-template <int D, int BITS, int WAVES>
+template <int D, int BITS, int WAVES, bool BF16>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttn a, KvSplit sp) {
   using P = Prompt<D, BITS, WAVES>;
   constexpr int kRows = P::kRows, kStep = P::kStep;
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
   // elements 4 hi .. 4 hi + 3 of units 2 k and 2 k + 1, alternating.
   const int myrow = tile * kRows + 32 * wave + col, myquery = kv_query_of(a, myrow);
   float common;                                        // what a score's product is multiplied by, without the key's scale
-  v8h q[P::kSteps];
+  v8h q[P::kSteps], left_over[BF16 ? 1 : P::kSteps];        // fp16 rows: and what the rounding leaves
   {
     v16f x[P::kTiles];
 #pragma unroll
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
       for (int r = 0; r < 16; ++r) x[t][r] = 0.0f;
     // W's operand of tile t, step k: the sign of element (m, d), m = 32 t + col, d = 16 k + 8 hi + j, is the parity of
     // m & d = that of (col & 7) & j, of (col >> 3 & hi & 1), of (col >> 4) & k & 1 and of t & (k >> 1)
-    const uint32_t one = a.bf16 ? 0x3F80u : 0x3C00u;
+    const uint32_t one = BF16 ? 0x3F80u : 0x3C00u;
     v4u w[2][2];                                       // by k & 1, and negated
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -179,21 +182,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
       raw[k] = *reinterpret_cast<const v4u*>(src + 8 * (2 * k + hi));
       if (!in) raw[k] = (v4u){0, 0, 0, 0};
     }
-    if (a.bf16) {
 #pragma unroll
-      for (int k = 0; k < P::kSteps; ++k)
+    for (int k = 0; k < P::kSteps; ++k)
 #pragma unroll
-        for (int t = 0; t < P::kTiles; ++t)
-          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, w[k & 1][__builtin_popcount(t & k >> 1) & 1]),
-                                                         __builtin_bit_cast(v8b, raw[k]), x[t], 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int k = 0; k < P::kSteps; ++k)
-#pragma unroll
-        for (int t = 0; t < P::kTiles; ++t)
-          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, w[k & 1][__builtin_popcount(t & k >> 1) & 1]),
-                                                        __builtin_bit_cast(v8h, raw[k]), x[t], 0, 0, 0);
-    }
+      for (int t = 0; t < P::kTiles; ++t) {
+        const v4u sign = w[k & 1][__builtin_popcount(t & k >> 1) & 1];
+        if constexpr (BF16)
+          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, sign), __builtin_bit_cast(v8b, raw[k]), x[t], 0, 0, 0);
+        else
+          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, sign), __builtin_bit_cast(v8h, raw[k]), x[t], 0, 0, 0);
+      }
     float top = 0.0f;
 #pragma unroll
     for (int t = 0; t < P::kTiles; ++t)
@@ -213,13 +211,17 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit;
 #pragma unroll
     for (int k = 0; k < P::kSteps; ++k) {
-      v4u y;
+      v4u y, z;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 8 * (k % 2) + i;
-        y[i] = pack_f16x2_rn(x[k / 2][r] * (i % 2 ? odd : by), x[k / 2][r + 4] * (i % 2 ? odd : by));
+        const float f = x[k / 2][r] * (i % 2 ? odd : by), g = x[k / 2][r + 4] * (i % 2 ? odd : by);
+        y[i] = pack_f16x2_rn(f, g);
+        const h2 near = __builtin_bit_cast(h2, (uint32_t)y[i]);
+        z[i] = pack_f16x2_rn(f - (float)near[0], g - (float)near[1]);
       }
       q[k] = __builtin_bit_cast(v8h, y);
+      if constexpr (!BF16) left_over[k] = __builtin_bit_cast(v8h, z);
     }
   }
 
@@ -289,6 +291,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     for (int k = 0; k < P::kSteps; ++k) {
       const v8h c = *reinterpret_cast<const v8h*>(kbuf + buf * P::kBuffer + ((kt * P::kSteps + k) * 64 + lane) * 16);
       z = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[k], z, 0, 0, 0);
+      if constexpr (!BF16) z = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, left_over[k], z, 0, 0, 0);
     }
     return z;
   };
@@ -296,7 +299,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
   auto use = [&](int buf, int kt, int j, v16f z) {
     const v2u gone = *reinterpret_cast<const v2u*>(&absent[buf][2 * kt]);
     const bool whole = __builtin_amdgcn_readfirstlane((j + 32 <= first) & !(gone[0] | gone[1]));
-    auto seen = [&](int r) { return (j + 8 * (r / 4) + 4 * hi + r % 4 < end) & !gone[r / 8]; };
+    const int left = end - j - 4 * hi;                 // (one register, where the compiler would keep sixteen bounds)
+    auto seen = [&](int r) { return (8 * (r / 4) + r % 4 < left) & !gone[r / 8]; };
     const float* vmost = &vtop[buf][2 * kt];
     float sum;
     auto weigh = [&]() {                               // z becomes the weights times the values' scales
@@ -437,15 +441,15 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
   }
   const int head = h * a.group + myrow - myquery * a.group;
   uint16_t* dst = a.o + ((s.first + myquery) * a.q_heads + head) * D;
-  units([&](int unit, float (&y)[8]) { store_row<8>(dst + 8 * unit, a.bf16, y); });
+  units([&](int unit, float (&y)[8]) { store_row<8>(dst + 8 * unit, BF16, y); });
 }
 
-template <int D, int BITS, int WAVES>
+template <int D, int BITS, int WAVES, bool BF16>
 hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
   KvSplit sp = p.split;
   sp.o = static_cast<float*>(workspace);
   sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
-  const auto fn = kv_prompt_kernel<D, BITS, WAVES>;
+  const auto fn = kv_prompt_kernel<D, BITS, WAVES, BF16>;
   const size_t lds = Prompt<D, BITS, WAVES>::kBytes;
   if (hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fn), lds)) return e;
   fn<<<dim3((unsigned)(a.c.heads * sp.splits * sp.tiles), 1, a.batch), 64 * WAVES, lds, stream>>>(a, sp);
@@ -453,11 +457,16 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
   return sp.splits > 1 ? launch_kv_join(a, sp, stream) : hipSuccess;
 }
 
+template <int BITS, bool BF16>
+hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
+  if (a.c.head_dim == 64) return run<64, BITS, 4, BF16>(a, p, workspace, stream);
+  if (a.c.head_dim == 256) return run<256, BITS, 4, BF16>(a, p, workspace, stream);
+  return p.waves == 8 ? run<128, BITS, 8, BF16>(a, p, workspace, stream) : run<128, BITS, 4, BF16>(a, p, workspace, stream);
+}
+
 template <int BITS>
 hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
-  if (a.c.head_dim == 64) return run<64, BITS, 4>(a, p, workspace, stream);
-  if (a.c.head_dim == 256) return run<256, BITS, 4>(a, p, workspace, stream);
-  return p.waves == 8 ? run<128, BITS, 8>(a, p, workspace, stream) : run<128, BITS, 4>(a, p, workspace, stream);
+  return a.bf16 ? run<BITS, true>(a, p, workspace, stream) : run<BITS, false>(a, p, workspace, stream);
 }
 
 }  // namespace
