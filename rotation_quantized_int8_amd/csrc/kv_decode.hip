@@ -399,41 +399,29 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
     }
 
     // ---- weights
-    auto seen = [&](int t, int u, int r) { return (j0 + 16 * u + 4 * r + quad < end[t]) & here[u]; };
-    if (!whole) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          vs[u][r] = (here[u] & (j0 + 16 * u + 4 * r + quad < c1)) ? vs[u][r] : 0.0f;
-    }
+    auto seen = [&](int t, int u, int r) { return (16 * u + 4 * r < end[t] - j0 - quad) & here[u]; };
     v8h w[QT];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      float p[8], x[8], sum;
-      auto weigh = [&]() {
+      float x[8], sum;
+      for (bool again = false;; again = true) {
+        float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int u = e / 4, r = e % 4;
-          p[e] = __builtin_amdgcn_exp2f(__fmaf_rn((float)sc[t][u][r], ks[u][r] * qf[t], base[t]));
-        }
+        for (int e = 0; e < 8; ++e)
+          p[e] = __builtin_amdgcn_exp2f(__fmaf_rn((float)sc[t][e / 4][e % 4], ks[e / 4][e % 4] * qf[t], base[t]));
         if (!whole) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) p[e] = seen(t, e / 4, e % 4) ? p[e] : 0.0f;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = p[e] * vs[e / 4][e % 4];
-        if (!whole) {   // a token that another row sees may have a NaN scale
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = p[e] == 0.0f ? 0.0f : x[e];
-        }
         sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      };
-      weigh();
-      float top = x[0];
+        // a weight of 0 stays 0 under a NaN scale, which another row may see
 #pragma unroll
-      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-      if (__any((top > kMostWeight) | (sum > kMostSum) | (base[t] == kUnset))) {   // raise the maximum
+        for (int e = 0; e < 8; ++e) x[e] = mul_legacy(p[e], vs[e / 4][e % 4]);
+        float top = x[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+        // raise the maximum (rare); a row that has seen no token has an infinite sum
+        if (again || !__any((top > kMostWeight) | (sum > kMostSum))) break;
         float best = kLowest;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -448,7 +436,6 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
         for (int i = 0; i < E; ++i) o[t][i] *= by;
         base[t] = next;
-        weigh();
       }
       l[t] += sum;
       v4u packed;

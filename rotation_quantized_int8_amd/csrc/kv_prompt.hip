@@ -301,9 +301,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     const bool whole = __builtin_amdgcn_readfirstlane((j + 32 <= first) & !(gone[0] | gone[1]));
     const int left = end - j - 4 * hi;                 // (one register, where the compiler would keep sixteen bounds)
     auto seen = [&](int r) { return (8 * (r / 4) + r % 4 < left) & !gone[r / 8]; };
-    const float* vmost = &vtop[buf][2 * kt];
+    const float vmost = fmaxf(vtop[buf][2 * kt], vtop[buf][2 * kt + 1]);
     float sum;
-    auto weigh = [&]() {                               // z becomes the weights times the values' scales
+    for (bool again = false;; again = true) {          // z becomes the weights
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
@@ -314,23 +314,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
 #pragma unroll
         for (int r = 0; r < 16; ++r) z[r] = seen(r) ? z[r] : 0.0f;
       }
-      sum = 0.0f;
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) sum += (z[r] + z[r + 1]) + (z[r + 2] + z[r + 3]);
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
-        if (!whole) {                                  // a NaN scale that another row sees
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vs[i] = z[r + i] == 0.0f ? 0.0f : vs[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[r + i] *= vs[i];
-      }
-    };
-    weigh();
-    // raise the maximum (rare) where a weight might pass 2^15; a row that has seen no token has an infinite sum
-    if (__any((sum * fmaxf(vmost[0], vmost[1]) > kMostWeight) | (sum > kMostSum))) {
+      sum = ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
+      sum += ((z[8] + z[9]) + (z[10] + z[11])) + ((z[12] + z[13]) + (z[14] + z[15]));
+      // raise the maximum (rare) where a weight might pass 2^15; a row that has seen no token has an infinite sum
+      if (again || !__any((sum * vmost > kMostWeight) | (sum > kMostSum))) break;
       z = score(buf, kt);
       float best = kLowest;
 #pragma unroll
@@ -349,7 +336,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
 #pragma unroll
       for (int t = 0; t < P::kTiles; ++t) o[t] *= by;
       base = next;
-      weigh();
+    }
+    // times the values' scales; a weight of 0 stays 0 under a NaN scale, which another row may see
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[r + i] = mul_legacy(z[r + i], vs[i]);
     }
     l += sum;
     v4u w[2];
