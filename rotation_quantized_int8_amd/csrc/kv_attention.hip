@@ -6,10 +6,14 @@
 namespace convrot {
 namespace {
 
-// Up to 32 rows (queries times heads of a group) per key head the cached rows
-// are read for one or two tiles of 16: HBM counts, and the single-token
-// kernel decodes in registers.  More rows share the decoding through LDS.
-bool few_rows(const KvAttn& a) { return (int64_t)a.max_q * a.group <= 32; }
+// Rows (queries times heads of a group) per key head.  The few-row kernel
+// decodes the cached rows anew for each 32 of them, in registers, and fills
+// the card with few; the other shares the decoding among 128 or 256 through
+// LDS.  Measured, few against many, us (heads of 128 in 4 bits, 8 key heads):
+//   4 sequences of 8192 tokens:    40 rows 31 / 39, 72 rows 42 / 45, 128 rows 50 / 52, 192 rows 82 / 85
+//   32 sequences of 2048 tokens:   40 rows 49 / 91, 72 rows 64 / 94, 128 rows 77 / 102, 256 rows 136 / 125
+//   64 sequences of 512 tokens:    72 rows 53 / 55, 128 rows 60 / 58, 256 rows 111 / 72
+bool few_rows(const KvAttn& a) { return (int64_t)a.max_q * a.group <= 128; }
 
 }  // namespace
 

@@ -709,13 +709,34 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
 
 }  // namespace
 
-// A short context (and a batch that fills the card several times over with
-// contexts that are not long) takes one workgroup per sequence, key head and
-// tile of rows, and no join; where these would leave CUs idle, of 16
-// wavefronts (8 for heads of 256).  Otherwise the tokens of all sequences are
-// cut into units that fill the card once (measured on 32 sequences of up to
-// 8192 tokens: twice as many units 51 us, four times as many 58 us, against
-// 45 us: starting and joining a unit costs about as much as 500 tokens).
+// A call runs in one of three ways, by `base`, its workgroups when each takes
+// a whole sequence for one key head and tile of rows, and by `slots`, the
+// workgroups that 256 CUs hold.  Measured with heads of 128 in 4 bits, 8 key
+// heads of 4 query heads (slots 1024), us:
+//   one workgroup of 4 wavefronts each, no join: while the walk is short
+//   against starting, splitting and joining, and where it fills the card;
+//   one workgroup of 16 wavefronts (8 for heads of 256) each, at most one a
+//   CU, no join: longer walks that about fill the CUs, and short ones that
+//   would leave most idle (there the split is as fast in a captured graph, but
+//   its second launch costs a stream of single calls 4 us);
+//   units of equal work over all sequences, then the join: the rest.  The
+//   units fill the card once: twice as many cost 51 us, four times as many
+//   58 us, against 45 us for 32 sequences of up to 8192 tokens.
+//     base  tokens   4 waves  16 waves  split
+//        8     512       8.9       9.9   10.8
+//        8    1024      12.3      12.1   10.8 (single calls: 13.5, 13.6, 17.5)
+//        8    2048      19.3      15.5   11.2
+//      128    2048      20.4      16.8   19.1
+//      128    4096      34.3      23.3   23.6 (unequal lengths: 34.0, 23.1, 20.6)
+//      256    1024      13.8      16.1   18.8
+//      256    4096      34.5      28.7   34.0 (unequal lengths: 33.6, 25.0, 28.8)
+//      512    4096      58.1      61.8   66.0 (unequal lengths: 47.6, 48.6, 52.8)
+//     1024    1024      29.1      52.5   34.0
+//     6000    2048       291       ---    301 (unequal lengths: 196, ---, 226)
+// More sequences than kv_units counts take equal chunks instead: 300 sequences
+// of up to 8192 tokens and one key head, 58.7 us in chunks of 2048 against
+// 68.0 whole; where base fills the card (8 key heads, up to 16384 tokens) 660
+// whole, 719 in chunks of 4096, 750 in chunks of 2048.
 KvPlan kv_decode_plan(const KvAttn& a) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_q * a.group;
@@ -729,12 +750,13 @@ KvPlan kv_decode_plan(const KvAttn& a) {
   s.units = a.batch;
   const int64_t heads = (int64_t)s.tiles * a.c.heads, base = heads * a.batch;
   const int64_t slots = 256 * kv_decode_wgs(a.c.head_dim, s.rows / 16, 4);   // resident on 256 CUs
-  if (a.max_kv <= 256) return p;
-  if (a.max_kv <= 1024 && base <= 256 && s.rows == 16) {
+  if (a.max_kv <= 512 || (a.max_kv <= 1024 && 4 * base >= slots) || (a.max_kv <= 4096 && 2 * base >= slots) ||
+      (a.max_kv <= 8192 && base >= 4 * slots))
+    return p;
+  if (s.rows == 16 && base <= 256 && a.max_kv <= (base < 128 ? 1024 : 16 * base)) {
     p.waves = kv_decode_wide(a.c.head_dim);
     return p;
   }
-  if (base >= 4 * slots && a.max_kv <= 8192) return p;
   if (a.batch <= 256) {
     const int64_t want = slots / heads;
     s.balance = (int)(want < a.batch ? a.batch : want);
@@ -745,8 +767,9 @@ KvPlan kv_decode_plan(const KvAttn& a) {
     s.splits = (a.max_kv + 255) / 256;                                  // a sequence's units at most
     if (s.splits > s.units) s.splits = s.units;
   } else {
-    if (a.max_kv <= 8192) return p;
-    s.chunk = 4096;
+    const int chunk = base < slots ? 2048 : 16384;
+    if (a.max_kv <= 2 * chunk) return p;
+    s.chunk = chunk;
     s.splits = (a.max_kv + s.chunk - 1) / s.chunk;
     s.units = a.batch * s.splits;
   }
@@ -762,7 +785,7 @@ hipError_t join(const KvAttn& a, const KvSplit& sp, hipStream_t stream) {
   const unsigned rows = (unsigned)a.max_q * a.group;
   const int64_t all = (int64_t)rows * a.c.heads * a.batch;
   if (sp.splits <= 16 && all >= 16384) kv_join_kernel<D, 1><<<dim3((rows + 15) / 16, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
-  else if (sp.splits <= 4) kv_join_kernel<D, 4><<<dim3((rows + 3) / 4, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
+  else if (sp.splits <= 8) kv_join_kernel<D, 4><<<dim3((rows + 3) / 4, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
   else if (sp.splits <= 32) kv_join_kernel<D, 16><<<dim3(rows, a.c.heads, a.batch), 256, 0, stream>>>(a, sp);
   else kv_join_kernel<D, 64><<<dim3(rows, a.c.heads, a.batch), 1024, 0, stream>>>(a, sp);
   return hipGetLastError();

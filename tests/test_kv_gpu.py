@@ -301,6 +301,16 @@ ATTENTION = [
     # enough rows of 128 for workgroups of 256, lengths that leave tiles and groups of 16 part empty
     ([512, 499, 3, 290], [600, 499, 300, 777], 8, 4, 128, 4, BF16, 32, True),
     ([400, 513], [450, 100], 16, 4, 128, 8, F16, 16, False),
+    # many rows over a longer context: split; rows around the border between the two kernels
+    ([150, 141], [4000, 2222], 1, 2, 64, 4, F16, 16, True),
+    ([128, 100], [300, 900], 2, 1, 128, 4, BF16, 16, True),
+    ([129, 128], [300, 900], 2, 1, 256, 8, F16, 32, True),
+    ([127, 33], [2000, 1029], 3, 1, 64, 8, F16, 16, False),
+    # about a sequence and key head for each CU: workgroups of 16 wavefronts, single ones for a whole sequence
+    ([1] * 20, [2040, 0, 1] + [97 * i + 13 for i in range(17)], 8, 2, 128, 4, F16, 32, True),
+    ([2] * 26, [1500, 3, 1] + [53 * i for i in range(23)], 7, 2, 64, 8, BF16, 16, True),
+    ([1] * 9, [1024, 1, 999, 1000, 31, 0, 512, 513, 768], 2, 3, 256, 8, F16, 64, True),
+    ([9] * 40, [900 - 17 * i for i in range(40)], 4, 3, 128, 8, BF16, 16, True),
     # states of another length
     ([100, 64], [77, 1], 2, 1, 128, 4, F16, 16, False),
     ([1, 1, 5], [77, 513, 0], 2, 4, 64, 4, BF16, 32, False),
@@ -346,20 +356,26 @@ def test_attention_of_many_sequences(batch):
 
 
 def test_attention_of_more_sequences_than_are_balanced():
-    """Over 256 sequences and a wide table: fixed chunks of 4096 tokens."""
-    _say("300 sequences")
+    """Over 256 sequences and a wide table: fixed chunks of 2048 tokens, of 16384 where the heads fill the card."""
+    for heads, most in ((1, 9001), (4, 33001)):
+        _say("300 sequences", heads)
+        _more_sequences(heads, most)
+
+
+def _more_sequences(heads, most):
     g = _gen(12)
     kv_lens = [int(x) for x in torch.randint(0, 40, (300,), generator=g)]
-    kv_lens[7] = 9001
-    cache = _random_cache(g, sum(-(-m // 16) for m in kv_lens), 16, 1, 64, 8)
+    kv_lens[7] = most
+    cache = _random_cache(g, sum(-(-m // 16) for m in kv_lens), 16, heads, 64, 8)
     table, lens = _sequences(g, cache, kv_lens)
-    q = torch.randn((300, 3, 64), generator=g).bfloat16().to(DEV)
+    q = torch.randn((300, 3 * heads, 64), generator=g).bfloat16().to(DEV)
     got = cr.kv_attention(cache, q, table, lens)
     _check_attention(cache, q, table, [1] * 300, kv_lens, True, got)
 
 
 @pytest.mark.parametrize("n,m,heads,d", [(1, 9001, 1024, 64), (3, 8700, 1100, 128), (40, 5003, 1600, 64),
-                                         (36, 4500, 1100, 128), (33, 4300, 600, 256)])
+                                         (36, 4500, 1100, 128), (33, 4300, 600, 256), (136, 4500, 600, 128),
+                                         (140, 4300, 1600, 64), (133, 4100, 300, 256)])
 def test_attention_walks_long_contexts_alone(n, m, heads, d):
     """So many heads that one workgroup walks a context past its 64 remembered pages; three heads are compared."""
     _say("long and alone", n, m, heads, d)
@@ -382,7 +398,7 @@ def test_attention_walks_long_contexts_alone(n, m, heads, d):
     _check_attention(part, q[:, some], table, [n], [m], True, got[:, some])
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 140])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_attention_value_rows_of_all_sizes(rows, bits):
     """Values of zero under the largest weight, and values whose scales span fp32."""
@@ -443,7 +459,7 @@ def test_attention_is_repeatable_on_streams_and_buffers(n, m):
     assert torch.equal(cr.kv_attention(cache, odd, table, lens), want)
 
 
-@pytest.mark.parametrize("n,m", [(1, 3000), (17, 300), (70, 300)])
+@pytest.mark.parametrize("n,m", [(1, 3000), (17, 300), (70, 300), (30, 300)])
 def test_attention_absent_pages_and_extreme_scores(n, m):
     _say("absent pages", n, m)
     g = _gen(n, m, 1)
@@ -489,7 +505,7 @@ def test_attention_sums_a_long_even_tail():
     lens = torch.tensor([m], dtype=torch.int32, device=DEV)
     q = torch.zeros((1, 1, d), dtype=F16)
     q[..., 0] = 1.0
-    for rows in (1, 40):
+    for rows in (1, 40, 140):
         x = q.expand(rows, 1, d).contiguous().to(DEV)
         got = cr.kv_attention(cache, x, table, lens, scale=float(np.log(60000.0)), causal=False)
         _check_attention(cache, x, table, [rows], [m], False, got, scale=float(np.log(60000.0)))
@@ -518,7 +534,7 @@ def test_attention_scores_that_keep_rising(rows, step):
 def test_attention_shows_a_nan_that_is_seen_only():
     _say("NaN rows")
     g = _gen(8)
-    for n, m in ((1, 700), (50, 100)):
+    for n, m in ((1, 700), (50, 100), (80, 100)):
         cache = _random_cache(g, -(-m // 16), 16, 2, 128, 4)
         table, lens = _sequences(g, cache, [m])
         q = torch.randn((n, 4, 128), generator=g).half().to(DEV)
@@ -529,7 +545,7 @@ def test_attention_shows_a_nan_that_is_seen_only():
         assert n == 1 or got[:-1].isfinite().all()
 
 
-@pytest.mark.parametrize("n", [1, 64])
+@pytest.mark.parametrize("n", [1, 64, 20])
 def test_graph_replays_write_and_attend(n):
     """Write, attend and read inside one graph, replayed with new inputs and
     eager work between the replays; each replay equals the eager calls."""
@@ -589,7 +605,7 @@ def test_offsets_past_32_bits():
         assert torch.equal(got.cpu(), torch.from_numpy(O.read_f32(c, s)).half())
     table = torch.arange(pages - 3, pages, dtype=torch.int32, device=DEV)[None]
     lens = torch.tensor([n], dtype=torch.int32, device=DEV)
-    for rows in (1, 40):
+    for rows in (1, 40, 140):
         q = torch.randn((rows, heads, d), generator=g).half().to(DEV)
         got = cr.kv_attention(cache, q, table, lens)
         _check_attention(cache, q, table, [rows], [n], True, got)
