@@ -88,14 +88,17 @@ size_t convrot_kv_workspace_bytes(const convrot_kv_cache* cache, int64_t T, int6
  *   table     int32 [batch, table_width]: token j of sequence b is at page
  *             table[b, j / page_size], offset j % page_size.  The tokens of a
  *             page number out of range are left out (an absent page).
- *   max_kv    at most table_width * page_size.
+ *   max_kv    at most table_width * page_size and 2^30.
  *   causal    nonzero: query i of n sees the first kv_len - n + i + 1 tokens
  *             (the queries are the sequence's last tokens, already cached);
  *             zero: every token (states of another length).
- * A query that sees no token gives zeros.  Sums, maxima and accumulators are
- * fp32 (scores of single tokens: int32); the softmax weights and, for more
- * than 32 query rows per key head, the rotated queries enter the matrix cores
- * as fp16.  O must not overlap an input; the workspace (may be NULL where 0
+ * A query that sees no token gives zeros; a NaN scale shows in the queries
+ * that see its token and in no other.  Sums, maxima and accumulators are fp32.
+ * For up to 128 query rows (queries times heads of a group) per key head the
+ * rotated queries enter the matrix cores as 16-bit fixed point of their row's
+ * maximum and the scores are exact sums in int32; for more rows fp16 queries
+ * enter as two fp16 numbers, bf16 queries as one.  The softmax weights enter
+ * as fp16, at 2^8 and more for the largest.  O must not overlap an input; the workspace (may be NULL where 0
  * bytes are needed) must not overlap anything. */
 convrot_status convrot_kv_attention(const convrot_kv_cache* cache, const void* Q, int64_t q_token_stride,
                                     int64_t q_head_stride, int dtype, int64_t T, int64_t q_heads,
