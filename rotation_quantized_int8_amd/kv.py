@@ -63,26 +63,28 @@ class KVCache:
                  "device", "_struct", "_ref")
 
     def __init__(self, k_codes: torch.Tensor, k_scale: torch.Tensor, v_codes: torch.Tensor, v_scale: torch.Tensor):
-        kind = k_codes.dtype
+        kind, shape, index = k_codes.dtype, k_codes.shape, k_codes.get_device()
         if kind not in (torch.uint8, torch.int8) or v_codes.dtype != kind:
             raise TypeError("codes must both be uint8 (4 bits, two a byte) or both int8 (8 bits)")
         if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
             raise TypeError("scales must be float32")
-        shape = k_codes.shape
-        if len(shape) != 4 or v_codes.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+        if len(shape) != 4 or v_codes.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != k_scale.shape:
             raise ValueError("codes must be [pages, heads, page_size, bytes] and scales [pages, heads, page_size]")
-        self.device = k_codes.device
-        for t in (k_codes, k_scale, v_codes, v_scale):
-            if t.device != self.device or t.device.type != "cuda":
+        tensors = (k_codes, k_scale, v_codes, v_scale)
+        at = [t.data_ptr() for t in tensors]
+        for t in tensors:
+            if index < 0 or t.get_device() != index:
                 raise ValueError("the cache's tensors must be on one GPU (no CPU path exists)")
-            if not t.is_contiguous() or t.data_ptr() % 16:
+            if not t.is_contiguous():
                 raise ValueError("the cache's tensors must be contiguous and aligned to 16 bytes")
+        if (at[0] | at[1] | at[2] | at[3]) % 16:
+            raise ValueError("the cache's tensors must be contiguous and aligned to 16 bytes")
+        self.device = k_codes.device
         self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
         self.pages, self.heads, self.page_size, row = shape
         self.bits = 4 if kind == torch.uint8 else 8
         self.head_dim = row * 2 if self.bits == 4 else row
-        self._struct = _Cache(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(),
-                              self.pages, self.page_size, self.heads, self.head_dim, self.bits)
+        self._struct = _Cache(*at, self.pages, self.page_size, self.heads, self.head_dim, self.bits)
         self._ref = ctypes.addressof(self._struct)
 
     @classmethod
@@ -106,12 +108,13 @@ class KVCache:
 # builds a Python object around it (2.8 us of a call's 9, against 0.1).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, name: str, device: torch.device, *args) -> None:
     """fn(*args, stream) with the device current, on its current stream."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -173,7 +176,8 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
         raise ValueError("slots must be one-dimensional")
     shape = (slots.shape[0], cache.heads, cache.head_dim)
     if out is None:
-        k, v = torch.empty((2, *shape), dtype=dtype, device=cache.device).unbind(0)
+        k = slots.new_empty(shape, dtype=dtype)
+        v = torch.empty_like(k)
     else:
         k, v = out
         for t in (k, v):
@@ -226,7 +230,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, kv_lens: 
     if max_kv is None:
         max_kv = width * cache.page_size
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != q.device:
         raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
     need = kv_workspace_bytes(cache, tokens, q_heads, batch, max_q, max_kv)
