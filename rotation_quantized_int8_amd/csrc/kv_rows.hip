@@ -58,25 +58,26 @@ __device__ __forceinline__ void stage_i16(v2s (&v)[16], int lane) {
 }
 
 // Codes of 32 values u with scale s, as 16 (4 bits) or 32 (8 bits) bytes.
-// Rounds u / s half to even through the product with the reciprocal: with r
-// within one ulp of 1 / s and |u / s| <= 127 (1 + 2^-23), u r lies within
-// 1.6e-5 of u / s and fp32(u / s) within 3.9e-6, so unless u r is within 3e-5
-// of a half-integer both round to the same integer, which fma(u, r, 1.5 2^23)
-// leaves in its low mantissa bits.  Lanes with a closer value, and scales
+// Rounds u / s half to even without dividing: r is within one ulp of 1 / s, so
+// with low = r (1 - 3 2^-23) and high = r (1 + 3 2^-23), each rounded once, u /
+// s and fp32(u / s) lie between u low and u high.  fma(x, y, 1.5 2^23) rounds
+// the exact product half to even and leaves it in its low mantissa bits; where
+// both ends round alike, so does all between.  Lanes where an element's ends
+// differ (a half lies between: one in 3e5 / |u / s| elements), and scales
 // whose reciprocal could leave fp32's normal range, divide.
 template <int BITS>
 __device__ __forceinline__ void codes32(const float (&u)[32], float s, uint32_t (&w)[BITS]) {
   constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
   const float r = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
-  uint32_t b[32];
-  float off = 0.0f;
+  const float low = __fmul_rn(r, 1.0f - 0x3p-23f), high = __fmul_rn(r, 1.0f + 0x3p-23f);
+  uint32_t b[32], apart = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const float m = __fmaf_rn(u[i], r, kMagic);
-    off = fmaxf(off, fabsf(__fmaf_rn(u[i], r, -__fsub_rn(m, kMagic))));
-    b[i] = __float_as_uint(m);
+    b[i] = __float_as_uint(__fmaf_rn(u[i], low, kMagic));
+    const uint32_t other = __float_as_uint(__fmaf_rn(u[i], high, kMagic));
+    asm("v_sad_u32 %0, %1, %2, %0" : "+v"(apart) : "v"(b[i]), "v"(other));   // += |b - other|
   }
-  if (off > 0.49997f || s < 1e-30f || s > 1e30f) {
+  if (apart || s < 1e-30f || s > 1e30f) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) b[i] = __float_as_uint(__fadd_rn(s == 0.0f ? 0.0f : u[i] / s, kMagic));
   }
@@ -84,7 +85,7 @@ __device__ __forceinline__ void codes32(const float (&u)[32], float s, uint32_t 
   for (int j = 0; j < BITS; ++j) {
     uint32_t x = 0;
 #pragma unroll
-    for (int i = 0; i < 32 / BITS; ++i) x |= (b[32 / BITS * j + i] & ((1u << BITS) - 1)) << (BITS * i);
+    for (int i = 0; i < 32 / BITS; ++i) x = __builtin_amdgcn_alignbit(b[32 / BITS * j + i], x, BITS);   // in at the top
     w[j] = x;
   }
 }
@@ -130,13 +131,14 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, Kv
     stage_f64<0>(v, lane);
     if constexpr (L > 2) stage_f64<1>(v, lane);
     if constexpr (L > 4) stage_f64<2>(v, lane);
-    float u[32];
-    uint32_t top = 0;   // the largest |u| by its bits, where a NaN is above infinity
+    // The largest |u| by its bits, where a NaN is above infinity.  An infinity or a NaN in a row leaves none of its u
+    // finite, so that one u shows it; the others, and a u that passes fp32, are compared as numbers.
+    float u[32], most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      u[i] = (float)v[i];
-      top = max(top, __float_as_uint(u[i]) & 0x7FFFFFFFu);
-    }
+    for (int i = 0; i < 32; ++i) u[i] = (float)v[i];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) most = fmaxf(fmaxf(most, fabsf(u[i])), fabsf(u[i + 1]));
+    uint32_t top = max(__float_as_uint(most), __float_as_uint(u[0]) & 0x7FFFFFFFu);
     top = max(top, (uint32_t)lane_swap<0>((int)top));
     if constexpr (L > 2) top = max(top, (uint32_t)lane_swap<1>((int)top));
     if constexpr (L > 4) top = max(top, (uint32_t)lane_swap<2>((int)top));
