@@ -7,14 +7,14 @@
 // rotation, five run in a lane's registers and the other one to three between
 // lanes, by DPP permutations inside a 16-lane row (no LDS).
 //
-// Both kernels are bound by HBM: a row costs 2 D bytes on its 16-bit side and
-// D bits / 8 + 4 in the cache, against about log2 D additions an element.
-// Measured, heads of 128 (a large copy reaches 5.1 TB/s): writing 16384 tokens
-// of 8 heads in 8 bits 28.6 us (3.6 TB/s), where four fifths of the additions
-// taken out would save 3 us; reading 65536 tokens of 8 heads from 4 bits 70 us
-// (4.9 TB/s); 1024 tokens of 16 heads in 4 bits 7.8 and 4.8 us.  Four tokens
-// of 8 heads cost 4.1 and 2.2 us, the latency of the dependent loads.  The
-// layout is what counted: with a lane's 64 bytes side by side instead of
+// A row costs 2 D bytes on its 16-bit side and D bits / 8 + 4 in the cache.
+// Reading is bound by HBM: 65536 tokens of 8 heads of 128 from 4 bits take 69
+// us, 4.9 TB/s where a large copy reaches 5.1.  Writing is bound by the vector
+// unit next to it, about 22 operations an element of 4 cycles a wavefront
+// (fp64 additions and conversions run at that rate too): 16384 tokens of 8
+// heads of 128 in 8 bits 26.4 us, 3.9 TB/s.  1024 tokens of 16 heads in 4 bits
+// take 6.3 and 4.8 us; four tokens of 8 heads 3.2 and 2.2 us, the latency of
+// the loads.  The layout is what counted: with a lane's 64 bytes side by side instead of
 // neighbouring lanes' 16 the large ones cost 38 and 94 us.  One pass over the
 // rows, since a grid of 2048 workgroups that walks them reads the large
 // context back in 95 us against 74; stores past the caches cost 77 us.
