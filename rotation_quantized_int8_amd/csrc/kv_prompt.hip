@@ -82,9 +82,11 @@ __device__ __forceinline__ void halves(const uint32_t* a, const uint32_t* b, uin
   }
 }
 
-template <int D, int BITS, int WAVES>
+// HALVES = 2: two wavefronts share 32 rows, each takes half of a step's tokens.
+template <int D, int BITS, int WAVES, int HALVES>
 struct Prompt {
-  static constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES;
+  static constexpr int kGroups = WAVES / HALVES;       // of 32 rows
+  static constexpr int kThreads = 64 * WAVES, kRows = 32 * kGroups;
   static constexpr int kStep = 16 * WAVES;             // tokens of a step: each wavefront decodes a group of 16
   static constexpr int kRow = D * BITS / 8;            // bytes of a cached row
   static constexpr int kUnit = BITS;                   // bytes of 8 codes
@@ -100,9 +102,10 @@ struct Prompt {
   static constexpr int kBytes = 4 * kBuffer;
 };
 
-template <int D, int BITS, int WAVES, bool BF16>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttn a, KvSplit sp) {
-  using P = Prompt<D, BITS, WAVES>;
+template <int D, int BITS, int WAVES, int HALVES, bool BF16>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 && HALVES == 1 ? 3 : 2)
+void kv_prompt_kernel(KvAttn a, KvSplit sp) {
+  using P = Prompt<D, BITS, WAVES, HALVES>;
   constexpr int kRows = P::kRows, kStep = P::kStep;
   extern __shared__ __align__(16) char lds[];          // keys [2], values [2]
   __shared__ __align__(16) float kscale[2][kStep], vscale[2][kStep];
@@ -112,6 +115,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 32, hi = lane / 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int group = HALVES == 1 ? wave : wave % P::kGroups, half = HALVES == 1 ? 0 : wave / P::kGroups;   // of rows, and of a step's tokens
   const int b = blockIdx.z;
   // the key head is the fastest index, so that the workgroups of one head meet in one XCD's L2 where the head
   // count is a multiple of 8; the last tiles, which see the most tokens, start first
@@ -140,7 +144,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     pages = p < a.c.pages ? p : -1;
   };
   const uint32_t koff = lane % 16 * P::kRow + lane / 16 % (P::kRow / 16) * 16;
-  auto load = [&](int step) {
+  auto load = [&](int step) __attribute__((always_inline)) {
     if (step % 64 == 0) find_pages(step);
     const int j = c0 + kStep * step + 16 * wave, p = __builtin_amdgcn_readlane(pages, step % 64);
     present = p >= 0;
@@ -166,7 +170,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
   // ---- the rotated queries as fp16.  The rotation is a matrix product too: W (+-1, exact) times the rows, whose
   // result layout is, in pairs of registers, the operand layout of the scores: lane (column = row, hi), step k, holds
   // elements 4 hi .. 4 hi + 3 of units 2 k and 2 k + 1, alternating.
-  const int myrow = tile * kRows + 32 * wave + col, myquery = kv_query_of(a, myrow);
+  const int myrow = tile * kRows + 32 * group + col, myquery = kv_query_of(a, myrow);
   float common;                                        // what a score's product is multiplied by, without the key's scale
   v8h q[P::kSteps], left_over[BF16 ? 1 : P::kSteps];        // fp16 rows: and what the rounding leaves
   {
@@ -241,7 +245,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
 
   char* kbuf = lds;
   char* vbuf = lds + 2 * P::kBuffer;
-  auto decode = [&](int buf, int step) {
+  auto decode = [&](int buf, int step) __attribute__((always_inline)) {
     if (P::kPieces >= 64 || lane < P::kPieces) {
       char* dst = kbuf + buf * P::kBuffer + ((wave / 2) * P::kSteps * 64 + wave % 2 * 16 + lane % 16) * 16;
 #pragma unroll
@@ -289,7 +293,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
 
   // ---- the steps
   const int end = myquery >= s.n ? 0 : a.causal ? s.kv - s.n + myquery + 1 : s.kv;
-  const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + 32 * wave) + 1 : s.kv;   // the wavefront's first row
+  const int first = a.causal ? s.kv - s.n + kv_query_of(a, tile * kRows + 32 * group) + 1 : s.kv;   // the wavefront's first row
   v16f o[P::kTiles];
   float base = kUnset, l = 0.0f;
 #pragma unroll
@@ -297,7 +301,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
 
-  auto score = [&](int buf, int kt) {
+  auto score = [&](int buf, int kt) __attribute__((always_inline)) {
     v16f z;
 #pragma unroll
     for (int r = 0; r < 16; ++r) z[r] = 0.0f;
@@ -310,7 +314,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     return z;
   };
   // the 32 tokens from j on, whose products with the queries are z: weights, then outputs
-  auto use = [&](int buf, int kt, int j, v16f z) {
+  auto use = [&](int buf, int kt, int j, v16f z) __attribute__((always_inline)) {
     const v2u gone = *reinterpret_cast<const v2u*>(&absent[buf][2 * kt]);
     const bool whole = __builtin_amdgcn_readfirstlane((j + 32 <= first) & !(gone[0] | gone[1]));
     const int left = end - j - 4 * hi;                 // (one register, where the compiler would keep sixteen bounds)
@@ -382,15 +386,46 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
         if (j + 2 * kStep < c1) load(step + 2);
       }
 #pragma unroll
-      for (int kt = 0; kt < WAVES / 2 && j + 32 * kt < c1; ++kt) use(buf, kt, j + 32 * kt, score(buf, kt));
+      for (int n = 0; n < P::kGroups / 2; ++n) {
+        const int kt = P::kGroups / 2 * half + n;
+        if (j + 32 * kt >= c1) break;
+        use(buf, kt, j + 32 * kt, score(buf, kt));
+      }
       __syncthreads();
     }
   }
 
+  l = sum32(l);
+  if constexpr (HALVES == 2) {                         // the second half's outputs join the first's
+    v4f* far = reinterpret_cast<v4f*>(lds) + 64 * group + lane;
+    float* rest_of = reinterpret_cast<float*>(lds + P::kTiles * 4 * P::kGroups * 1024) + 2 * (64 * group + lane);
+    if (half) {
+#pragma unroll
+      for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          far[(4 * t + r / 4) * P::kGroups * 64] = (v4f){o[t][r], o[t][r + 1], o[t][r + 2], o[t][r + 3]};
+      rest_of[0] = base;
+      rest_of[1] = l;
+    }
+    __syncthreads();
+    if (half) return;
+    const float other = rest_of[0], low = fminf(base, other);
+    const float mine = __builtin_amdgcn_exp2f(low - base), its = __builtin_amdgcn_exp2f(low - other);
+    l = l * mine + rest_of[1] * its;
+#pragma unroll
+    for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const v4f y = far[(4 * t + r / 4) * P::kGroups * 64];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][r + i] = o[t][r + i] * mine + y[i] * its;
+      }
+    base = low;
+  }
   // ---- a lane holds half a row: rotate it back (every bit of (tile, register) and the half-wave is a bit of the
   // element's number), or leave it to the join
-  l = sum32(l);
-  if (myquery >= s.n || 32 * wave + col >= rows) return;
+  if (myquery >= s.n || 32 * group + col >= rows) return;
   // element of (tile t, register r): row = 8 (r / 4) + 4 hi + r % 4, unit = row % kUnits, e = t * kSpread + row / kUnits
   auto unit_of = [&](int r) { return (8 * (r / 4) + 4 * hi + r % 4) % P::kUnits; };
   auto e_of = [&](int t, int r) { return t * P::kSpread + 8 * (r / 4) / P::kUnits; };
@@ -402,7 +437,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     for (int r = 0; r < 16; ++r)
       x[16 * t + r] = l == 0.0f ? 0.0f : o[t][r] * (BITS == 4 && e_of(t, r) % 2 ? by * 0.0625f : by);
   // the lane's units, 8 elements each
-  auto units = [&](auto&& store) {
+  auto units = [&](auto&& store) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < 2 * P::kTiles; ++n) {
       float y[8];
@@ -419,7 +454,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
     }
   };
   if (sp.splits > 1) {
-    const int64_t at = sp.row(h, tile, b * sp.splits + split, 32 * wave + col);
+    const int64_t at = sp.row(h, tile, b * sp.splits + split, 32 * group + col);
     float* dst = sp.o + at * D;
     units([&](int unit, float (&y)[8]) {
       *reinterpret_cast<v4f*>(dst + 8 * unit) = (v4f){y[0], y[1], y[2], y[3]};
@@ -451,13 +486,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 3 : 2) void kv
   units([&](int unit, float (&y)[8]) { store_row<8>(dst + 8 * unit, BF16, y); });
 }
 
-template <int D, int BITS, int WAVES, bool BF16>
+template <int D, int BITS, int WAVES, int HALVES, bool BF16>
 hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
   KvSplit sp = p.split;
   sp.o = static_cast<float*>(workspace);
   sp.ml = sp.o ? sp.o + p.parts * D : nullptr;
-  const auto fn = kv_prompt_kernel<D, BITS, WAVES, BF16>;
-  const size_t lds = Prompt<D, BITS, WAVES>::kBytes;
+  const auto fn = kv_prompt_kernel<D, BITS, WAVES, HALVES, BF16>;
+  const size_t lds = Prompt<D, BITS, WAVES, HALVES>::kBytes;
   if (hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fn), lds)) return e;
   fn<<<dim3((unsigned)(a.c.heads * sp.splits * sp.tiles), 1, a.batch), 64 * WAVES, lds, stream>>>(a, sp);
   if (hipError_t e = hipGetLastError()) return e;
@@ -466,9 +501,11 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
 
 template <int BITS, bool BF16>
 hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t stream) {
-  if (a.c.head_dim == 64) return run<64, BITS, 4, BF16>(a, p, workspace, stream);
-  if (a.c.head_dim == 256) return run<256, BITS, 4, BF16>(a, p, workspace, stream);
-  return p.waves == 8 ? run<128, BITS, 8, BF16>(a, p, workspace, stream) : run<128, BITS, 4, BF16>(a, p, workspace, stream);
+  if (a.c.head_dim == 256) return run<256, BITS, 4, 1, BF16>(a, p, workspace, stream);
+  if (a.c.head_dim == 64)
+    return p.waves == 8 ? run<64, BITS, 8, 2, BF16>(a, p, workspace, stream) : run<64, BITS, 4, 1, BF16>(a, p, workspace, stream);
+  if (p.waves == 8 && p.split.rows == 128) return run<128, BITS, 8, 2, BF16>(a, p, workspace, stream);
+  return p.waves == 8 ? run<128, BITS, 8, 1, BF16>(a, p, workspace, stream) : run<128, BITS, 4, 1, BF16>(a, p, workspace, stream);
 }
 
 template <int BITS>
@@ -478,24 +515,36 @@ hipError_t run(const KvAttn& a, const KvPlan& p, void* workspace, hipStream_t st
 
 }  // namespace
 
-// Heads of 128 with enough rows take workgroups of 8 wavefronts (256 rows),
+// Heads of 128 with enough rows take workgroups of 8 wavefronts for 256 rows,
 // which halves the decoding a row (4096 x 4096 causal, 32 heads: 190 us
-// against 210 us).  Where the tiles of rows fill less than half of the card
-// the tokens are split, so that about two rounds of workgroups even out
-// unequal lengths (three sequences of 700 queries over 6000 tokens: one split
-// 190 us, three 150 us, five 177 us).
+// against 210 us).  Where tiles of 128 rows leave at most one workgroup for a
+// CU, 8 wavefronts share them, two to 32 rows, each half of the tokens, so
+// that a SIMD still has two (1024 x 1024 causal, 32 heads over 8: 33.6 us
+// against 44.8 with 4 wavefronts; 1024 x 2048, 16 heads, twice: 60 against
+// 85).  They join for 2 us, so not for contexts of one step (64 x 64: 12.8
+// against 10.5), nor for long contexts of several sequences, where splitting
+// evens out their lengths (five of 150 queries over up to 8000 tokens: 174
+// against 139).
+// The tokens are split where the workgroups leave room for more: one sequence
+// into as many units as run at once (3000 x 3000, heads of 64: 96 us, twice
+// as many 122 us), several into two rounds, which evens out unequal lengths
+// (three sequences of 700 queries over 6000 tokens: one split 190 us, three
+// 150 us, five 177 us).
 KvPlan kv_prompt_plan(const KvAttn& a) {
   KvPlan p{};
   const int64_t rows = (int64_t)a.max_q * a.group;
   KvSplit& s = p.split;
   const int64_t heads = (int64_t)a.c.heads * a.batch;
-  p.waves = a.c.head_dim == 128 && (rows + 255) / 256 * heads >= 256 ? 8 : 4;
-  s.rows = 32 * p.waves;
+  const bool shared = a.c.head_dim < 256 && a.max_kv > 128 && (a.batch == 1 || a.max_kv <= 2048) &&
+                      (rows + 127) / 128 * heads <= 256;
+  const bool tall = a.c.head_dim == 128 && (rows + 255) / 256 * heads >= 256;
+  p.waves = shared || tall ? 8 : 4;
+  s.rows = tall ? 256 : 128;
   s.tiles = (int)((rows + s.rows - 1) / s.rows);
   s.kept = (int)(rows < s.rows ? rows : s.rows);
   const int64_t base = s.tiles * heads;
-  const int64_t slots = a.c.head_dim == 64 ? 768 : a.c.head_dim == 128 && p.waves == 4 ? 512 : 256;   // resident
-  int64_t splits = 2 * slots / base;
+  const int64_t slots = p.waves == 8 || a.c.head_dim == 256 ? 256 : a.c.head_dim == 128 ? 512 : 768;   // resident
+  int64_t splits = (a.batch > 1 && !shared ? 2 : 1) * slots / base;
   const int64_t most = ((int64_t)a.max_kv + 511) / 512;
   if (splits > most) splits = most;
   if (splits < 1) splits = 1;

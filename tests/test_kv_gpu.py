@@ -303,6 +303,12 @@ ATTENTION = [
     ([400, 513], [450, 100], 16, 4, 128, 8, F16, 16, False),
     # many rows over a longer context: split; rows around the border between the two kernels
     ([150, 141], [4000, 2222], 1, 2, 64, 4, F16, 16, True),
+    ([150, 141], [4000, 2222], 1, 2, 128, 8, F16, 16, True),
+    ([200, 130], [100, 128], 2, 2, 128, 4, BF16, 16, True),
+    ([200, 130], [77, 1], 2, 2, 64, 4, F16, 32, False),
+    ([700], [3000], 2, 2, 128, 4, BF16, 16, True),
+    ([700], [3000], 2, 2, 64, 8, F16, 64, True),
+    ([200, 130], [129, 2048], 1, 1, 64, 4, BF16, 16, False),
     ([128, 100], [300, 900], 2, 1, 128, 4, BF16, 16, True),
     ([129, 128], [300, 900], 2, 1, 256, 8, F16, 32, True),
     ([127, 33], [2000, 1029], 3, 1, 64, 8, F16, 16, False),
