@@ -10,9 +10,11 @@ namespace {
 // decodes the cached rows anew for each 32 of them, in registers, and fills
 // the card with few; the other shares the decoding among 128 or 256 through
 // LDS.  Measured, few against many, us (heads of 128 in 4 bits, 8 key heads):
-//   4 sequences of 8192 tokens:    40 rows 31 / 39, 72 rows 42 / 45, 128 rows 50 / 52, 192 rows 82 / 85
-//   32 sequences of 2048 tokens:   40 rows 49 / 91, 72 rows 64 / 94, 128 rows 77 / 102, 256 rows 136 / 125
-//   64 sequences of 512 tokens:    72 rows 53 / 55, 128 rows 60 / 58, 256 rows 111 / 72
+//   4 sequences of 8192 tokens:    40 rows 31 / 39, 72 rows 42 / 44, 128 rows 51 / 51, 192 rows 82 / 85
+//   32 sequences of 2048 tokens:   40 rows 41 / 81, 72 rows 60 / 78, 128 rows 72 / 80, 256 rows 136 / 125
+//   64 sequences of 512 tokens:    40 rows 33 / 52, 72 rows 46 / 54, 128 rows 60 / 58, 256 rows 111 / 72
+//   1 sequence of 300 tokens:      40 rows 12 / 17, 128 rows 12 / 19
+//   4 of 8192, heads of 256:       40 rows 49 / 101, 128 rows 82 / 138, 256 rows 243 / 209
 bool few_rows(const KvAttn& a) { return (int64_t)a.max_q * a.group <= 128; }
 
 }  // namespace

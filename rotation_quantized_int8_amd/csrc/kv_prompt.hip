@@ -4,8 +4,8 @@
 // The mathematics is that of the single-token kernel (kv_decode.hip): rotate
 // the queries once, use the codes as they are with their scales outside the
 // products, rotate the result back.  Here the arithmetic counts, so a
-// workgroup of 4 (8) wavefronts takes 128 (256) rows (queries times heads of
-// one group) and shares the decoding: of each 64 (128) tokens every wavefront
+// workgroup of 4 (8) wavefronts takes 128 (256, or 128 with half of the tokens
+// each) rows (queries times heads of one group) and shares the decoding: of each 64 (128) tokens every wavefront
 // turns the codes of 16 into fp16 (exact) and writes them to LDS in the order
 // in which the matrix instructions take their operands (16 bytes a lane, no
 // bank conflicts), two buffers deep, so that a step costs one barrier.
@@ -31,9 +31,9 @@
 // the two wavefronts of a SIMD overlap only in part.  Measured: 4096 causal
 // queries of 32 heads over 8 key heads, D 128, bf16, 4 bits: 169 us, 812
 // TFLOP/s, against 1220 of a large matrix product; three chunks of up to 701
-// queries, 24 heads over 8, D 64, fp16, 8 bits, contexts of up to 6007: 128
-// us, 347 TFLOP/s (the remainder's product is not counted); 1024 queries of 16
-// heads over 512 states, twice: 30 us.  Three wavefronts a SIMD for heads of
+// queries, 24 heads over 8, D 64, fp16, 8 bits, contexts of up to 6007: 129
+// us, 344 TFLOP/s (the remainder's product is not counted); 1024 queries of 16
+// heads over 512 states, twice: 26 us.  Three wavefronts a SIMD for heads of
 // 128, steps of 32 tokens, the two halves of a step offset between the
 // wavefronts, and the next scores formed before the outputs were no faster.
 
