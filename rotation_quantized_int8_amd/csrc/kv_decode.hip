@@ -111,9 +111,11 @@ __device__ __forceinline__ constexpr int query_place(int d) {
 
 // O^T operands of output tiles i .. i + 3: of 8 tokens' words, four half pairs
 // a tile.  A code enters as the fp16 number whose bits are c + 8 (c + 128 for
-// 8 bits), the subnormal (c + 8) 2^-24, and the sum of the weights times the
-// offset is taken off at the end: a mask and an exclusive or make the
-// operand.  With 4-bit codes the odd tiles hold 16 (c + 8).
+// 8 bits), a subnormal, and the sum of the weights times the offset is taken
+// off at the end.  4 bits enter 6 bits up, as (c + 8) 2^-18: the products of a
+// matrix instruction are cut off below the largest as if a subnormal's leading
+// zeros were digits, and at the bottom of the mantissa 18732 even tokens cost
+// an output 5e-4 of itself.
 template <int D, int BITS>
 __device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Ring<D, BITS>::kValueWords], int i,
                                                v4u (&f)[4]) {
@@ -122,15 +124,16 @@ __device__ __forceinline__ void value_operands(const uint32_t (&v)[2][4][Ring<D,
     const uint32_t* a = v[p / 2][2 * (p % 2)];
     const uint32_t* b = v[p / 2][2 * (p % 2) + 1];
     if constexpr (BITS == 4) {
-      const uint32_t x = __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u), y = x >> 8;
-      f[0][p] = (x & 0x000F000Fu) ^ 0x00080008u;
-      f[1][p] = (x & 0x00F000F0u) ^ 0x00800080u;
-      f[2][p] = (y & 0x000F000Fu) ^ 0x00080008u;
-      f[3][p] = (y & 0x00F000F0u) ^ 0x00800080u;
+      const uint32_t x =
+          __builtin_amdgcn_perm(b[i / 8], a[i / 8], i % 8 ? 0x07060302u : 0x05040100u) ^ 0x88888888u;
+      f[0][p] = x << 6 & 0x03C003C0u;
+      f[1][p] = x << 2 & 0x03C003C0u;
+      f[2][p] = x >> 2 & 0x03C003C0u;
+      f[3][p] = x >> 6 & 0x03C003C0u;
     } else {
+      const uint32_t x = a[i / 4] ^ 0x80808080u, y = b[i / 4] ^ 0x80808080u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        f[e][p] = __builtin_amdgcn_perm(b[i / 4], a[i / 4], 0x0C040C00u + (uint32_t)e * 0x00010001u) ^ 0x00800080u;
+      for (int e = 0; e < 4; ++e) f[e][p] = __builtin_amdgcn_perm(y, x, 0x0C040C00u + (uint32_t)e * 0x00010001u);
     }
   }
 }
@@ -526,7 +529,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i)
           sh.o[wave][col][PASS * (4 * quad + e) + i] =
-              __fmaf_rn(o[t][PASS * p + i][e], BITS == 4 && i % 2 ? 0x1p20f : 0x1p24f, offset) * mine;
+              __fmaf_rn(o[t][PASS * p + i][e], BITS == 4 ? 0x1p18f : 0x1p24f, offset) * mine;
       __syncthreads();
       // four wavefronts sum four; with more, each group of four its own, and then the first four the groups
       const int g = wave / 4;
