@@ -21,11 +21,16 @@
 //                   and interleaves pairs of tokens by byte permutes.
 // W = p scale' with p = 2^(score - m + 8) and m the running maximum of
 // score + log2 scale', so fp16 keeps weights down to 2^-32 of the largest.
+// For fp16 outputs what their rounding leaves takes a second product: left
+// out, it costs few rows up to the outputs' own rounding again (error 2.0 times
+// the plain form's at worst over 700 draws, with it 1.1; one token over 1000
+// 12.4 -> 12.8 us, larger calls level).  Next to a bf16 output's it is nothing.
 // m is raised only when a weight passes 2^15, so most steps neither reduce
 // over lanes nor rescale, and no maximum is needed before the exponential.
 // The values' codes enter with an offset of 8 (see value_operands), which
-// costs the outputs 2^-24 of 8 sum W against a mean that is smaller than it
-// by sqrt(tokens) at worst: below fp16's own rounding up to 10^6 even tokens.
+// costs a wavefront's sums about 2^-24 of 8 sum W a step, against a mean that
+// is smaller than sum W by sqrt(tokens) where they are even: at most 8192
+// tokens of a wavefront make that 1e-4 of an output.
 //
 // What bounds it: HBM (each cached row is read once for up to 32 rows of its
 // key head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
@@ -39,7 +44,7 @@
 // (174 MB): 37.9 us and 5.3 us for the join (4.6 TB/s in the kernel); two
 // sequences of 131072 tokens, 4 key heads of 8 (143 MB): 30.5 and 5.2 us (4.7
 // TB/s); 48 of up to 2501 tokens, 4 key heads of 5, D 256, 8 bits (164 MB):
-// 41 us in one launch (4.0 TB/s).  One token over 1000 of 16 heads: 11.8 us,
+// 41 us in one launch (4.0 TB/s).  One token over 1000 of 16 heads: 12.2 us,
 // the latency of the prologue, two steps and the join of the wavefronts.
 // What is left to the copy's rate is the start (lengths, pages, the rotation
 // of the queries, about 4 us a workgroup before the first product) and the
@@ -342,6 +347,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
   }
 
   v4f o[QT][E];
+  const bool fine = !a.bf16;                           // fp16 outputs: the weights' rounding takes a second product
   v4f weight[QT];                                      // sum of the rounded weights (four times the same)
   float base[QT], l[QT];
 #pragma unroll
@@ -415,7 +421,7 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 
     // ---- weights
     auto seen = [&](int t, int u, int r) { return (16 * u + 4 * r < end[t] - j0 - quad) & here[u]; };
-    v8h w[QT];
+    v8h w[QT], left_over[QT];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       float x[8], sum;
@@ -457,6 +463,12 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) packed[e] = pack_f16x2_rn(x[2 * e], x[2 * e + 1]);
       w[t] = __builtin_bit_cast(v8h, packed);
+      if (fine) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          packed[e] = pack_f16x2_rn(x[2 * e] - (float)w[t][2 * e], x[2 * e + 1] - (float)w[t][2 * e + 1]);
+        left_over[t] = __builtin_bit_cast(v8h, packed);
+      }
     }
 
     // ---- outputs; then the next values load
@@ -483,7 +495,10 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
       }
     const v8h ones = {1, 1, 1, 1, 1, 1, 1, 1};
 #pragma unroll
-    for (int t = 0; t < QT; ++t) weight[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, w[t], weight[t], 0, 0, 0);
+    for (int t = 0; t < QT; ++t) {
+      weight[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, w[t], weight[t], 0, 0, 0);
+      if (fine) weight[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, left_over[t], weight[t], 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < E; i += 4) {
       v4u f[4];
@@ -493,6 +508,13 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
         for (int t = 0; t < QT; ++t)
           o[t][i + n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f[n]), w[t], o[t][i + n], 0, 0, 0);
+      if (fine) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+            o[t][i + n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, f[n]), left_over[t], o[t][i + n], 0, 0, 0);
+      }
     }
     if (refill) {
       __builtin_amdgcn_s_waitcnt(0xC07F);
