@@ -99,8 +99,8 @@ size_t convrot_kv_workspace_bytes(const convrot_kv_cache* cache, int64_t T, int6
  * maximum and the scores are exact sums in int32; for more rows fp16 queries
  * enter as two fp16 numbers, bf16 queries as one.  The softmax weights enter
  * as fp16, at 2^8 and more for the largest, and for fp16 outputs of up to 128
- * rows as two fp16 numbers.  O must not overlap an input; the workspace (may be NULL where 0
- * bytes are needed) must not overlap anything. */
+ * rows as two fp16 numbers.  O must not overlap an input; the workspace (may
+ * be NULL where 0 bytes are needed) must not overlap anything. */
 convrot_status convrot_kv_attention(const convrot_kv_cache* cache, const void* Q, int64_t q_token_stride,
                                     int64_t q_head_stride, int dtype, int64_t T, int64_t q_heads,
                                     const int32_t* table, int64_t table_width, int64_t batch,
