@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
 // unit.  The chunk starts at the mean that gives `balance` units and, where
 // there are at least twice as many units as sequences, grows until the units
 // are no more than that, so that they all run at once.  A lane looks at WORDS
-// sequences.
+// sequences, so all 64 lanes of the wavefront have to call it together.
 struct KvUnits {
   int b, first, n, chunk;
   KvSeq seq;

@@ -621,14 +621,16 @@ __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn
   const int sub = threadIdx.x / 16 % SEGS, seg = threadIdx.x % 16, h = blockIdx.y, b = blockIdx.z;
   const int row = blockIdx.x * PER + threadIdx.x / 16 / SEGS % PER;   // of the sequence's with this key head
   const int tile = row / sp.rows, rr = row - tile * sp.rows;
-  if (tile >= sp.tiles || rr >= sp.kept) return;
   int first = b * sp.splits, n = sp.splits, chunk = sp.chunk;
   KvSeq s;
   if (sp.balance) {
-    const KvUnits u = kv_units(a, sp, b, 0);
+    const KvUnits u = kv_units(a, sp, b, 0);           // takes all 64 lanes: before any returns
     first = u.first, n = u.n, chunk = u.chunk, s = u.seq;
     if (n == 1) return;                                // written by its only unit
   }
+  // With SEGS = 1 a wavefront has four rows, of which some may end here and below; from here on lanes of one row
+  // meet only, and with more segments a wavefront, or all that meet, has one row.
+  if (tile >= sp.tiles || rr >= sp.kept) return;
   // the first 16 splits' maxima and sums, without waiting for the sequence's lengths
   const int64_t at = sp.row(h, tile, first, rr);
   int z = sub + seg * SEGS;                            // this lane's split
@@ -639,7 +641,7 @@ __global__ __launch_bounds__(SEGS == 64 ? 1024 : 256) void kv_join_kernel(KvAttn
   }
   if (!sp.balance) s = kv_sequence(a, b);
   const int i = kv_query_of(a, row);
-  if (i >= s.n) return;                                // uniform in a wavefront, and where wavefronts meet
+  if (i >= s.n) return;
   // the splits that the row's tile ran: up to the last token its last row sees
   int last = s.kv;
   if (a.causal) {

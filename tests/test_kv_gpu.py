@@ -404,6 +404,35 @@ def test_attention_walks_long_contexts_alone(n, m, heads, d):
     _check_attention(part, q[:, some], table, [n], [m], True, got[:, some])
 
 
+@pytest.mark.parametrize("n,heads,group,d,batch", [(18, 512, 1, 64, 2), (17, 520, 1, 128, 2), (11, 448, 2, 64, 4),
+                                                   (5, 1100, 1, 128, 3), (19, 300, 1, 256, 3), (20, 512, 1, 64, 2)])
+@pytest.mark.parametrize("q_each", [False, True])
+def test_attention_joins_rows_that_share_a_wavefront(n, heads, group, d, batch, q_each):
+    """Units of equal work over unequal lengths, and so many rows that the join puts four into a wavefront: a tile's
+    rows end inside one where their number is no multiple of four.  Three heads are compared."""
+    _say("join of shared wavefronts", n, heads, group, d, batch, q_each)
+    g = _gen(n, heads, d)
+    kv_lens = [5003, 300, 2700, 1][:batch]
+    pages = sum(-(-m // 16) for m in kv_lens)
+    dev = torch.Generator(device=DEV)
+    dev.manual_seed(n)
+    shape = (pages, heads, 16)
+    codes = [torch.randint(-7, 8, (*shape, d), dtype=torch.int8, device=DEV, generator=dev) for _ in range(2)]
+    scales = [torch.rand(shape, device=DEV, generator=dev) * 0.1 for _ in range(2)]
+    packed = [((c[..., 0::2] & 15) | (c[..., 1::2] << 4)).view(torch.uint8) for c in codes]
+    cache = cr.KVCache(packed[0], scales[0], packed[1], scales[1])
+    table, lens = _sequences(g, cache, kv_lens)
+    q_lens = [n - (i % 3 if q_each else 0) for i in range(batch)]
+    q = torch.randn((sum(q_lens), heads * group, d), generator=g).half().to(DEV)
+    got = cr.kv_attention(cache, q, table, lens, q_start=_starts(q_lens) if q_each else None, max_q=n,
+                          max_kv=max(kv_lens), out=torch.full_like(q, float("nan")))
+    some = torch.tensor([0, heads // 2 + 1, heads - 1])
+    rows = (some[:, None] * group + torch.arange(group)).flatten()
+    part = cr.KVCache(*(t[:, some].contiguous() for t in (cache.k_codes, cache.k_scale, cache.v_codes, cache.v_scale)))
+    assert got.isfinite().all()
+    _check_attention(part, q[:, rows], table, q_lens, kv_lens, True, got[:, rows])
+
+
 @pytest.mark.parametrize("rows", [1, 40, 140])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_attention_value_rows_of_all_sizes(rows, bits):
