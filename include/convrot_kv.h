@@ -96,8 +96,9 @@ size_t convrot_kv_workspace_bytes(const convrot_kv_cache* cache, int64_t T, int6
  * that see its token and in no other.  Sums, maxima and accumulators are fp32.
  * For up to 128 query rows (queries times heads of a group) per key head the
  * rotated queries enter the matrix cores as 16-bit fixed point of their row's
- * maximum and the scores are exact sums in int32; for more rows fp16 queries
- * enter as two fp16 numbers, bf16 queries as one.  The softmax weights enter
+ * maximum and the scores are exact sums in int32; for more rows, after a power
+ * of two of the row's own, fp16 queries enter as two fp16 numbers, bf16 queries
+ * as one.  Either way a row is as exact next to any other.  The softmax weights enter
  * as fp16, at 2^8 and more for the largest, and for fp16 outputs of up to 128
  * rows as two fp16 numbers.  O must not overlap an input; the workspace (may
  * be NULL where 0 bytes are needed) must not overlap anything. */

@@ -13,20 +13,22 @@
 //   O^T = C_v^T W^T   the same, 32 elements x 32 rows
 // A lane owns one row (column lane % 32); the result layout of S^T is the
 // operand layout of W^T up to an order of the tokens that C_v^T is stored in.
-// The rotated queries are rounded to fp16 after a power of two common to the
-// workgroup.  For fp16 rows the remainder, rounded again, takes a second
-// product into the same accumulator: left out, it would cost the outputs
-// twice their own rounding (measured: 4.1e-4 against 2.1e-4, with it 2.8e-4);
-// next to the rounding of a bf16 output it is nothing.  The weights are
-// rounded to fp16 (2^-11 of each at most, to nearest) as for few rows, so
-// a sum of many is off by less than the output's own rounding.  The unit,
-// sm_scale and log2 e are multiplied into the keys' scales, so
-// a weight is exp2(fma(S, scale_j, base_row)): one operation, its exponential,
-// its share of the sum and the product with the value's scale.  The running
+// The rotated queries are rounded to fp16 after a power of two of the row's
+// own, which brings its largest element to 2^9 .. 2^10, far from both ends of
+// fp16 (one common to the workgroup spares the product with it below, 2 % of
+// the large prompts, but loses a row next to one 2^16 times as loud).  For
+// fp16 rows the remainder, rounded again, takes a second product into the same
+// accumulator: left out, it would cost the outputs twice their own rounding
+// (measured: 4.1e-4 against 2.1e-4, with it 2.8e-4); next to the rounding of a
+// bf16 output it is nothing.  The weights are rounded to fp16 (2^-11 of each
+// at most, to nearest), so a sum of many is off by less than the output's own
+// rounding.  sm_scale and log2 e are multiplied into the keys' scales, so a
+// weight is exp2(fma(S, scale_j unit_row, base_row)): two operations, its
+// exponential, its share of the sum and the product with the value's scale.  The running
 // maximum is raised only when a weight could pass 2^15 (they start at 2^8 for
 // the largest).
 //
-// What bounds it: the vector work on the weights (five operations a weight,
+// What bounds it: the vector work on the weights (six operations a weight,
 // the exponential at a quarter of the rate) next to the matrix products, which
 // the two wavefronts of a SIMD overlap only in part.  Measured: 4096 causal
 // queries of 32 heads over 8 key heads, D 128, bf16, 4 bits: 169 us, 812
@@ -111,7 +113,6 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
   __shared__ __align__(16) float kscale[2][kStep], vscale[2][kStep];
   __shared__ __align__(16) int absent[2][WAVES];
   __shared__ __align__(16) float vtop[2][WAVES];      // largest value scale of each group
-  __shared__ float qtop[WAVES];
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 32, hi = lane / 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -149,10 +150,12 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
     const int j = c0 + kStep * step + 16 * wave, p = __builtin_amdgcn_readlane(pages, step % 64);
     present = p >= 0;
     const int64_t row = (((int64_t)(p < 0 ? 0 : p) * a.c.heads + h) << log2p) + (j & ((1 << log2p) - 1));
+    uint32_t key = koff;                               // (opaque: the compiler would keep kc + koff, two registers a lane)
+    asm volatile("" : "+v"(key));
     const uint8_t* kbase = a.c.kc + row * P::kRow;
     const uint8_t* vbase = a.c.vc + row * P::kRow;
 #pragma unroll
-    for (int i = 0; i < P::kKeyEach; ++i) rawk[i] = *reinterpret_cast<const v4u*>(kbase + (koff + i * 64));
+    for (int i = 0; i < P::kKeyEach; ++i) rawk[i] = *reinterpret_cast<const v4u*>(kbase + (key + i * 64));
 #pragma unroll
     for (int i = 0; i < P::kValueEach; ++i) {
       const int task = (lane + 64 * i) % P::kTasks;
@@ -171,7 +174,10 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
   // result layout is, in pairs of registers, the operand layout of the scores: lane (column = row, hi), step k, holds
   // elements 4 hi .. 4 hi + 3 of units 2 k and 2 k + 1, alternating.
   const int myrow = tile * kRows + 32 * group + col, myquery = kv_query_of(a, myrow);
-  float common;                                        // what a score's product is multiplied by, without the key's scale
+  // what a score's product is multiplied by: sm_scale, the rotation's 1 / sqrt(D) and log2 e, in the keys' scales (the
+  // sign of sm_scale is the queries'), and the unit of this lane's row
+  const float common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f;
+  float unit;
   v8h q[P::kSteps], left_over[BF16 ? 1 : P::kSteps];        // fp16 rows: and what the rounding leaves
   {
     v16f x[P::kTiles];
@@ -215,18 +221,11 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
     for (int t = 0; t < P::kTiles; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[t][r]));
-    top = top < INFINITY ? top : 0.0f;                 // (a row with an infinity or a NaN has no finite element)
-    top = wave_max64(top);
-    if (lane == 0) qtop[wave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) top = fmaxf(top, qtop[v]);
-    // 2^e above the largest, so that the queries enter below 1
-    const uint32_t e2 = (__float_as_uint(top) >> 23) + 1u;
-    const float unit = __uint_as_float((e2 < 1u ? 1u : e2 > 253u ? 253u : e2) << 23);
+    top = max32(top);
+    // (a row with an infinity or a NaN has no finite element, and shows NaN)
+    const uint32_t e2 = __float_as_uint(top) >> 23;
+    unit = top < INFINITY ? __uint_as_float((e2 < 10u ? 1u : e2 - 9u) << 23) : __uint_as_float(0x7FC00000u);
     const float by = (a.scale < 0.0f ? -1.0f : 1.0f) / unit, odd = BITS == 4 ? by * 0.0625f : by;
-    // sm_scale, the rotation's 1 / sqrt(D), log2 e and the queries' unit
-    common = fabsf(a.scale) * kv_rsqrt(D) * 1.44269504088896340736f * unit;
 #pragma unroll
     for (int k = 0; k < P::kSteps; ++k) {
       v4u y, z;
@@ -326,7 +325,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
       for (int r = 0; r < 16; r += 4) {
         const v4f ks = *reinterpret_cast<const v4f*>(&kscale[buf][32 * kt + 2 * r + 4 * hi]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[r + i] = __builtin_amdgcn_exp2f(__fmaf_rn(z[r + i], ks[i], base));
+        for (int i = 0; i < 4; ++i) z[r + i] = __builtin_amdgcn_exp2f(__fmaf_rn(z[r + i], ks[i] * unit, base));
       }
       if (!whole) {
 #pragma unroll
@@ -344,7 +343,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
         const v4f vs = *reinterpret_cast<const v4f*>(&vscale[buf][32 * kt + 2 * r + 4 * hi]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float y = z[r + i] * ks[i] + __builtin_amdgcn_logf(fmaxf(vs[i], kLeastScale));
+          const float y = z[r + i] * (ks[i] * unit) + __builtin_amdgcn_logf(fmaxf(vs[i], kLeastScale));
           best = fmaxf(best, (whole | seen(r + i)) ? y : kLowest);
         }
       }

@@ -1,0 +1,146 @@
+"""Attention over the key/value cache against 64 bits, with the terms of the
+kernel that runs (test_kv_gpu.py allows every kernel the roundings of all).
+
+A score is off by at most  delta = |scale| max|k| (e + 2^-20 |q|)  (2-norms),
+2^-20 for the fp32 arithmetic of a score and e for the rotated query as it
+enters the matrix cores; with top = max |q W| of the row (W the +-1 matrix):
+  up to 128 rows per key head: 16-bit fixed point of the row's own maximum,
+          half a step of top / 32512, and fp32 butterflies:
+          e = top / 65024 + 2^-21 sqrt(D) |q|;
+  more rows, fp16: two fp16 numbers (2^-22, and the end of fp16's range, 2^-30
+          of the row's maximum), and fp32 sums of the rotation:
+          e = 2^-21 top + 2^-19 sqrt(D) |q|;
+  more rows, bf16: one fp16 number: 2^-11 |q| more.
+A weight is off, through itself and the sum, by 2 delta of itself, and by its
+rounding: 2^-11 for one fp16 number, 2^-21 for two (fp16, up to 128 rows).
+The sums over n tokens: up to 128 rows a wavefront adds 32 tokens at a time to
+sums that hold the codes' offset (up to 15, or 255, where a row's codes have a
+2-norm of at least 2, or 32, sqrt(D) in these tests: 8 times the value, 2^-23
+each), 4 wavefronts and their join; more rows, 16 tokens at a time without an
+offset.  With both,
+  rel = expm1(2 delta) + rounding + (n / 128 + 16) 2^-20       (up to 128 rows)
+  rel = expm1(2 delta) + rounding + (n / 16 + 64) 2^-22        (more).
+H keeps 2-norms, so the error of an output row before its own rounding has a
+2-norm of at most rel sum_j p_j |v_j|, and so has each element; the rounding
+adds half a step of the output, to an element and in the 2-norm.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import rotation_quantized_int8_amd as cr
+from oracle import kv_oracle as O
+from test_kv_gpu import BF16, DEV, F16, _check_attention, _gen, _host_rows, _np, _random_cache, _say, _sequences
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    cr.lib()
+    torch.cuda.set_device(0)
+
+
+def _half_step(x, dtype):
+    """Half the distance of dtype's neighbours at |x|."""
+    f = torch.finfo(dtype)
+    return 2.0 ** np.floor(np.log2(np.maximum(np.abs(x), f.smallest_normal))) * f.eps / 2
+
+
+def _check(cache, q, table, q_lens, kv_lens, causal, got, scale=None, tell=""):
+    d, group = cache.head_dim, q.shape[1] // cache.heads
+    scale = d ** -0.5 if scale is None else scale
+    few, fp16 = max(q_lens) * group <= 128, q.dtype == F16
+    at, worst = 0, 0.0
+    for b, (n, m) in enumerate(zip(q_lens, kv_lens)):
+        k, v, here = _host_rows(cache, table[b].cpu().numpy(), m)
+        assert here.all()
+        qb = _np(q[at:at + n])
+        o, spread = O.attention(qb, k, v, scale, causal)
+        size = np.linalg.norm(qb, axis=-1)
+        top = np.abs(qb @ O.signs(d)).max(-1)
+        if few:
+            e = top / 65024 + 2.0 ** -21 * d ** 0.5 * size
+        else:
+            e = 2.0 ** -21 * top + 2.0 ** -19 * d ** 0.5 * size + (0.0 if fp16 else 2.0 ** -11 * size)
+        delta = abs(scale) * (np.linalg.norm(k, axis=-1).max() if m else 0.0) * (e + 2.0 ** -20 * size)
+        rel = np.expm1(np.minimum(2 * delta, 3.0)) + (2.0 ** -21 if few and fp16 else 2.0 ** -11)
+        rel += (m / 128 + 16) * 2.0 ** -20 if few else (m / 16 + 64) * 2.0 ** -22
+        room = rel * spread[..., 0]
+        y = _np(got[at:at + n])
+        assert np.isfinite(y).all(), tell
+        off, step = np.abs(y - o), _half_step(y, got.dtype)
+        for share in (off / (step + room[..., None]),
+                      np.linalg.norm(off, axis=-1) / (np.linalg.norm(step, axis=-1) + room)):
+            if share.size:
+                worst = max(worst, float(share.max()))
+                assert share.max() <= 1.0, (tell, b, n, m, float(share.max()), np.argwhere(share > 1.0)[:4].tolist())
+        at += n
+    _say("   largest share of the bound:", tell, round(worst, 3))
+
+
+def _plain_table(m, page=16):
+    return (torch.arange(-(-m // page), dtype=torch.int32, device=DEV)[None],
+            torch.tensor([m], dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.parametrize("dtype,loud", [(F16, 2.0 ** 6), (F16, 2.0 ** 12), (BF16, 2.0 ** 6), (BF16, 2.0 ** 12),
+                                        (BF16, 2.0 ** 20), (BF16, 2.0 ** -20)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [40, 300])
+def test_a_loud_row_leaves_its_neighbours_alone(rows, d, bits, dtype, loud):
+    """One query row far above (or below) the others of its tile, in another query and another head."""
+    _say("loud row", rows, d, bits, dtype, loud)
+    g = _gen(d, bits, rows)
+    m = 600
+    cache = _random_cache(g, -(-m // 16), 16, 1, d, bits)
+    table, lens = _sequences(g, cache, [m])
+    q = torch.randn((rows // 2, 2, d), generator=g)
+    q[7, 1] *= loud
+    q = q.to(dtype).to(DEV)
+    got = cr.kv_attention(cache, q, table, lens)
+    assert got.isfinite().all()
+    _check_attention(cache, q, table, [rows // 2], [m], True, got)
+    _check(cache, q, table, [rows // 2], [m], True, got)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rows", [40, 300])
+def test_rows_of_all_sizes_in_one_tile(rows, bits, dtype):
+    _say("rows of all sizes", rows, bits, dtype)
+    g = _gen(bits, rows)
+    m, d = 600, 128
+    cache = _random_cache(g, -(-m // 16), 16, 1, d, bits)
+    table, lens = _sequences(g, cache, [m])
+    size = torch.exp2(torch.linspace(*((-8, 12) if dtype == F16 else (-20, 20)), rows))
+    q = (torch.randn((rows, 1, d), generator=g) * size[torch.randperm(rows, generator=g)][:, None, None]).to(dtype)
+    q[3] = 0
+    q = q.to(DEV)
+    got = cr.kv_attention(cache, q, table, lens, causal=False)
+    _check_attention(cache, q, table, [rows], [m], False, got)
+    _check(cache, q, table, [rows], [m], False, got)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rows", [40, 140, 300])
+def test_queries_whose_rounding_tells_two_keys_apart(rows, bits, d):
+    """q = X e0 + Y e1 with X + Y odd above 2048, so that one fp16 number of the rotated query is off by 1, and keys
+    along e0 and e1 whose scores, near 100, balance: with one number a weight would be off by a hundredth."""
+    _say("queries' second number", rows, bits, d)
+    g = _gen(rows, bits, d)
+    table, lens = _plain_table(2)
+    cache = cr.KVCache.empty(1, 16, 1, d, bits, DEV)
+    k, v = torch.zeros((2, 1, d)), torch.randn((2, 1, d), generator=g)
+    k[0, 0, 0], k[1, 0, 1] = 1.0, 1501.0 / 600.0
+    cr.kv_append(cache, k.half().to(DEV), v.half().to(DEV), torch.arange(2, device=DEV))
+    q = torch.zeros((rows, 1, d))
+    q[:, 0, 0], q[:, 0, 1] = 1501.0 + 2.0 * (torch.arange(rows) % 8), 600.0
+    q = q.half().to(DEV)
+    got = cr.kv_attention(cache, q, table, lens, scale=1.0 / 15.0, causal=False)
+    _check(cache, q, table, [rows], [2], False, got, scale=1.0 / 15.0)
