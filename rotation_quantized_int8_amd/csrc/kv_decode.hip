@@ -27,10 +27,11 @@
 // 12.4 -> 12.8 us, larger calls level).  Next to a bf16 output's it is nothing.
 // m is raised only when a weight passes 2^15, so most steps neither reduce
 // over lanes nor rescale, and no maximum is needed before the exponential.
-// The values' codes enter with an offset of 8 (see value_operands), which
-// costs a wavefront's sums about 2^-24 of 8 sum W a step, against a mean that
-// is smaller than sum W by sqrt(tokens) where they are even: at most 8192
-// tokens of a wavefront make that 1e-4 of an output.
+// The values' codes enter with an offset of 8 or 128 (see value_operands), so
+// the sums round at 2^-24 of 8 (128) sum W where even tokens leave a mean that
+// is smaller than sum W by sqrt(tokens).  The offset is taken off every 64 steps
+// (2048 tokens), which keeps that at 3e-5 of an output for any context; taken
+// off at the end alone it comes to 6e-4 over 131072 tokens in one workgroup.
 //
 // What bounds it: HBM (each cached row is read once for up to 32 rows of its
 // key head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
@@ -117,7 +118,7 @@ __device__ __forceinline__ constexpr int query_place(int d) {
 // O^T operands of output tiles i .. i + 3: of 8 tokens' words, four half pairs
 // a tile.  A code enters as the fp16 number whose bits are c + 8 (c + 128 for
 // 8 bits), a subnormal, and the sum of the weights times the offset is taken
-// off at the end.  4 bits enter 6 bits up, as (c + 8) 2^-18: the products of a
+// off later.  4 bits enter 6 bits up, as (c + 8) 2^-18: the products of a
 // matrix instruction are cut off below the largest as if a subnormal's leading
 // zeros were digits, and at the bottom of the mantissa 18732 even tokens cost
 // an output 5e-4 of itself.
@@ -413,7 +414,15 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
         for (int r = 0; r < 4; ++r) sc[t][u][r] = (sc[t][u][r] << 8) + lo[t][r];
     }
     if (refill) {
-      if ((step + S) % 64 == 0) find_pages(step + S);
+      if ((step + S) % 64 == 0) {
+        find_pages(step + S);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {                   // the values' offset comes off
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[t][i] += weight[t][0] * (BITS == 4 ? -0x1p-15f : -0x1p-17f);
+          weight[t] = (v4f){0, 0, 0, 0};
+        }
+      }
       find_rows(step + S, stage);
       __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the reads are done
       load_keys(row0, row1, stage);

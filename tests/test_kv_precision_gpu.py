@@ -144,3 +144,40 @@ def test_queries_whose_rounding_tells_two_keys_apart(rows, bits, d):
     q = q.half().to(DEV)
     got = cr.kv_attention(cache, q, table, lens, scale=1.0 / 15.0, causal=False)
     _check(cache, q, table, [rows], [2], False, got, scale=1.0 / 15.0)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_many_even_tokens_in_one_workgroup(bits):
+    """131072 tokens of equal scores, so many heads that a workgroup walks them all; 16 heads are compared.  The mean
+    of the values is 1 / 362 of one, and the sums that hold the codes' offset are 8 (128) times one: restarted every
+    64 steps of 32 tokens their rounding (2 products a step of at most 2^-24 of a sum that grows to 15, 255 times the
+    weights, independent) comes to 3e-5 of the mean; 4 times that, and the output's own rounding, are allowed."""
+    _say("many even tokens", bits)
+    d, heads, page, m = 64, 1024, 256, 131072
+    dev = torch.Generator(device=DEV)
+    dev.manual_seed(bits)
+    shape = (m // page, heads, page)
+    if bits == 4:                                          # nibbles 9 .. 15, 0 .. 7
+        v = torch.randint(0, 15, (*shape, d // 2), dtype=torch.uint8, device=DEV, generator=dev).add_(9).bitwise_and_(15)
+        high = torch.randint(0, 15, (*shape, d // 2), dtype=torch.uint8, device=DEV, generator=dev).add_(9).bitwise_and_(15)
+        v.bitwise_or_(high.mul_(16))
+        del high
+    else:
+        v = torch.randint(-127, 128, (*shape, d), dtype=torch.int8, device=DEV, generator=dev)
+    scale = torch.rand(shape, device=DEV, generator=dev).mul_(0.01).add_(0.01)
+    cache = cr.KVCache(torch.zeros_like(v), scale, v, scale)
+    table = torch.arange(m // page, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([m], dtype=torch.int32, device=DEV)
+    got = cr.kv_attention(cache, torch.zeros((1, heads, d), dtype=F16, device=DEV), table, lens)
+    h = torch.tensor(O.signs(d), device=DEV)
+    for a in range(0, heads, 64):
+        raw = v[:, a].reshape(m, -1)
+        if bits == 4:
+            b = raw.int()
+            raw = torch.stack([((b & 15) ^ 8) - 8, ((b >> 4) ^ 8) - 8], -1).flatten(-2)
+        mean = (raw.double() * scale[:, a].reshape(m, 1).double()).mean(0)
+        o = ((mean[None] @ h)[0] / d ** 0.5).cpu()
+        y = got[0, a].double().cpu()
+        off, own, size = (y - o).norm().item(), (o.half().double() - o).norm().item(), o.norm().item()
+        _say("   error", off / size, "of it the output's rounding", own / size)
+        assert off <= (1.1 * own ** 2 + (2.0 ** -13 * size) ** 2) ** 0.5
