@@ -48,13 +48,6 @@ hipError_t launch_kv_prompt(const KvAttn& a, const KvPlan& p, void* workspace, h
 // The finished rows from the splits' partial ones.
 hipError_t launch_kv_join(const KvAttn& a, const KvSplit& sp, hipStream_t stream);
 
-// a b, and 0 where a is 0 whatever b is.
-__device__ __forceinline__ float mul_legacy(float a, float b) {
-  float d;
-  asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
-  return d;
-}
-
 // Maximum, and sum, with the lane whose number differs in bit 4 (and in bit 5):
 // the two results of a lane swap of v with itself are the pair's two values.
 __device__ __forceinline__ float pair32(float v, float& other) {

@@ -444,9 +444,13 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
           for (int e = 0; e < 8; ++e) p[e] = seen(t, e / 4, e % 4) ? p[e] : 0.0f;
         }
         sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        // a weight of 0 stays 0 under a NaN scale, which another row may see
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = mul_legacy(p[e], vs[e / 4][e % 4]);
+        for (int e = 0; e < 8; ++e) x[e] = p[e] * vs[e / 4][e % 4];
+        // a scale of NaN shows in the rows that see it, however small their weight, and in no others
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = seen(t, e / 4, e % 4) ? x[e] : 0.0f;
+        }
         float top = x[0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);

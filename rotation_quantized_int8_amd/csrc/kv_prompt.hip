@@ -56,6 +56,13 @@ constexpr float kMostSum = 0x1p92f;
 constexpr float kUnset = 1e30f;               // base of a row that has seen no token
 constexpr float kLowest = -1e30f;             // its maximum
 
+// a b, and 0 where a is 0 whatever b is.
+__device__ __forceinline__ float mul_legacy(float a, float b) {
+  float d;
+  asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t less(uint32_t x, float by) {
   const h2 off = {(_Float16)by, (_Float16)by};
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, x) - off);
@@ -279,8 +286,12 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
     }
     const int j = c0 + kStep * step + 16 * wave + lane % 16;
     const float v = (j < c1) & (present != 0) ? raws : 0.0f, most = warp_max16(v);
+    // a value's scale of NaN (lanes 32 on hold the values' too) makes its key's one, so that it shows in every row that
+    // sees the token, however small its weight
+    float value;
+    pair32(raws, value);
     if (lane < 16) {
-      kscale[buf][16 * wave + lane] = raws * common;
+      kscale[buf][16 * wave + lane] = value == value ? raws * common : value;
     } else if (lane < 32) {
       vscale[buf][16 * wave + lane - 16] = v;
       if (lane == 16) {

@@ -181,3 +181,24 @@ def test_many_even_tokens_in_one_workgroup(bits):
         off, own, size = (y - o).norm().item(), (o.half().double() - o).norm().item(), o.norm().item()
         _say("   error", off / size, "of it the output's rounding", own / size)
         assert off <= (1.1 * own ** 2 + (2.0 ** -13 * size) ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("rows,m", [(1, 90), (24, 90), (24, 900), (150, 210), (150, 900)])
+def test_a_nan_shows_under_a_weight_of_nothing(rows, m, d, bits):
+    """A value of NaN whose score lies 300 below the others': the queries that see it show it, the others do not."""
+    _say("NaN far below", rows, m, d, bits)
+    g = _gen(rows, m, d)
+    table, lens = _plain_table(m)
+    k, v = torch.randn((m, 1, d), generator=g) * 0.1, torch.randn((m, 1, d), generator=g)
+    q = torch.randn((rows, 1, d), generator=g) * 0.1
+    q[..., 0] = 10.0
+    for at in (m - 1 - rows // 2, m - rows, 3):
+        kk, vv = k.clone(), v.clone()
+        kk[at, 0, 0], vv[at, 0, 5] = -30.0, float("nan")
+        cache = cr.KVCache.empty(table.numel(), 16, 1, d, bits, DEV)
+        cr.kv_append(cache, kk.half().to(DEV), vv.half().to(DEV), torch.arange(m, device=DEV))
+        got = cr.kv_attention(cache, q.half().to(DEV), table, lens, scale=1.0)
+        sees = m - rows + torch.arange(rows) >= at
+        assert got[sees.to(DEV)].isnan().all()
+        assert got[~sees.to(DEV)].isfinite().all()
