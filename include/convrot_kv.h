@@ -98,7 +98,9 @@ size_t convrot_kv_workspace_bytes(const convrot_kv_cache* cache, int64_t T, int6
  * rotated queries enter the matrix cores as 16-bit fixed point of their row's
  * maximum and the scores are exact sums in int32; for more rows, after a power
  * of two of the row's own, fp16 queries enter as two fp16 numbers, bf16 queries
- * as one.  Either way a row is as exact next to any other.  The softmax weights enter
+ * as one.  Either way a row is as exact next to any other.  A row whose
+ * largest score passes 2^24 is taken with its scores scaled down to there, as
+ * fp32 could not tell their differences apart.  The softmax weights enter
  * as fp16, at 2^8 and more for the largest, and for fp16 outputs of up to 128
  * rows as two fp16 numbers.  O must not overlap an input; the workspace (may
  * be NULL where 0 bytes are needed) must not overlap anything. */

@@ -81,6 +81,28 @@ __device__ __forceinline__ float sum16_32(float v) {
   return sum32(v + w);
 }
 
+// What raises a row's maximum, `best` log2 units, past base (weights are 2^(score + base)): base as its next value,
+// and what the row's sums are multiplied by.  fp32 holds scores past 2^25 in steps of 4 and more, where their sums
+// with base are no small numbers any more; such a row's factor, and with it all of its scores, shrink by a power of
+// two that brings `best` below.  Its softmax is then flatter by what no query's rounding tells apart: weights change
+// where scores differ by less than 2^-17 of the largest.
+constexpr float kWeightBits = 8.0f;           // the largest weight is 2^8
+constexpr float kUnset = 1e30f;               // base of a row that has seen no token
+constexpr float kLowest = -1e30f;             // its maximum
+__device__ __forceinline__ float kv_raise(float best, float& base, float& factor) {
+  const uint32_t e = __float_as_uint(best) >> 23 & 255u;
+  const bool far = (e > 127u + 24u) & (kWeightBits - best < base);
+  const float shrink = far ? __uint_as_float((278u - e) << 23) : 1.0f;   // 2^(151 - e)
+  const float was = far & (base != kUnset) ? kWeightBits - (kWeightBits - base) * shrink : base;
+  factor *= shrink;
+  base = fminf(was, kWeightBits - best * shrink);
+  return __builtin_amdgcn_exp2f(base - was);
+}
+// The row's maximum for the joins, in the units of the factor that it began with.
+__device__ __forceinline__ float kv_maximum(float base, float factor, float began) {
+  return base == kUnset ? kLowest : factor == began ? kWeightBits - base : (kWeightBits - base) * (began / factor);
+}
+
 // Inclusive sum over the lanes up to this one.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
   x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, true);    // row_shr 1, 2, 4, 8

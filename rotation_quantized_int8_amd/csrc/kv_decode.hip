@@ -61,12 +61,9 @@ namespace {
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
 constexpr int kStep = 32;                     // tokens a wavefront takes at once
-constexpr float kWeightBits = 8.0f;           // p = 2^(score - m + 8)
 constexpr float kMostWeight = 32768.0f;       // m is raised past this weight
 constexpr float kLeastScale = 0x1p-80f;       // a value's scale in the maximum, at least
 constexpr float kMostSum = 0x1p92f;           // and past this sum of a step: only values of almost 0 get there
-constexpr float kUnset = 1e30f;               // 8 - m of a row that has seen no token
-constexpr float kLowest = -1e30f;             // its m
 
 // The ring of a wavefront in LDS: kStages steps of 32 tokens, each the keys'
 // codes, the values' codes and the scales (keys' then values', 16 each).  One
@@ -464,12 +461,11 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
           best = fmaxf(best, (whole | seen(t, u, r)) ? z : kLowest);
         }
         best = max16_32(best);
-        const float next = fminf(base[t], kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base[t]);
+        const float by = kv_raise(best, base[t], qf[t]);
         l[t] *= by;
         weight[t] *= by;
 #pragma unroll
         for (int i = 0; i < E; ++i) o[t][i] *= by;
-        base[t] = next;
       }
       l[t] += sum;
       v4u packed;
@@ -539,16 +535,17 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     l[t] = sum16_32(l[t]);
+    const float most = kv_maximum(base[t], qf[t], qscale[16 * t + col]);
     __syncthreads();
     if (quad == 0) {
-      stat[wave][col][0] = base[t] == kUnset ? kLowest : kWeightBits - base[t];
+      stat[wave][col][0] = most;
       stat[wave][col][1] = l[t];
     }
     __syncthreads();
     float top = kLowest;
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) top = fmaxf(top, stat[v][col][0]);
-    const float mine = __builtin_amdgcn_exp2f((base[t] == kUnset ? kLowest : kWeightBits - base[t]) - top);
+    const float mine = __builtin_amdgcn_exp2f(most - top);
     const float offset = weight[t][0] * (BITS == 4 ? -8.0f : -128.0f);
     const int r = tid / 16 % 16, seg = tid % 16;       // the first four wavefronts finish the rows
     float rtop = kLowest, sum = 0.0f, out[E];

@@ -49,12 +49,9 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
-constexpr float kWeightBits = 8.0f;
 constexpr float kMostWeight = 32768.0f;
 constexpr float kLeastScale = 0x1p-80f;       // as in the single-token kernel
 constexpr float kMostSum = 0x1p92f;
-constexpr float kUnset = 1e30f;               // base of a row that has seen no token
-constexpr float kLowest = -1e30f;             // its maximum
 
 // a b, and 0 where a is 0 whatever b is.
 __device__ __forceinline__ float mul_legacy(float a, float b) {
@@ -120,6 +117,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
   __shared__ __align__(16) float kscale[2][kStep], vscale[2][kStep];
   __shared__ __align__(16) int absent[2][WAVES];
   __shared__ __align__(16) float vtop[2][WAVES];      // largest value scale of each group
+  __shared__ float began[WAVES][32];                   // the rows' units
 
   const int tid = threadIdx.x, lane = tid % 64, col = lane % 32, hi = lane / 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -232,6 +230,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
     // (a row with an infinity or a NaN has no finite element, and shows NaN)
     const uint32_t e2 = __float_as_uint(top) >> 23;
     unit = top < INFINITY ? __uint_as_float((e2 < 10u ? 1u : e2 - 9u) << 23) : __uint_as_float(0x7FC00000u);
+    if (hi == 0) began[wave][col] = unit;              // (read by the same wavefront)
     const float by = (a.scale < 0.0f ? -1.0f : 1.0f) / unit, odd = BITS == 4 ? by * 0.0625f : by;
 #pragma unroll
     for (int k = 0; k < P::kSteps; ++k) {
@@ -359,11 +358,10 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
         }
       }
       best = max32(best);
-      const float next = fminf(base, kWeightBits - best), by = __builtin_amdgcn_exp2f(next - base);
+      const float by = kv_raise(best, base, unit);
       l *= by;
 #pragma unroll
       for (int t = 0; t < P::kTiles; ++t) o[t] *= by;
-      base = next;
     }
     // times the values' scales; a weight of 0 stays 0 under a NaN scale, which another row may see
 #pragma unroll
@@ -406,6 +404,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
   }
 
   l = sum32(l);
+  float most = kv_maximum(base, unit, began[wave][col]);
   if constexpr (HALVES == 2) {                         // the second half's outputs join the first's
     v4f* far = reinterpret_cast<v4f*>(lds) + 64 * group + lane;
     float* rest_of = reinterpret_cast<float*>(lds + P::kTiles * 4 * P::kGroups * 1024) + 2 * (64 * group + lane);
@@ -415,13 +414,13 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
         for (int r = 0; r < 16; r += 4)
           far[(4 * t + r / 4) * P::kGroups * 64] = (v4f){o[t][r], o[t][r + 1], o[t][r + 2], o[t][r + 3]};
-      rest_of[0] = base;
+      rest_of[0] = most;
       rest_of[1] = l;
     }
     __syncthreads();
     if (half) return;
-    const float other = rest_of[0], low = fminf(base, other);
-    const float mine = __builtin_amdgcn_exp2f(low - base), its = __builtin_amdgcn_exp2f(low - other);
+    const float other = rest_of[0], top = fmaxf(most, other);
+    const float mine = __builtin_amdgcn_exp2f(most - top), its = __builtin_amdgcn_exp2f(other - top);
     l = l * mine + rest_of[1] * its;
 #pragma unroll
     for (int t = 0; t < P::kTiles; ++t)
@@ -431,7 +430,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][r + i] = o[t][r + i] * mine + y[i] * its;
       }
-    base = low;
+    most = top;
   }
   // ---- a lane holds half a row: rotate it back (every bit of (tile, register) and the half-wave is a bit of the
   // element's number), or leave it to the join
@@ -471,7 +470,7 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
       *reinterpret_cast<v4f*>(dst + 8 * unit + 4) = (v4f){y[4], y[5], y[6], y[7]};
     });
     if (hi == 0) {
-      sp.ml[2 * at] = base == kUnset ? kLowest : kWeightBits - base;
+      sp.ml[2 * at] = most;
       sp.ml[2 * at + 1] = l;
     }
     return;

@@ -202,3 +202,35 @@ def test_a_nan_shows_under_a_weight_of_nothing(rows, m, d, bits):
         sees = m - rows + torch.arange(rows) >= at
         assert got[sees.to(DEV)].isnan().all()
         assert got[~sees.to(DEV)].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,loud,key", [(F16, 2.0 ** 12, 2.0 ** 13), (BF16, 2.0 ** 25, 1.0), (BF16, 2.0 ** 28, 1.0),
+                                            (BF16, -2.0 ** 32, 1.0), (BF16, 2.0 ** 60, 2.0 ** 20), (BF16, 2.0 ** 80, 2.0 ** -40)])
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4), (256, 8)])
+@pytest.mark.parametrize("rows,m", [(1, 600), (24, 600), (40, 600), (300, 600), (2, 9000), (24, 5000), (200, 5000)])
+def test_scores_past_the_steps_of_fp32(rows, m, d, bits, dtype, loud, key):
+    """Scores so large that fp32 holds them in steps of more than 1: where the largest is clear of the others by more
+    than the query's own rounding, its token has all the weight."""
+    _say("large scores", rows, m, d, bits, dtype, loud, key)
+    g = _gen(rows, d, bits)
+    table, lens = _plain_table(m)
+    cache = cr.KVCache.empty(table.numel(), 16, 1, d, bits, DEV)
+    k, v = torch.randn((m, 1, d), generator=g) * key, torch.randn((m, 1, d), generator=g)
+    v[::3] *= 2.0 ** -8
+    cr.kv_append(cache, k.to(dtype).to(DEV), v.to(dtype).to(DEV), torch.arange(m, device=DEV))
+    q = torch.randn((rows, 1, d), generator=g) * loud
+    if rows > 1:
+        q[rows // 2] /= loud                               # an ordinary row among them
+    q = q.to(dtype).to(DEV)
+    got = cr.kv_attention(cache, q, table, lens, causal=False)
+    _check(cache, q, table, [rows], [m], False, got)
+    got = _np(got)[:, 0]
+    kk, vv, _ = _host_rows(cache, table[0].cpu().numpy(), m)
+    s = _np(q)[:, 0] @ kk[:, 0].T * d ** -0.5
+    size = np.linalg.norm(_np(q)[:, 0], axis=-1) * np.linalg.norm(kk[:, 0], axis=-1).max() * d ** -0.5
+    order = np.sort(s, axis=-1)
+    clear = (order[:, -1] - order[:, -2] > 2.0 ** -10 * size) & (size > 2.0 ** 22)
+    assert rows < 3 or clear.sum() > rows // 2
+    one = vv[s.argmax(-1), 0]                              # off by its weight's rounding to fp16 at most
+    off = np.abs(got - one)
+    assert (off <= _half_step(got, dtype) + 2.0 ** -11 * np.linalg.norm(one, axis=-1)[:, None])[clear].all()
