@@ -81,8 +81,9 @@ size_t convrot_kv_workspace_bytes(const convrot_kv_cache* cache, int64_t T, int6
  *             multiple of cache->heads; query head h reads key head
  *             h / (q_heads / heads).
  *   q_start   int32 [batch + 1]: sequence b's queries are rows q_start[b] ..
- *             q_start[b + 1] - 1, at most max_q of them; NULL: T / batch each
- *             (T a multiple of batch).  Rows of no sequence are not written.
+ *             q_start[b + 1] - 1, at most max_q of them; NULL: T / batch each,
+ *             a whole number and at most max_q.  Rows of no sequence are not
+ *             written.
  *   kv_lens   int32 [batch]: cached tokens of each sequence, clamped to
  *             0 .. max_kv.
  *   table     int32 [batch, table_width]: token j of sequence b is at page

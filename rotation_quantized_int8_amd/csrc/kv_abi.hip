@@ -150,8 +150,9 @@ convrot_status convrot_kv_attention(const convrot_kv_cache* cache, const void* Q
   if (!attention_sizes_ok(cache, T, q_heads, batch, max_q, max_kv)) return CONVROT_ERR_SHAPE;
   if (table_width < 0 || table_width > kInt || max_kv > table_width * cache->page_size) return CONVROT_ERR_SHAPE;
   if (!dtype_ok(dtype)) return CONVROT_ERR_INVALID_ARG;
-  if (T == 0 || batch == 0 || max_q == 0) return CONVROT_OK;
-  if (!q_start && (T % batch || T / batch > max_q)) return CONVROT_ERR_SHAPE;
+  if (T == 0) return CONVROT_OK;
+  if (!q_start && (batch == 0 || T % batch || T / batch > max_q)) return CONVROT_ERR_SHAPE;
+  if (batch == 0 || max_q == 0) return CONVROT_OK;
   if (!strides_ok(q_token_stride, q_head_stride)) return CONVROT_ERR_SHAPE;
   if (!Q || !O || !kv_lens || (table_width && !table)) return CONVROT_ERR_INVALID_ARG;
   if (convrot_status st = check_cache_pointers(cache)) return st;

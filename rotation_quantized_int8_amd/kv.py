@@ -206,9 +206,10 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, kv_lens: 
 
     table int32 [batch, width] holds each sequence's pages in order, kv_lens
     int32 [batch] its cached tokens, q_start int32 [batch + 1] the first row
-    of each sequence's queries (None: tokens / batch queries each).  max_q and
-    max_kv bound the queries and the cached tokens of a sequence; tight values
-    make the call faster (defaults: all tokens, and the table's width).  With
+    of each sequence's queries (None: tokens / batch queries each); rows of no
+    sequence, or past its first max_q, are not written.  max_q and max_kv bound
+    the queries and the cached tokens of a sequence; tight values make the call
+    faster (defaults: all tokens, and the table's width).  With
     ``causal`` the queries are each sequence's last tokens; without it every
     query sees every token (cross attention).  A query that sees no token
     gives zeros.  scale defaults to head_dim ** -0.5."""

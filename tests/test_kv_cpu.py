@@ -202,3 +202,17 @@ def test_binding_refuses_before_the_library():
     for bad in (dict(bits=5), dict(head_dim=100), dict(page_size=48), dict(pages=0)):
         with pytest.raises(ValueError):
             cr.KVCache.empty(**{**dict(pages=2, page_size=16, heads=1, head_dim=128, device="cpu"), **bad})
+
+
+def test_attention_refuses_queries_that_no_sequence_has(L):
+    """Without q_start every query belongs to a sequence: no batch, or no room for its queries, is no empty call."""
+    c = _cache()
+
+    def call(T, batch, max_q, start=None):
+        return L.convrot_kv_attention(ctypes.addressof(c), A, 512, 128, 0, T, 4, B, 3, batch, C, start, max_q, 48, 1.0, 1, E,
+                                      F, 1 << 34, None)
+
+    assert call(4, 0, 3) == SHAPE and call(4, 0, 0) == SHAPE
+    assert call(4, 2, 0) == SHAPE and call(4, 2, 1) == SHAPE and call(5, 2, 3) == SHAPE
+    assert call(0, 0, 0) == OK and call(0, 2, 3) == OK
+    assert call(4, 0, 3, D) == OK and call(4, 2, 0, D) == OK     # with q_start these are rows of no sequence
