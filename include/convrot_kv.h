@@ -30,7 +30,7 @@
  * seen by the host: the kernels check them, and an entry that is out of range
  * reads and writes nothing (see each call).  Rows of K, V and Q are addressed
  * by a stride between tokens and one between heads, in elements, multiples of
- * 8 and not negative; a row's D elements are contiguous.
+ * 8 from 0 to 2^31 - 8; a row's D elements are contiguous.
  */
 #ifndef CONVROT_KV_H
 #define CONVROT_KV_H

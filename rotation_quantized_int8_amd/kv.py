@@ -133,7 +133,7 @@ def _rows(t: torch.Tensor, cache: KVCache, heads: Optional[int], name: str) -> T
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {cache.head_dim}], "
                          f"got {list(t.shape)}")
     token, head, last = t.stride()
-    if last != 1 or token % 8 or head % 8 or t.data_ptr() % 16:
+    if last != 1 or (token | head) & ~0x7FFFFFF8 or t.data_ptr() % 16:   # multiples of 8 below 2^31
         t = torch.empty(t.shape, dtype=t.dtype, device=t.device).copy_(t)
         token, head, last = t.stride()
     return t, token, head

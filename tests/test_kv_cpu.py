@@ -216,3 +216,23 @@ def test_attention_refuses_queries_that_no_sequence_has(L):
     assert call(4, 2, 0) == SHAPE and call(4, 2, 1) == SHAPE and call(5, 2, 3) == SHAPE
     assert call(0, 0, 0) == OK and call(0, 2, 3) == OK
     assert call(4, 0, 3, D) == OK and call(4, 2, 0, D) == OK     # with q_start these are rows of no sequence
+
+
+def test_rows_are_copied_where_the_library_does_not_take_their_strides():
+    """Strides of 2^31 elements and more, no multiples of 8, or an odd address: the binding hands on a copy."""
+    class At:
+        device, head_dim = torch.device("cpu"), 64
+
+    x = torch.arange(3 * 2 * 64, dtype=torch.float16).view(3, 2, 64)
+    assert kv._rows(x, At, 2, "x") == (x, 128, 64)
+    kept, token, head = kv._rows(x[:1, :1].expand(3, 2, 64), At, 2, "x")
+    assert (token, head) == (0, 0)
+    one = x[:1, :1]
+    for strides in ((1 << 31, 64, 1), (128, 1 << 31, 1), (1 << 40, 1 << 35, 1), (12, 64, 1), (128, 4, 1)):
+        odd = torch.as_strided(one, (1, 1, 64), strides)
+        copy, token, head = kv._rows(odd, At, 1, "x")
+        assert torch.equal(copy, one) and copy.data_ptr() != one.data_ptr()
+        assert 0 <= token <= 0x7FFFFFFF and 0 <= head <= 0x7FFFFFFF and token % 8 == head % 8 == 0
+    for odd in (torch.arange(385, dtype=torch.float16)[1:].view(3, 2, 64), x.transpose(0, 2).contiguous().transpose(0, 2)):
+        copy, token, head = kv._rows(odd, At, 2, "x")
+        assert torch.equal(copy, odd) and copy.stride(2) == 1 and copy.data_ptr() % 16 == 0
