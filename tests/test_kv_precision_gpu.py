@@ -234,3 +234,39 @@ def test_scores_past_the_steps_of_fp32(rows, m, d, bits, dtype, loud, key):
     one = vv[s.argmax(-1), 0]                              # off by its weight's rounding to fp16 at most
     off = np.abs(got - one)
     assert (off <= _half_step(got, dtype) + 2.0 ** -11 * np.linalg.norm(one, axis=-1)[:, None])[clear].all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("rows", [1, 24, 100, 150])
+def test_scales_of_both_signs(rows, d, bits, dtype):
+    _say("signs of the scale", rows, d, bits, dtype)
+    g = _gen(rows, d)
+    m = 500
+    cache = _random_cache(g, -(-m // 16), 16, 1, d, bits)
+    table, lens = _sequences(g, cache, [m])
+    q = torch.randn((rows, 1, d), generator=g).to(dtype).to(DEV)
+    for scale in (-0.1, 0.1, -0.01, 0.0):
+        got = cr.kv_attention(cache, q, table, lens, scale=scale)
+        _check(cache, q, table, [rows], [m], True, got, scale=scale, tell=str(scale))
+
+
+@pytest.mark.parametrize("d,bits", [(64, 4), (128, 8), (256, 4)])
+@pytest.mark.parametrize("rows", [1, 20, 128])
+def test_weights_that_all_round_one_way(rows, d, bits):
+    """One token's weight is twice the others', less 0.9 half steps of fp16, and all have one value: rounded once to
+    fp16 the weights would cost an output of fp16 a step."""
+    _say("weights that round one way", rows, d, bits)
+    m = 400
+    table, lens = _plain_table(m)
+    cache = cr.KVCache.empty(table.numel(), 16, 1, d, bits, DEV)
+    k, v = torch.zeros((m, 1, d)), torch.full((m, 1, d), 1.99)
+    k[0, 0, 0] = 1.0
+    cr.kv_append(cache, k.half().to(DEV), v.half().to(DEV), torch.arange(m, device=DEV))
+    q = torch.zeros((rows, 1, d), dtype=F16)
+    q[..., 0] = 1.0
+    q = q.to(DEV)
+    for part in (0.9, -0.9, 0.5, -0.5):
+        scale = float(np.log(2.0 / (1.0 + part * 2.0 ** -11)))
+        got = cr.kv_attention(cache, q, table, lens, scale=scale, causal=False)
+        _check(cache, q, table, [rows], [m], False, got, scale=scale, tell=str(part))
