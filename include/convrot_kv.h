@@ -20,8 +20,9 @@
  * Layout.  The cache is paged.  codes [pages, heads, page_size, D bits / 8]
  * bytes and scales fp32 [pages, heads, page_size], one pair of arrays for the
  * keys and one for the values, dense.  4-bit codes are two's complement, two a
- * byte, the even element in the low half; 8-bit codes are int8.  A slot is
- * page * page_size + offset.
+ * byte, the even element in the low half; 8-bit codes are int8 (-8 and -128,
+ * which convrot_kv_append does not write, are read as such; scales are not
+ * negative).  A slot is page * page_size + offset.
  *
  * Conventions are those of convrot.h: device pointers aligned to 16 bytes,
  * caller-owned buffers, work enqueued on `stream` without synchronising, all

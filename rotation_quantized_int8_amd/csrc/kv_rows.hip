@@ -158,8 +158,11 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvRows kr, Kv
   }
 }
 
-// The codes' transform runs in packed 16-bit integers: |sum| <= 127 * 256 =
-// 32512, so it is exact.
+// The codes' transform runs in packed 16-bit integers, where it is exact: a
+// sum of 256 codes from -127 to 127 is at most 32512 in size.  Codes of -128,
+// which kv_append does not write, fit too: the lowest sum is 256 times -128 =
+// -32768 (of the row of W that has no minus), the highest 128 times 128 + 128
+// times 127 = 32640.
 template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, const int64_t* __restrict__ slots, int rows,
                                                       KvDivider by_heads, uint16_t* ko, uint16_t* vo, int bf16) {

@@ -270,3 +270,28 @@ def test_weights_that_all_round_one_way(rows, d, bits):
         scale = float(np.log(2.0 / (1.0 + part * 2.0 ** -11)))
         got = cr.kv_attention(cache, q, table, lens, scale=scale, causal=False)
         _check(cache, q, table, [rows], [m], False, got, scale=scale, tell=str(part))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_lowest_codes(d, bits):
+    """Codes of -8 and -128, which kv_append does not write, in rows of nothing else and among others."""
+    _say("lowest codes", d, bits)
+    low = -8 if bits == 4 else -128
+    r = np.random.default_rng(d)
+    h = O.signs(d)
+    c = np.stack([np.full(d, low), np.where(h[1] > 0, low, -low - 1), np.where(h[d - 1] < 0, low, -low - 1), h[3] * (low + 1)]
+                 + list(r.integers(low, -low, (28, d)))).astype(np.int8)
+    scale = r.uniform(0.01, 0.02, 32).astype(np.float32)
+    raw = torch.from_numpy(O.pack(c, bits)).view(2, 1, 16, -1).to(DEV)
+    scales = torch.from_numpy(scale).view(2, 1, 16).to(DEV)
+    cache = cr.KVCache(raw, scales, raw.clone(), scales.clone())
+    want = O.read_f32(c, scale)
+    for dtype in (F16, BF16):
+        for got in cr.kv_read(cache, torch.arange(32, device=DEV), dtype=dtype):
+            assert torch.equal(got[:, 0].cpu(), torch.from_numpy(want).to(dtype))
+    table, lens = _plain_table(32)
+    for rows in (1, 40, 140):
+        q = torch.randn((rows, 1, d), generator=_gen(rows, d)).half().to(DEV)
+        got = cr.kv_attention(cache, q, table, lens, causal=False)
+        _check(cache, q, table, [rows], [32], False, got)
