@@ -58,8 +58,6 @@
 namespace convrot {
 namespace {
 
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-
 constexpr int kStep = 32;                     // tokens a wavefront takes at once
 constexpr float kMostWeight = 32768.0f;       // m is raised past this weight
 constexpr float kLeastScale = 0x1p-80f;       // a value's scale in the maximum, at least
