@@ -81,21 +81,28 @@ __device__ __forceinline__ float sum16_32(float v) {
   return sum32(v + w);
 }
 
-// What raises a row's maximum, `best` log2 units, past base (weights are 2^(score + base)): base as its next value,
-// and what the row's sums are multiplied by.  fp32 holds scores past 2^25 in steps of 4 and more, where their sums
-// with base are no small numbers any more; such a row's factor, and with it all of its scores, shrink by a power of
-// two that brings `best` below.  Its softmax is then flatter by what no query's rounding tells apart: weights change
-// where scores differ by less than 2^-17 of the largest.
 constexpr float kWeightBits = 8.0f;           // the largest weight is 2^8
 constexpr float kUnset = 1e30f;               // base of a row that has seen no token
 constexpr float kLowest = -1e30f;             // its maximum
-__device__ __forceinline__ float kv_raise(float best, float& base, float& factor) {
+// Before a row's maximum is raised to `best` log2 units.  Weights are 2^(score + base), and fp32 holds scores past
+// 2^25 in steps of 4 and more, where their sums with base are no small numbers any more; such a row's factor, and with
+// it all of its scores, shrink by a power of two that brings `best` below 2^24.  Its softmax is then flatter by what
+// no query's rounding tells apart: weights change where scores differ by less than 2^-16 of the largest.  `best` then
+// counts the scores of such a row with log2 scale' = `value` for all of its tokens.  True where a row of the wavefront
+// shrank.
+__device__ __forceinline__ bool kv_shrink(float& best, float& base, float& factor, float value) {
   const uint32_t e = __float_as_uint(best) >> 23 & 255u;
   const bool far = (e > 127u + 24u) & (kWeightBits - best < base);
-  const float shrink = far ? __uint_as_float((278u - e) << 23) : 1.0f;   // 2^(151 - e)
-  const float was = far & (base != kUnset) ? kWeightBits - (kWeightBits - base) * shrink : base;
-  factor *= shrink;
-  base = fminf(was, kWeightBits - best * shrink);
+  const float by = far ? __uint_as_float((277u - e) << 23) : 1.0f;    // 2^(150 - e)
+  factor *= by;
+  best = far ? best * by + value : best;
+  base = far & (base != kUnset) ? kWeightBits - (kWeightBits - base) * by : base;
+  return __any(far);
+}
+// Raises it, and gives what the row's sums are multiplied by.
+__device__ __forceinline__ float kv_raise(float best, float& base) {
+  const float was = base;
+  base = fminf(was, kWeightBits - best);
   return __builtin_amdgcn_exp2f(base - was);
 }
 // The row's maximum for the joins, in the units of the factor that it began with.

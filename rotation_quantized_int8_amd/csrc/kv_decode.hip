@@ -451,15 +451,19 @@ void kv_decode_kernel(KvAttn a, KvSplit sp) {
         for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
         // raise the maximum (rare); a row that has seen no token has an infinite sum
         if (again || !__any((top > kMostWeight) | (sum > kMostSum))) break;
-        float best = kLowest;
+        float best;
+        for (bool shrunk = false;; shrunk = true) {
+          best = kLowest;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int u = e / 4, r = e % 4;
-          const float z = (float)sc[t][u][r] * (ks[u][r] * qf[t]) + __builtin_amdgcn_logf(fmaxf(vs[u][r], kLeastScale));
-          best = fmaxf(best, (whole | seen(t, u, r)) ? z : kLowest);
+          for (int e = 0; e < 8; ++e) {
+            const int u = e / 4, r = e % 4;
+            const float z = (float)sc[t][u][r] * (ks[u][r] * qf[t]) + __builtin_amdgcn_logf(fmaxf(vs[u][r], kLeastScale));
+            best = fmaxf(best, (whole | seen(t, u, r)) ? z : kLowest);
+          }
+          best = max16_32(best);
+          if (shrunk || !kv_shrink(best, base[t], qf[t], 0.0f)) break;
         }
-        best = max16_32(best);
-        const float by = kv_raise(best, base[t], qf[t]);
+        const float by = kv_raise(best, base[t]);
         l[t] *= by;
         weight[t] *= by;
 #pragma unroll

@@ -358,7 +358,8 @@ void kv_prompt_kernel(KvAttn a, KvSplit sp) {
         }
       }
       best = max32(best);
-      const float by = kv_raise(best, base, unit);
+      kv_shrink(best, base, unit, __builtin_amdgcn_logf(fmaxf(vmost, kLeastScale)));
+      const float by = kv_raise(best, base);
       l *= by;
 #pragma unroll
       for (int t = 0; t < P::kTiles; ++t) o[t] *= by;

@@ -295,3 +295,31 @@ def test_the_lowest_codes(d, bits):
         q = torch.randn((rows, 1, d), generator=_gen(rows, d)).half().to(DEV)
         got = cr.kv_attention(cache, q, table, lens, causal=False)
         _check(cache, q, table, [rows], [32], False, got)
+
+
+@pytest.mark.parametrize("loud", [2.0 ** 22, 2.0 ** 26, 2.0 ** 31, -2.0 ** 31, 2.0 ** 50])
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("rows,m", [(1, 600), (5, 4336), (40, 600), (300, 600), (200, 5000)])
+def test_large_scores_over_values_of_all_sizes(rows, m, d, bits, loud):
+    """As above, bf16, with values whose sizes differ by 2^24: the largest score's token has all the weight."""
+    _say("large scores, values of all sizes", rows, m, d, bits, loud)
+    g = _gen(rows, d, bits, 7)
+    table, lens = _plain_table(m)
+    cache = cr.KVCache.empty(table.numel(), 16, 1, d, bits, DEV)
+    k, v = torch.randn((m, 1, d), generator=g), torch.randn((m, 1, d), generator=g)
+    v *= torch.exp2(torch.randint(-8, 17, (m, 1, 1), generator=g).float())
+    cr.kv_append(cache, k.bfloat16().to(DEV), v.bfloat16().to(DEV), torch.arange(m, device=DEV))
+    q = (torch.randn((rows, 1, d), generator=g) * loud).bfloat16().to(DEV)
+    got = _np(cr.kv_attention(cache, q, table, lens, causal=False))[:, 0]
+    assert np.isfinite(got).all()
+    kk, vv, _ = _host_rows(cache, table[0].cpu().numpy(), m)
+    s = _np(q)[:, 0] @ kk[:, 0].T * d ** -0.5
+    size = np.linalg.norm(_np(q)[:, 0], axis=-1) * np.linalg.norm(kk[:, 0], axis=-1).max() * d ** -0.5
+    order = np.sort(s, axis=-1)
+    clear = order[:, -1] - order[:, -2] > 2.0 ** -10 * size
+    assert rows < 8 or clear.sum() > rows // 2
+    one = vv[s.argmax(-1), 0]
+    # a weight of fp16 that is up to 2^24 below the largest possible is off by 2^-25 of that
+    room = 2.0 ** -11 * np.linalg.norm(one, axis=-1) + 2.0 ** -33 * np.linalg.norm(vv[:, 0], axis=-1).max()
+    off = np.abs(got - one)
+    assert (off <= _half_step(got, BF16) + room[:, None])[clear].all()
