@@ -323,3 +323,35 @@ def test_large_scores_over_values_of_all_sizes(rows, m, d, bits, loud):
     room = 2.0 ** -11 * np.linalg.norm(one, axis=-1) + 2.0 ** -33 * np.linalg.norm(vv[:, 0], axis=-1).max()
     off = np.abs(got - one)
     assert (off <= _half_step(got, BF16) + room[:, None])[clear].all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4), (256, 8)])
+@pytest.mark.parametrize("rows,m", [(5, 90), (40, 3000), (300, 90), (300, 3000)])
+def test_a_query_without_finite_scores_shows_alone(rows, m, d, bits, dtype):
+    """Queries with an infinity or a NaN, or whose rotation passes fp32, give NaN where they see a token, zeros where
+    they see none, and leave the other rows as they are without them."""
+    _say("queries that are not finite", rows, m, d, bits, dtype)
+    g = _gen(rows, m, d)
+    cache = _random_cache(g, -(-m // 16), 16, 1, d, bits)
+    table, lens = _sequences(g, cache, [m])
+    q = torch.randn((rows, 1, d), generator=g).to(dtype)
+    clean = q.clone()
+    bad = torch.zeros(rows, dtype=torch.bool)
+    for i, value in enumerate((float("nan"), float("inf"), float("-inf"))):
+        q[i + 1, 0, 5 * i] = value
+        clean[i + 1] = 0
+        bad[i + 1] = True
+    if dtype == BF16:
+        q[rows - 1] = 3e38
+        clean[rows - 1] = 0
+        bad[rows - 1] = True
+    for causal in (True, False):
+        got = cr.kv_attention(cache, q.to(DEV), table, lens, causal=causal).cpu()[:, 0]
+        sees = torch.ones(rows, dtype=torch.bool) if not causal else m - rows + torch.arange(rows) >= 0
+        assert got[bad & sees].isnan().all() and not got[~sees].any()
+        fine = clean.to(DEV)
+        want = cr.kv_attention(cache, fine, table, lens, causal=causal)
+        _check(cache, fine, table, [rows], [m], causal, want)
+        got[bad] = want[:, 0].cpu()[bad]
+        _check(cache, fine, table, [rows], [m], causal, got[:, None].to(DEV))
