@@ -30,8 +30,8 @@
 // The values' codes enter with an offset of 8 or 128 (see value_operands), so
 // the sums round at 2^-24 of 8 (128) sum W where even tokens leave a mean that
 // is smaller than sum W by sqrt(tokens).  The offset is taken off every 64 steps
-// (2048 tokens), which keeps that at 3e-5 of an output for any context; taken
-// off at the end alone it comes to 6e-4 over 131072 tokens in one workgroup.
+// (2048 tokens), which keeps that at 5e-5 of an output over 131072 tokens in
+// one workgroup; taken off at the end alone it comes to 4e-4.
 //
 // What bounds it: HBM (each cached row is read once for up to 32 rows of its
 // key head).  A workgroup of 4 wavefronts owns one chunk of the tokens of one
@@ -42,11 +42,13 @@
 //
 // Measured, against the time of a copy of as many bytes at 5.1 TB/s: 32
 // sequences of up to 8192 tokens, 8 key heads of 4 query heads, D 128, 4 bits
-// (174 MB): 37.9 us and 5.3 us for the join (4.6 TB/s in the kernel); two
-// sequences of 131072 tokens, 4 key heads of 8 (143 MB): 30.5 and 5.2 us (4.7
+// (174 MB): 38.7 us and 5.3 us for the join (4.5 TB/s in the kernel); two
+// sequences of 131072 tokens, 4 key heads of 8 (143 MB): 30 and 5.2 us (4.7
 // TB/s); 48 of up to 2501 tokens, 4 key heads of 5, D 256, 8 bits (164 MB):
-// 41 us in one launch (4.0 TB/s).  One token over 1000 of 16 heads: 12.2 us,
-// the latency of the prologue, two steps and the join of the wavefronts.
+// 41 us in one launch (4.0 TB/s).  One token over 1000 of 16 heads: 13 us, the
+// latency of the prologue, two steps and the join of 16 wavefronts (split over
+// more workgroups and joined by a second launch it is as fast in a graph and
+// slower in a stream of single calls, see the plan).
 // What is left to the copy's rate is the start (lengths, pages, the rotation
 // of the queries, about 4 us a workgroup before the first product) and the
 // vector work of a step, which a SIMD's four wavefronts overlap with loads

@@ -5,10 +5,11 @@
 // the queries once, use the codes as they are with their scales outside the
 // products, rotate the result back.  Here the arithmetic counts, so a
 // workgroup of 4 (8) wavefronts takes 128 (256, or 128 with half of the tokens
-// each) rows (queries times heads of one group) and shares the decoding: of each 64 (128) tokens every wavefront
-// turns the codes of 16 into fp16 (exact) and writes them to LDS in the order
-// in which the matrix instructions take their operands (16 bytes a lane, no
-// bank conflicts), two buffers deep, so that a step costs one barrier.
+// each) rows (queries times heads of one group) and shares the decoding: of
+// each 64 (128) tokens every wavefront turns the codes of 16 into fp16 (exact)
+// and writes them to LDS in the order in which the matrix instructions take
+// their operands (16 bytes a lane, no bank conflicts), two buffers deep, so
+// that a step costs one barrier.
 //   S^T = C_k Q^T     mfma f32 32x32x16 f16, 32 tokens x 32 rows
 //   O^T = C_v^T W^T   the same, 32 elements x 32 rows
 // A lane owns one row (column lane % 32); the result layout of S^T is the
@@ -24,20 +25,24 @@
 // at most, to nearest), so a sum of many is off by less than the output's own
 // rounding.  sm_scale and log2 e are multiplied into the keys' scales, so a
 // weight is exp2(fma(S, scale_j unit_row, base_row)): two operations, its
-// exponential, its share of the sum and the product with the value's scale.  The running
-// maximum is raised only when a weight could pass 2^15 (they start at 2^8 for
-// the largest).
+// exponential, its share of the sum and the product with the value's scale.
+// The running maximum is raised only when a weight could pass 2^15 (they start
+// at 2^8 for the largest).
 //
 // What bounds it: the vector work on the weights (six operations a weight,
 // the exponential at a quarter of the rate) next to the matrix products, which
 // the two wavefronts of a SIMD overlap only in part.  Measured: 4096 causal
-// queries of 32 heads over 8 key heads, D 128, bf16, 4 bits: 169 us, 812
+// queries of 32 heads over 8 key heads, D 128, bf16, 4 bits: 174 us, 790
 // TFLOP/s, against 1220 of a large matrix product; three chunks of up to 701
-// queries, 24 heads over 8, D 64, fp16, 8 bits, contexts of up to 6007: 129
-// us, 344 TFLOP/s (the remainder's product is not counted); 1024 queries of 16
-// heads over 512 states, twice: 26 us.  Three wavefronts a SIMD for heads of
+// queries, 24 heads over 8, D 64, fp16, 8 bits, contexts of up to 6007: 134
+// us, 330 TFLOP/s (the remainder's product is not counted); 1024 queries of 16
+// heads over 512 states, twice: 26.5 us.  Three wavefronts a SIMD for heads of
 // 128, steps of 32 tokens, the two halves of a step offset between the
 // wavefronts, and the next scores formed before the outputs were no faster.
+// Heads of 256 hold 128 (fp16: 192) registers of outputs and queries before
+// anything else and run one wavefront a SIMD, with what does not fit in the
+// accumulation registers: 2048 x 2048 causal, 16 heads over 8, fp16, 4 bits,
+// 147 us, 234 TFLOP/s; 256 rows over 4 x 8192, 8 heads, 186 us.
 
 #include "kv_core.hpp"
 #include "launch.hpp"
