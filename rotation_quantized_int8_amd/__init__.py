@@ -14,6 +14,10 @@ Functions mirror the C entry points:
 The attention side (a paged key/value cache, rotated and quantised the same
 way; C ABI in ``include/convrot_kv.h``) is in ``kv.py``:
   KVCache, kv_append, kv_read, kv_attention, kv_workspace_bytes.
+The linear in 4 bits (MXFP4; C ABI in ``include/convrot_mx.h``) is in ``mx.py``:
+  mx_quantize_weights, mx_linear, mx_act_quant, mx_gemm, mx_dequantize, mx_workspace_bytes.
+The norms around the linears (C ABI in ``include/convrot_norm.h``) are in ``norms.py``:
+  norm, norm_quant, residual_norm, residual_norm_quant.
 """
 
 from __future__ import annotations
@@ -460,3 +464,6 @@ def gemm_f16(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
 
 
 from .kv import KVCache, kv_append, kv_attention, kv_read, kv_workspace_bytes  # noqa: E402,F401
+from .mx import (mx_act_quant, mx_dequantize, mx_gemm, mx_linear, mx_quantize_weights,  # noqa: E402,F401
+                 mx_workspace_bytes)
+from .norms import norm, norm_quant, residual_norm, residual_norm_quant  # noqa: E402,F401

@@ -1,0 +1,129 @@
+// Rows to microscaled 4-bit floating point and back: weights (fp32) and
+// activations (fp16, bf16) rotated and quantised, and the rows that codes and
+// scales stand for.
+//
+// Mathematics.  u = fp32(x H) in groups of 256; a block of 32 has the scale
+// 2^e, e = max(floor(log2 max|u|) - 2, -127), so that its largest value lies in
+// [4, 8) of the codes' +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} (those past 6 saturate).
+// floor(log2) is the exponent field of the maximum's bits; the codes come from
+// the hardware conversion, which rounds to nearest even.
+//
+// Work split.  As in the int8 prologue 16 lanes own a group of 256, each the 16
+// elements of one row of the 16 x 16 view, so a block of 32 is two neighbouring
+// lanes: one lane permutation completes its maximum.  No scale spans a row, so
+// groups are independent and no workgroup barrier is needed.
+
+#include "mx.hpp"
+
+namespace convrot {
+namespace {
+
+constexpr int kSegs = 16;   // groups of a 256-thread workgroup
+
+template <bool kBF16>
+__global__ void __launch_bounds__(256)
+mx_act_quant_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K, uint8_t* __restrict__ codes,
+                    uint8_t* __restrict__ scales) {
+  __shared__ __align__(16) char smem[kSegs * kSlotBytes];
+  const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
+  const int64_t G = K / kGroup;
+  const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
+  if (u >= M * G) return;
+  const int64_t row = u / G, g = u - row * G;
+  double y[16];
+  rotate_group<kBF16>(X + row * K + g * kGroup, smem + seg * kSlotBytes, lane, y);
+  float f[16];
+  // fp16: 16 u stays in fp32's normal range, and 2^4 goes into the scale;
+  // bf16: u itself, which may be as large or small as fp32 holds.  The sum
+  // with 0 makes a zero +0.
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = kBF16 ? (float)__fma_rn(y[i], 0.0625, 0.0) : (float)y[i] + 0.0f;
+  mx_store<kBF16 ? 0 : 4>(f, row, M, K, g, lane, codes, scales);
+}
+
+__global__ void __launch_bounds__(256)
+mx_quantize_weights_kernel(const float* __restrict__ W, int64_t N, int64_t K, uint8_t* __restrict__ codes,
+                           uint8_t* __restrict__ scales) {
+  __shared__ __align__(16) char smem[kSegs * kSlotBytes];
+  const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
+  const int64_t G = K / kGroup;
+  const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
+  if (u >= N * G) return;
+  const int64_t row = u / G, g = u - row * G;
+  const float4* src = reinterpret_cast<const float4*>(W + row * K + g * kGroup + 16 * lane);
+  double v[16];   // the sum with 0 makes a zero +0, and so every zero after it
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4 t = src[c];
+    v[4 * c] = __fma_rn((double)t.x, 0.0625, 0.0);
+    v[4 * c + 1] = __fma_rn((double)t.y, 0.0625, 0.0);
+    v[4 * c + 2] = __fma_rn((double)t.z, 0.0625, 0.0);
+    v[4 * c + 3] = __fma_rn((double)t.w, 0.0625, 0.0);
+  }
+  float f[16];
+  rotate_rows(v, smem + seg * kSlotBytes, lane, f);
+  mx_store<0>(f, row, N, K, g, lane, codes, scales);
+}
+
+// An e2m1 code as the integer 2 c: 0 1 2 3 4 6 8 12 and their negatives.
+__device__ __forceinline__ int e2m1_twice(uint32_t code) {
+  const int m = (int)((0xC8643210u >> (4 * (code & 7))) & 15u);
+  return code & 8 ? -m : m;
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(256)
+mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
+                     int64_t K, uint16_t* __restrict__ V) {
+  __shared__ __align__(16) char smem[kSegs * kSlotBytes];
+  const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
+  const int64_t G = K / kGroup;
+  const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
+  if (u >= rows * G) return;
+  const int64_t row = u / G, g = u - row * G;
+  const uint2 c = *reinterpret_cast<const uint2*>(codes + row * (K / 2) + g * 128 + 8 * lane);
+  const uint32_t byte = scales[(g * rows + row) * 8 + (lane >> 1)];
+  // 2^(byte - 127) / 2 (the codes are taken twice) / 16 (the transform of +-1)
+  const double s = byte == 255u ? __longlong_as_double(0x7FF8000000000000ll)
+                                : __longlong_as_double((long long)(byte + 1023 - 127 - 5) << 52);
+  double v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = (double)e2m1_twice((i < 8 ? c.x : c.y) >> (4 * (i & 7))) * s;
+  float f[16];
+  rotate_rows(v, smem + seg * kSlotBytes, lane, f);
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o[i] = kBF16 ? (uint32_t)f32_to_bf16_rn(f[2 * i]) | (uint32_t)f32_to_bf16_rn(f[2 * i + 1]) << 16
+                 : pack_f16x2_rn(f[2 * i], f[2 * i + 1]);
+  uint4* dst = reinterpret_cast<uint4*>(V + row * K + g * kGroup + 16 * lane);
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+dim3 grid_of(int64_t rows, int64_t K) { return dim3((unsigned)((rows * (K / kGroup) + kSegs - 1) / kSegs)); }
+
+}  // namespace
+
+hipError_t launch_mx_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* codes, uint8_t* scales,
+                                      hipStream_t stream) {
+  hipLaunchKernelGGL(mx_quantize_weights_kernel, grid_of(N, K), dim3(256), 0, stream, W, N, K, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_act_quant(const void* X, bool bf16, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales,
+                               hipStream_t stream) {
+  const auto fn = bf16 ? &mx_act_quant_kernel<true> : &mx_act_quant_kernel<false>;
+  hipLaunchKernelGGL(fn, grid_of(M, K), dim3(256), 0, stream, static_cast<const uint16_t*>(X), M, K, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* V,
+                                bool bf16, hipStream_t stream) {
+  const auto fn = bf16 ? &mx_dequantize_kernel<true> : &mx_dequantize_kernel<false>;
+  hipLaunchKernelGGL(fn, grid_of(rows, K), dim3(256), 0, stream, codes, scales, rows, K,
+                     static_cast<uint16_t*>(V));
+  return hipGetLastError();
+}
+
+}  // namespace convrot

@@ -1,0 +1,39 @@
+// Host-side launchers of the norms around the linears (internal to the library).
+#pragma once
+
+#include "mx.hpp"
+
+namespace convrot {
+
+enum NormKind { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
+enum NormOut { kOutNone = -1, kOut16 = 0, kOutInt8 = 1, kOutMx = 2 };
+
+struct NormDesc {
+  int kind;
+  float eps;
+  const float* weight;   // [D] or null
+  const float* bias;     // [D] or null
+};
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* y;              // the block's output (residual form) or null
+  int64_t x_stride, y_stride;
+  int64_t M;
+  int D;
+  double residual_scale;
+  NormDesc post, norm;
+  const void *scale, *shift, *gate;   // rows of the modulation or null
+  int64_t scale_stride, shift_stride, gate_stride;
+  int mod_f32;                    // the modulation is fp32 (else the rows' type)
+  int64_t mod_rows;
+  int64_t each;                   // rows of x per row of the modulation (index null)
+  const int32_t* index;
+  uint16_t* h;
+  void* values;
+  void* scales;
+};
+
+hipError_t launch_norm(const NormArgs& a, bool bf16, NormOut out, hipStream_t stream);
+
+}  // namespace convrot
