@@ -11,14 +11,16 @@
  * The residual:
  *   h = residual_scale x + gate_i post(y)
  * with post a norm without modulation, or y itself; what follows takes h
- * before its rounding.  All arithmetic is fp64 up to the one rounding of an
- * output, so codes are those of the formula but where the rounding of n H to
- * fp32 or the fp64 sums (2^-50) move a value across a border.
+ * before its rounding.  All arithmetic is fp32 up to the one rounding of an
+ * output: the mean first, then the squares of the differences, with what the
+ * mean's rounding left taken out.  Rows of any finite size have their norm (one
+ * whose squares leave fp32's range is taken times a power of two); an h that
+ * passes fp32, an infinity or a NaN shows in its own row alone.
  *
  * Conventions are those of convrot.h, but for these.  Rows of X, Y and of the
  * modulation have strides in elements (0 .. 2^31 - 1) with D contiguous
  * elements each, and need no alignment but their element's; H and the outputs
- * are dense.  D is 1 .. 32768, for quantised outputs a multiple of 256; M is
+ * are dense.  D is 1 .. 16384, for quantised outputs a multiple of 256; M is
  * 0 .. 2^24 with M D at most 2^35.
  */
 #ifndef CONVROT_NORM_H
@@ -30,7 +32,7 @@
 extern "C" {
 #endif
 
-#define CONVROT_NORM_D_MAX 32768
+#define CONVROT_NORM_D_MAX 16384
 
 enum { CONVROT_NORM_RMS = 1, CONVROT_NORM_LAYER = 2 };
 enum { CONVROT_NORM_OUT_16 = 0, CONVROT_NORM_OUT_INT8 = 1, CONVROT_NORM_OUT_MXFP4 = 2 };

@@ -4,18 +4,18 @@
 //
 // Mathematics.  h = residual_scale x + gate post(y) (or x), n = ((h - mu) r
 // weight + bias)(1 + scale) + shift, in one pass: a row is held in registers
-// from its load to its last output, its statistics are two sums over the lanes
-// (the mean first, then the squares of the differences, so that nothing
-// cancels).  All of it is fp64: gfx950 issues fp64 additions and fused
-// multiply-adds at the rate of single fp32 ones, the rows are bound by memory,
-// and so no square overflows and codes come out as those of the formula.
+// from its load to its last output.  All of it is fp32 (fp64 conversions issue at
+// a quarter of the rate: the same kernel in fp64 took 49 instead of @Q@ us for
+// 16384 x 2048 to 4 bits).  The mean is taken first, then the sums of d = h - mu
+// and of d^2, whose first takes out what the rounding of mu left, so that rows of
+// one value give 0 and a mean far above the spread costs no digits.  A row whose
+// squares leave fp32's range is taken times a power of two instead.
 //
-// Work split.  `waves` wavefronts own a row, each lane units of V neighbouring
+// Work split.  WAVES wavefronts own a row, each lane S units of V neighbouring
 // elements: 8 (one 16-byte load) for outputs of 16 bits, 16 (a row of the
-// rotation's 16 x 16 view) for quantised ones, S units a lane.  One wavefront a
-// row needs no barrier; four such rows share a workgroup.  Rows need no
-// alignment: the loads are 16 bytes at any element, a last partial unit goes
-// element by element.
+// rotation's 16 x 16 view) for quantised ones.  One wavefront a row needs no
+// barrier; four such rows share a workgroup.  Rows need no alignment: the loads
+// are 16 bytes at any element, a last partial unit goes element by element.
 
 #include "norm.hpp"
 
@@ -26,58 +26,55 @@ typedef uint16_t v8u __attribute__((ext_vector_type(8)));
 typedef v8u v8u_any __attribute__((aligned(2)));
 typedef v4f v4f_any __attribute__((aligned(4)));
 
-__device__ __forceinline__ double dpp_f64(double v, const int step) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  int lo = (int)(uint32_t)u, hi = (int)(uint32_t)(u >> 32);
-  switch (step) {
-    case 0: lo = __builtin_amdgcn_update_dpp(0, lo, 0xB1, 0xF, 0xF, true);
-            hi = __builtin_amdgcn_update_dpp(0, hi, 0xB1, 0xF, 0xF, true); break;
-    case 1: lo = __builtin_amdgcn_update_dpp(0, lo, 0x4E, 0xF, 0xF, true);
-            hi = __builtin_amdgcn_update_dpp(0, hi, 0x4E, 0xF, 0xF, true); break;
-    case 2: lo = __builtin_amdgcn_update_dpp(0, lo, 0x141, 0xF, 0xF, true);
-            hi = __builtin_amdgcn_update_dpp(0, hi, 0x141, 0xF, 0xF, true); break;
-    default: lo = __builtin_amdgcn_update_dpp(0, lo, 0x140, 0xF, 0xF, true);
-             hi = __builtin_amdgcn_update_dpp(0, hi, 0x140, 0xF, 0xF, true); break;
-  }
-  return __longlong_as_double((long long)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo));
-}
-
 // Sum over the wavefront, the same bits in every lane.
-__device__ __forceinline__ double wave_sum_f64(double v) {
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  v += dpp_f32<0x141>(v);
+  v += dpp_f32<0x140>(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Sums over the row's wavefronts, in their order.  `part` is written by this sum
+// alone until the next barrier has passed.
+template <int WAVES>
+__device__ __forceinline__ void row_sums(float& a, float& b, float2* part) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (WAVES > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(a, b);
+    __syncthreads();
+    float2 s = part[0];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) v += dpp_f64(v, s);
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const auto l = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
-  const auto h = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
-  v = __longlong_as_double((long long)((uint64_t)h[0] << 32 | l[0])) +
-      __longlong_as_double((long long)((uint64_t)h[1] << 32 | l[1]));
-  const uint64_t w = (uint64_t)__double_as_longlong(v);
-  const auto l2 = __builtin_amdgcn_permlane32_swap((uint32_t)w, (uint32_t)w, false, false);
-  const auto h2 = __builtin_amdgcn_permlane32_swap((uint32_t)(w >> 32), (uint32_t)(w >> 32), false, false);
-  return __longlong_as_double((long long)((uint64_t)h2[0] << 32 | l2[0])) +
-         __longlong_as_double((long long)((uint64_t)h2[1] << 32 | l2[1]));
-}
-
-// Sum over the row's wavefronts, in their order; `part` is used by this sum
-// alone (one of the kernel's, so that no barrier has to free it).
-__device__ __forceinline__ double row_sum(double v, int waves, double* part) {
-  v = wave_sum_f64(v);
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
-  for (int w = 1; w < waves; ++w) v += part[w];
-  return v;
+    for (int w = 1; w < WAVES; ++w) {
+      const float2 t = part[w];
+      s.x += t.x;
+      s.y += t.y;
+    }
+    a = s.x;
+    b = s.y;
+  }
 }
 
 template <bool kBF16>
-__device__ __forceinline__ double widen(uint16_t b) {
-  return kBF16 ? (double)bf16_to_f32(b) : (double)__half2float(__ushort_as_half(b));
+__device__ __forceinline__ float widen(uint16_t b) {
+  return kBF16 ? bf16_to_f32(b) : __half2float(__ushort_as_half(b));
 }
+
+// 8 values to the rows' type, nearest even.
 template <bool kBF16>
-__device__ __forceinline__ uint16_t narrow(double v) {
-  const float f = (float)v;
-  return kBF16 ? f32_to_bf16_rn(f) : __half_as_ushort(__float2half_rn(as_fp32(f)));
+__device__ __forceinline__ v8u narrow(const float (&v)[8]) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  v4i r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = kBF16 ? __builtin_bit_cast(int, __builtin_convertvector((f2){v[2 * i], v[2 * i + 1]}, b2))
+                 : (int)pack_f16x2_rn(v[2 * i], v[2 * i + 1]);
+  return __builtin_bit_cast(v8u, r);
 }
 
 // 8 neighbouring elements from e0 of a 16-bit row of D (zeros past its end).
@@ -107,7 +104,7 @@ __device__ __forceinline__ void load_mod(const void* base, int64_t at, int f32, 
   } else {
     const v8u v = load8(static_cast<const uint16_t*>(base) + at, e0, D);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)widen<kBF16>(v[i]);
+    for (int i = 0; i < 8; ++i) f[i] = widen<kBF16>(v[i]);
   }
 }
 __device__ __forceinline__ void store8(uint16_t* row, int e0, int D, v8u v) {
@@ -120,30 +117,104 @@ __device__ __forceinline__ void store8(uint16_t* row, int e0, int D, v8u v) {
   }
 }
 
-// mu and r of the row that the lanes hold in v (zeros past its end).
-template <int V, int S>
-__device__ __forceinline__ void statistics(const double (&v)[S][V], int kind, double eps, int D, int waves,
-                                           int wave, int lane, double (*part)[16], double& mu, double& r) {
-  mu = 0.0;
-  if (kind == kNormLayer) {
-    double s = 0.0;
+constexpr float kSmall = 0x1p-90f, kUp = 0x1p96f;
+
+// A row in fp32, element i of chunk c of unit k as at(k, c, i) (0 past the row's
+// end; `first(k)` is the unit's first element), to its mu and r: t = (at - mu) r.
+// `scale_by` multiplies the row by a power of two, which t does not feel: a row
+// whose squares pass fp32 is taken 2^-96 times, one whose squares vanish (eps 0)
+// 2^96 times.
+template <int V, int S, int WAVES, typename At, typename First, typename ScaleBy>
+__device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by, int kind, float eps, int D,
+                                           float2 (*part)[16], float& mu, float& r) {
+  const float inv = 1.0f / (float)D;
+  for (int round = 0;; ++round) {
+    mu = 0.0f;
+    if (kind == kNormLayer) {
+      float s = 0.0f, none = 0.0f;
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+#pragma unroll
+        for (int c = 0; c < V / 8; ++c) {
+          float p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = at(k, c, i);
+          s += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+        }
+      row_sums<WAVES>(s, none, part[0]);
+      mu = s * inv;
+    }
+    float e = 0.0f, q = 0.0f;
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += v[k][i];
-    mu = row_sum(s, waves, part[0]) / D;
-  }
-  double q = 0.0;
+      for (int c = 0; c < V / 8; ++c) {
+        const int left = D - first(k) - 8 * c;
+        float p[8], w = 0.0f;
 #pragma unroll
-  for (int k = 0; k < S; ++k) {
-    const int e0 = ((wave + waves * k) * 64 + lane) * V;
+        for (int i = 0; i < 8; ++i) p[i] = at(k, c, i) - mu;
+        if (left < 8) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const double d = e0 + i < D ? v[k][i] - mu : 0.0;
-      q = __fma_rn(d, d, q);
-    }
+          for (int i = 0; i < 8; ++i) p[i] = i < left ? p[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w = __fmaf_rn(p[i], p[i], w);
+        q += w;
+        if (kind == kNormLayer) e += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      }
+    row_sums<WAVES>(e, q, part[1 + round]);
+    e *= inv;
+    const float var = fmaxf(__fmaf_rn(-e, e, q * inv), 0.0f) + eps;
+    mu += e;
+    r = 1.0f / sqrtf(var);
+    if ((q <= 0x1p120f && var >= kSmall) || round) return;
+    const float by = q <= 0x1p120f ? kUp : 1.0f / kUp;
+    scale_by(by);
+    if (eps > 0.0f) eps = fmaxf(eps * by * by, 0x1p-126f);   // still above 0: a row of one value gives 0
   }
-  r = 1.0 / sqrt(row_sum(q, waves, part[1]) / D + eps);
+}
+
+// Rotation of a group whose row `lane` (elements 16 lane .. + 15) this lane
+// holds in fp32, in place: along the row in registers, a transpose in the
+// segment's LDS slot (16-byte chunks swizzled by row, conflict-free both ways),
+// along the column, and the transpose back.  The transform is that of +-1.
+constexpr int kTurnSlot = 1024 + 64;   // bytes: 256 floats, and an offset of 16 banks to the next slot
+__device__ __forceinline__ void fwht16(float (&v)[16]) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+}
+__device__ __forceinline__ void rotate_rows(float (&v)[16], char* slot, int lane) {
+  const int key = (lane >> 2) & 3;
+  fwht16(v);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<float4*>(slot + 64 * lane + 16 * (c ^ key)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  wave_lds_sync();
+  float* sf = reinterpret_cast<float*>(slot) + (lane & 3);
+#pragma unroll
+  for (int a = 0; a < 16; ++a) v[a] = sf[16 * a + 4 * (key ^ (a >> 2))];
+  wave_lds_sync();
+  fwht16(v);
+#pragma unroll
+  for (int a = 0; a < 16; ++a) sf[16 * a + 4 * (key ^ (a >> 2))] = v[a];
+  wave_lds_sync();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4 t = *reinterpret_cast<const float4*>(slot + 64 * lane + 16 * (c ^ key));
+    v[4 * c] = t.x;
+    v[4 * c + 1] = t.y;
+    v[4 * c + 2] = t.z;
+    v[4 * c + 3] = t.w;
+  }
+  wave_lds_sync();
 }
 
 // int8 codes of 16 values with the row's scale s > 0.  quantize16 multiplies
@@ -161,117 +232,163 @@ __device__ __forceinline__ uint4 codes16(const float (&f)[16], float s) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool kBF16, int OUT, bool RES, int S>
-__global__ void __launch_bounds__(1024)
-norm_kernel(NormArgs a, int waves) {
-  constexpr int V = OUT == kOutInt8 || OUT == kOutMx ? 16 : 8;
+template <bool kBF16, int OUT, bool RES, int S, int WAVES>
+__global__ void __launch_bounds__(WAVES <= 4 ? 256 : 64 * WAVES)
+norm_kernel(NormArgs a) {
+  constexpr int V = OUT == kOutInt8 || OUT == kOutMx ? 16 : 8, C = V / 8;
   constexpr bool kTurn = V == 16;
   extern __shared__ __align__(16) char slots[];     // quantised: a slot for each group in work
-  __shared__ double part[4][16];
+  __shared__ float2 part[6][16];
   __shared__ uint32_t top[16];
   const int lane = threadIdx.x & 63, wave_id = threadIdx.x >> 6;
-  const int wave = waves == 1 ? 0 : wave_id;
-  const int64_t row = waves == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + wave_id : blockIdx.x;
+  const int wave = WAVES == 1 ? 0 : wave_id;
+  const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + wave_id : blockIdx.x;
   if (row >= a.M) return;
   const int64_t mrow = a.index ? a.index[row] : row / a.each;
   if (mrow < 0 || mrow >= a.mod_rows) return;       // of no sequence: the whole row's wavefronts leave
   const int D = a.D;
-  auto first = [&](int k) { return ((wave + waves * k) * 64 + lane) * V; };
+  auto first = [&](int k) { return ((wave + WAVES * k) * 64 + lane) * V; };
 
-  double v[S][V];
-  {
-    const uint16_t* xr = a.x + row * a.x_stride;
+  v8u xr[S][C];
+#pragma unroll
+  for (int k = 0; k < S; ++k)
+#pragma unroll
+    for (int c = 0; c < C; ++c) xr[k][c] = load8(a.x + row * a.x_stride, first(k) + 8 * c, D);
+  auto rescale = [&](v8u (&raw)[S][C], float by) {
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
-      for (int c = 0; c < V; c += 8) {
-        const v8u t = load8(xr, first(k) + c, D);
+      for (int c = 0; c < C; ++c) {
+        float p[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][c + i] = widen<kBF16>(t[i]);
+        for (int i = 0; i < 8; ++i) p[i] = widen<kBF16>(raw[k][c][i]) * by;
+        raw[k][c] = narrow<kBF16>(p);
       }
-  }
+  };
+  float h[RES ? S : 1][C][8];       // the residual form's rows; the plain one widens x where it is read
   if constexpr (RES) {
-    double y[S][V];
-    const uint16_t* yr = a.y + row * a.y_stride;
+    v8u yr[S][C];
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
-      for (int c = 0; c < V; c += 8) {
-        const v8u t = load8(yr, first(k) + c, D);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[k][c + i] = widen<kBF16>(t[i]);
-      }
-    double mu = 0.0, r = 1.0;
+      for (int c = 0; c < C; ++c) yr[k][c] = load8(a.y + row * a.y_stride, first(k) + 8 * c, D);
+    float mu = 0.0f, r = 1.0f;
     if (a.post.kind != kNormNone)
-      statistics<V, S>(y, a.post.kind, (double)a.post.eps, D, waves, wave, lane, &part[0], mu, r);
-    uint16_t* hr = a.h + row * D;
+      statistics<V, S, WAVES>([&](int k, int c, int i) { return widen<kBF16>(yr[k][c][i]); }, first,
+                              [&](float by) { rescale(yr, by); }, a.post.kind, a.post.eps, D, &part[0], mu, r);
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
-      for (int c = 0; c < V; c += 8) {
-        const int e0 = first(k) + c;
+      for (int c = 0; c < C; ++c) {
+        const int e0 = first(k) + 8 * c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][c][i] = 0.0f;
         if (e0 >= D) continue;
-        float w[8] = {1, 1, 1, 1, 1, 1, 1, 1}, b[8] = {0, 0, 0, 0, 0, 0, 0, 0}, g[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-        if (a.post.weight) load8(a.post.weight, e0, D, w);
-        if (a.post.bias) load8(a.post.bias, e0, D, b);
-        if (a.gate) load_mod<kBF16>(a.gate, mrow * a.gate_stride, a.mod_f32, e0, D, g);
-        v8u o;
+        float t[8], p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = widen<kBF16>(yr[k][c][i]);
+        if (a.post.kind != kNormNone) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = (t[i] - mu) * r;
+          if (a.post.weight) {
+            load8(a.post.weight, e0, D, p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] *= p[i];
+          }
+          if (a.post.bias) {
+            load8(a.post.bias, e0, D, p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] += p[i];
+          }
+        }
+        if (a.gate) {
+          load_mod<kBF16>(a.gate, mrow * a.gate_stride, a.mod_f32, e0, D, p);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] *= p[i];
+        }
+        const int left = D - e0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const double t = __fma_rn((y[k][c + i] - mu) * r, (double)w[i], (double)b[i]);
-          const double h = __fma_rn((double)g[i], t, a.residual_scale * v[k][c + i]);
-          v[k][c + i] = e0 + i < D ? h : 0.0;
-          o[i] = narrow<kBF16>(h);
+          const float v = __fmaf_rn(a.residual_scale, widen<kBF16>(xr[k][c][i]), t[i]);
+          h[k][c][i] = i < left ? v : 0.0f;
         }
-        store8(hr, e0, D, o);
+        store8(a.h + row * D, e0, D, narrow<kBF16>(h[k][c]));
       }
   }
   if constexpr (OUT == kOutNone) return;
+  auto at = [&](int k, int c, int i) {
+    if constexpr (RES) return h[k][c][i];
+    else return widen<kBF16>(xr[k][c][i]);
+  };
 
-  double mu, r;
-  statistics<V, S>(v, a.norm.kind, (double)a.norm.eps, D, waves, wave, lane, &part[2], mu, r);
-  float f[kTurn ? S : 1][16];
+  float mu, r;
+  statistics<V, S, WAVES>(
+      at, first,
+      [&](float by) {
+        if constexpr (RES) {
+#pragma unroll
+          for (int k = 0; k < S; ++k)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) h[k][c][i] *= by;
+        } else {
+          rescale(xr, by);
+        }
+      },
+      a.norm.kind, a.norm.eps, D, &part[3], mu, r);
+  float f[kTurn ? (OUT == kOutInt8 ? S : 1) : 1][16];
   const int seg = (int)threadIdx.x >> 4, sl = lane & 15;
 #pragma unroll
   for (int k = 0; k < S; ++k) {
+    float(&n)[16] = f[OUT == kOutInt8 ? k : 0];
+    if constexpr (OUT == kOutInt8) {
 #pragma unroll
-    for (int c = 0; c < V; c += 8) {
-      const int e0 = first(k) + c;
+      for (int i = 0; i < 16; ++i) n[i] = 0.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e0 = first(k) + 8 * c;
       if (e0 >= D) continue;
-      float w[8] = {1, 1, 1, 1, 1, 1, 1, 1}, b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      float sc[8] = {0, 0, 0, 0, 0, 0, 0, 0}, sh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (a.norm.weight) load8(a.norm.weight, e0, D, w);
-      if (a.norm.bias) load8(a.norm.bias, e0, D, b);
-      if (a.scale) load_mod<kBF16>(a.scale, mrow * a.scale_stride, a.mod_f32, e0, D, sc);
-      if (a.shift) load_mod<kBF16>(a.shift, mrow * a.shift_stride, a.mod_f32, e0, D, sh);
+      float t[8], p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double t = __fma_rn((v[k][c + i] - mu) * r, (double)w[i], (double)b[i]);
-        v[k][c + i] = __fma_rn(t, 1.0 + (double)sc[i], (double)sh[i]);
+      for (int i = 0; i < 8; ++i) t[i] = (at(k, c, i) - mu) * r;
+      if (a.norm.weight) {
+        load8(a.norm.weight, e0, D, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] *= p[i];
       }
-      if constexpr (!kTurn) {
-        v8u o;
+      if (a.norm.bias) {
+        load8(a.norm.bias, e0, D, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = narrow<kBF16>(v[k][c + i]);
-        store8(static_cast<uint16_t*>(a.values) + row * D, e0, D, o);
+        for (int i = 0; i < 8; ++i) t[i] += p[i];
+      }
+      if (a.scale) {
+        load_mod<kBF16>(a.scale, mrow * a.scale_stride, a.mod_f32, e0, D, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = __fmaf_rn(t[i], p[i], t[i]);
+      }
+      if (a.shift) {
+        load_mod<kBF16>(a.shift, mrow * a.shift_stride, a.mod_f32, e0, D, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] += p[i];
+      }
+      if constexpr (kTurn) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[8 * c + i] = __fmaf_rn(t[i], 0.0625f, 0.0f);   // a zero becomes +0
+      } else {
+        store8(static_cast<uint16_t*>(a.values) + row * D, e0, D, narrow<kBF16>(t));
       }
     }
     if constexpr (kTurn) {
       // D is a multiple of 256, so the 16 lanes of a group are all inside or all outside
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[k][i] = __fma_rn(v[k][i], 0.0625, 0.0);   // a zero becomes +0
-        f[k][i] = 0.0f;
+      if (first(k) < D) {
+        rotate_rows(n, slots + seg * kTurnSlot, sl);
+        if constexpr (OUT == kOutMx)
+          mx_store<0>(n, row, a.M, D, first(k) / kGroup, sl, static_cast<uint8_t*>(a.values),
+                      static_cast<uint8_t*>(a.scales));
       }
-      if (first(k) < D) rotate_rows(v[k], slots + seg * kSlotBytes, sl, f[k]);
     }
-  }
-  if constexpr (OUT == kOutMx) {
-#pragma unroll
-    for (int k = 0; k < S; ++k)
-      if (first(k) < D)
-        mx_store<0>(f[k], row, a.M, D, first(k) / kGroup, sl, static_cast<uint8_t*>(a.values),
-                    static_cast<uint8_t*>(a.scales));
   }
   if constexpr (OUT == kOutInt8) {
     uint32_t m = 0;
@@ -282,11 +399,12 @@ norm_kernel(NormArgs a, int waves) {
     m = seg_max16_bits(m);
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    if (waves > 1) {
+    if (WAVES > 1) {
       if (lane == 0) top[wave] = m;
       __syncthreads();
       m = top[0];
-      for (int w = 1; w < waves; ++w) m = max(m, top[w]);
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) m = max(m, top[w]);
     }
     const bool finite = m < 0x7F800000u;
     const float s = finite ? __uint_as_float(m) / 127.0f : __uint_as_float(0x7FC00000u);
@@ -299,29 +417,34 @@ norm_kernel(NormArgs a, int waves) {
   }
 }
 
-template <bool kBF16, int OUT, bool RES, int S>
-hipError_t launch(const NormArgs& a, int waves, hipStream_t stream) {
+template <bool kBF16, int OUT, bool RES, int S, int WAVES>
+hipError_t launch(const NormArgs& a, hipStream_t stream) {
   constexpr bool kTurn = OUT == kOutInt8 || OUT == kOutMx;
-  const int rows = waves == 1 ? 4 : 1, threads = 64 * waves * rows;
-  const size_t lds = kTurn ? (size_t)threads / 16 * kSlotBytes : 0;
-  const auto fn = &norm_kernel<kBF16, OUT, RES, S>;
+  const int rows = WAVES == 1 ? 4 : 1, threads = 64 * WAVES * rows;
+  const size_t lds = kTurn ? (size_t)threads / 16 * kTurnSlot : 0;
+  const auto fn = &norm_kernel<kBF16, OUT, RES, S, WAVES>;
   if (const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fn), lds); e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3((unsigned)((a.M + rows - 1) / rows)), dim3(threads), lds, stream, a, waves);
+  hipLaunchKernelGGL(fn, dim3((unsigned)((a.M + rows - 1) / rows)), dim3(threads), lds, stream, a);
   return hipGetLastError();
 }
 
-// Wavefronts a row and units a lane: one wavefront with up to 32 elements a
-// lane (no barrier), more for wider rows.
+// Wavefronts a row and units a lane.  Many rows: one wavefront with up to 32
+// elements a lane (no barrier), more for wider rows.  Few rows: as many
+// wavefronts as the row has units for, which is where the latency is.
 template <bool kBF16, int OUT, bool RES>
 hipError_t choose(const NormArgs& a, hipStream_t stream) {
   constexpr int V = OUT == kOutInt8 || OUT == kOutMx ? 16 : 8, kMost = 32 / V;
   const int units = (a.D + 64 * V - 1) / (64 * V);   // of a wavefront's lanes, over the row
-  int waves = 1;
-  while (waves * kMost < units) waves *= 2;
-  const int s = (units + waves - 1) / waves;
-  if (s == 1) return launch<kBF16, OUT, RES, 1>(a, waves, stream);
-  if (s == 2 || kMost == 2) return launch<kBF16, OUT, RES, 2>(a, waves, stream);
-  return launch<kBF16, OUT, RES, kMost>(a, waves, stream);
+  const bool few = a.M <= 512;
+  if (units <= 1) return launch<kBF16, OUT, RES, 1, 1>(a, stream);
+  if (!few) {
+    if (units <= 2) return launch<kBF16, OUT, RES, 2, 1>(a, stream);
+    if (kMost == 4 && units <= 4) return launch<kBF16, OUT, RES, kMost, 1>(a, stream);
+  }
+  if (units <= 2) return launch<kBF16, OUT, RES, 1, 2>(a, stream);
+  if (units <= 4 && (few || kMost == 2)) return launch<kBF16, OUT, RES, 1, 4>(a, stream);
+  if (units <= 4 * kMost) return launch<kBF16, OUT, RES, kMost, 4>(a, stream);
+  return launch<kBF16, OUT, RES, kMost / 2, 16>(a, stream);   // 1024 elements a wavefront: D up to 16384
 }
 
 template <bool kBF16>

@@ -21,7 +21,7 @@ struct NormArgs {
   int64_t x_stride, y_stride;
   int64_t M;
   int D;
-  double residual_scale;
+  float residual_scale;
   NormDesc post, norm;
   const void *scale, *shift, *gate;   // rows of the modulation or null
   int64_t scale_stride, shift_stride, gate_stride;

@@ -74,7 +74,7 @@ convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_str
   a.y_stride = y_stride;
   a.M = M;
   a.D = (int)D;
-  a.residual_scale = (double)residual_scale;
+  a.residual_scale = residual_scale;
   a.post = view(post);
   a.norm = view(norm);
   a.h = static_cast<uint16_t*>(H);

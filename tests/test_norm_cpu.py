@@ -98,7 +98,7 @@ def test_refusals(L, residual):
     def call(**kw):
         return _call(L, residual, **kw)
 
-    for m, d in ((-1, 512), ((1 << 24) + 1, 8), (4, 0), (4, -1), (4, 32769), (1 << 21, 32768)):
+    for m, d in ((-1, 512), ((1 << 24) + 1, 8), (4, 0), (4, -1), (4, 16385), (1 << 22, 16384)):
         assert call(m=m, d=d) == SHAPE, (m, d)
     assert call(dtype=2) == INVALID and call(dtype=-1) == INVALID
     assert call(norm=None) == INVALID and call(out=None) == INVALID
