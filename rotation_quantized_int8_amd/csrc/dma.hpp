@@ -49,6 +49,14 @@ __device__ __forceinline__ void dma4(const void* gptr, uint32_t lds) {
                :: "v"(gptr), "s"(lds) : "memory", "m0");
 }
 
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+  const uint64_t b = (uint64_t)base;
+  base = (const void*)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+
 // Eight fp16 additions, each rounded once (fp32 sum, then fp16).
 __device__ __forceinline__ v4i add_f16x8(v4i a, v4i b) {
   const __half* x = reinterpret_cast<const __half*>(&a);

@@ -1,22 +1,26 @@
 // The product of microscaled 4-bit rows, Y = out(X W^T + bias + residual), on
 // the scaled matrix instructions of gfx950.
 //
-// Mathematics.  v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 rows
-// over 128 elements, four blocks of 32 with a scale each: a lane holds one
-// block of one row (16 bytes) and, in a byte of a register, its scale.  The sum
-// over K does not ask which block a lane takes, as long as both operands agree:
-// of a rotation group (8 blocks, 128 bytes a row) lane quarter q takes blocks 2q
-// and 2q + 1, one an instruction, so that its two scales are neighbouring bytes
-// of the layout [K / 256, rows, 8] and one 16-bit read serves both instructions.
+// Mathematics.  v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 rows by 32 rows
+// over 64 elements, two blocks of 32 with a scale each: a lane holds one block of
+// one row (16 bytes) and, in a byte of a register, its scale.  The sum over K does
+// not ask which blocks an instruction takes, as long as both operands agree: of a
+// rotation group (8 blocks, 128 bytes a row) lane half q takes blocks 4q .. 4q + 3,
+// one an instruction, so that its four scales are one word of the layout
+// [K / 256, rows, 8].  Of the two shapes this one is faster (operands in registers:
+// 8.7 PFLOP/s against 6.2 with 16x16x128, whose issue takes as long as its product;
+// with operands of random bits 6.1, where the clock gives way).
 //
 // Data flow.  Tiles as in the int8 product: direct global->LDS loads into a ring
-// of STAGES slices of one rotation group, 16-byte chunks XOR-swizzled by row & 7
-// (conflict-free fills and reads); the slice's scales, 8 bytes a row, follow the
-// codes in the same ring.  The weight tile is the left operand, so a lane's four
-// accumulators are four neighbouring outputs of one row.
+// of STAGES slices of one rotation group, 16-byte chunks XOR-swizzled by
+// (row >> 1) & 7 (16 rows cover all banks; row & 7 leaves 7 times the conflicts); the slice's scales, 8 bytes a row, follow the
+// codes in the same ring.  The weight tile is the left operand, so a lane's
+// accumulators are fours of neighbouring outputs of one row.
 //
 // Rows past M or N repeat the last valid row for the loads and are dropped in
 // the epilogue.
+
+#include <type_traits>
 
 #include "dma.hpp"
 #include "mx.hpp"
@@ -25,213 +29,349 @@ namespace convrot {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
-// acc += (w 2^sw) (x 2^sx)^T; byte kk of the registers sw and sx.
+// The four registers of e2m1 operands in the eight that the builtins take.
+__device__ __forceinline__ v8i as_operand(v4i v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+
+// acc += (w 2^sw) (x 2^sx)^T; byte kk of the registers sw and sx (4: e2m1).
 template <int kk>
 __device__ __forceinline__ v4f mx_mfma(v4i w, v4i x, v4f acc, int sw, int sx) {
-  const v8i a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
-  const v8i b = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, kk, sw, kk, sx);   // 4: e2m1
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(as_operand(w), as_operand(x), acc, 4, 4, kk, sw, kk, sx);
+}
+template <int kk>
+__device__ __forceinline__ v16f mx_mfma(v4i w, v4i x, v16f acc, int sw, int sx) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_operand(w), as_operand(x), acc, 4, 4, kk, sw, kk, sx);
 }
 
 __device__ __forceinline__ float in16_to_f32(uint16_t bits, int bf16) {
   return bf16 ? bf16_to_f32(bits) : __half2float(__ushort_as_half(bits));
 }
 
-// Four neighbouring outputs (row m, columns n ..) from finished sums: bias and
-// residual added in fp32, one rounding; columns past N give anything.
-__device__ __forceinline__ uint2 mx_finish(const MxGemm& p, v4f y, int64_t m, int64_t n, const float (&bias)[4]) {
-  if (p.bias) {
+// Two finished sums to the output's type, each rounded once to nearest even.
+__device__ __forceinline__ uint32_t out_pair(float a, float b, int bf16) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return bf16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2)) : pack_f16x2_rn(a, b);
+}
+
+// C neighbouring outputs of row m from column n: y + bias + residual in fp32,
+// rounded once and stored.  `whole`: all C columns are inside (rows may start at
+// any element); else element by element.  The residual is read by the thread that
+// writes the element, before it: it may be the output.
+template <int C>
+__device__ __forceinline__ void finish(const MxGemm& p, float (&y)[C], int64_t m, int64_t n, const float (&bias)[C],
+                                       bool whole) {
+  typedef uint16_t vec __attribute__((ext_vector_type(C)));
+  typedef vec vec_any __attribute__((aligned(2)));
+  const int64_t at = m * p.N + n;
+  const uint16_t* res = static_cast<const uint16_t*>(p.res);
+  uint16_t* out = static_cast<uint16_t*>(p.out);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) y[r] += bias[r];
-  }
-  if (p.res) {
-    const uint16_t* src = static_cast<const uint16_t*>(p.res) + m * p.N + n;
-    uint16_t h[4];
-    if ((p.N & 3) == 0 && n < p.N) {
-      const uint2 t = *reinterpret_cast<const uint2*>(src);
-      h[0] = t.x & 0xFFFF;
-      h[1] = t.x >> 16;
-      h[2] = t.y & 0xFFFF;
-      h[3] = t.y >> 16;
+  for (int r = 0; r < C; ++r) y[r] += bias[r];
+  if (res) {
+    vec h;
+    if (whole) {
+      h = __builtin_nontemporal_load(reinterpret_cast<const vec_any*>(res + at));
     } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) h[r] = n + r < p.N ? src[r] : 0;
+      for (int r = 0; r < C; ++r) h[r] = n + r < p.N ? res[at + r] : 0;
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) y[r] += in16_to_f32(h[r], p.bf16);
+    for (int r = 0; r < C; ++r) y[r] += in16_to_f32(h[r], p.bf16);
   }
-  uint2 v;
-  if (p.bf16) {
-    v.x = (uint32_t)f32_to_bf16_rn(y[0]) | (uint32_t)f32_to_bf16_rn(y[1]) << 16;
-    v.y = (uint32_t)f32_to_bf16_rn(y[2]) | (uint32_t)f32_to_bf16_rn(y[3]) << 16;
+  vec v;
+#pragma unroll
+  for (int r = 0; r < C; r += 2) {
+    const uint32_t w = out_pair(y[r], y[r + 1], p.bf16);
+    v[r] = (uint16_t)w;
+    v[r + 1] = (uint16_t)(w >> 16);
+  }
+  if (whole) {
+    __builtin_nontemporal_store(v, reinterpret_cast<vec_any*>(out + at));
   } else {
-    v.x = pack_f16x2_rn(y[0], y[1]);
-    v.y = pack_f16x2_rn(y[2], y[3]);
+#pragma unroll
+    for (int r = 0; r < C; ++r)
+      if (n + r < p.N) out[at + r] = v[r];
   }
-  return v;
+}
+
+// -0, so that a sum without a bias stays as it is.
+template <int C>
+__device__ __forceinline__ void load_bias(const MxGemm& p, int64_t n, float (&bias)[C]) {
+#pragma unroll
+  for (int r = 0; r < C; ++r) bias[r] = p.bias ? p.bias[n + r < p.N ? n + r : p.N - 1] : -0.0f;
 }
 
 template <int WAVES_M, int WAVES_N, int FM, int FN, int STAGES>
 __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
 mx_gemm_kernel(MxGemm p) {
   constexpr int NW = WAVES_M * WAVES_N;
-  constexpr int WM = 16 * FM, WN = 16 * FN;
+  constexpr int WM = 32 * FM, WN = 32 * FN;
   constexpr int BM = WAVES_M * WM, BN = WAVES_N * WN;
+  constexpr int NKK = 4;                                          // K steps (64 elements) of a slice
   constexpr int XL = BM / 8 / NW, WL = BN / 8 / NW;               // 1 KiB blocks (8 rows) a wave loads per slice
   constexpr int SL = ((BM + BN) / 32 + NW - 1) / NW;              // 256-byte blocks of scales (32 rows)
   constexpr int LPW = XL + WL + SL;
   constexpr int XBYTES = BM * 128, WBYTES = BN * 128, SBYTES = SL * NW * 256;
   constexpr int STAGE = XBYTES + WBYTES + SBYTES;
   constexpr int kAhead = (STAGES - 2) * LPW;
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && (BM + BN) % 32 == 0, "blocks split evenly over waves");
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 32 == 0, "blocks split evenly over waves");
   static_assert(STAGES >= 2 && kAhead < 64, "pipeline depth");
+  constexpr bool kDeep = FM * FN <= 4;                            // fragments of whole slices in registers
 
   extern __shared__ __align__(16) char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int64_t M = p.M, N = p.N, nk = p.K / kGroup, ld = p.K / 2;
   const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN, T = tiles_m * tiles_n;
-  int64_t t;
-  {
-    const int64_t b = blockIdx.x, x = b & 7, i = b >> 3, per = T >> 3, rem = T & 7;
-    t = x * per + (x < rem ? x : rem) + i;
-  }
-  const int64_t in_group = p.group_m * tiles_n;
-  const int64_t first_m = (t / in_group) * p.group_m;
-  const int64_t gsize = (tiles_m - first_m) < p.group_m ? (tiles_m - first_m) : p.group_m;
-  const int64_t m0 = (first_m + (t % in_group) % gsize) * BM, n0 = ((t % in_group) / gsize) * BN;
+  // XCD-aware order as in the int8 product (fewer than 2^23 tiles): the i-th
+  // workgroup on XCD x takes the i-th tile of a contiguous range
+  const uint32_t b = blockIdx.x, xcd = b & 7, per = (uint32_t)T >> 3, rem = (uint32_t)T & 7;
+  const uint32_t t = xcd * per + (xcd < rem ? xcd : rem) + (b >> 3);
+  const uint32_t gm = (uint32_t)p.group_m, in_group = gm * (uint32_t)tiles_n;
+  const uint32_t group = t / in_group, in = t - group * in_group, first_m = group * gm;
+  const uint32_t gsize = (uint32_t)tiles_m - first_m < gm ? (uint32_t)tiles_m - first_m : gm;
+  const int64_t m0 = (int64_t)(first_m + in % gsize) * BM, n0 = (int64_t)(in / gsize) * BN;
 
-  const char* srcx[XL];
-  const char* srcw[WL];
-  const char* srcs[SL];
-  int64_t steps[SL];   // bytes from one group's scales to the next group's
+  // Sources of this wave's loads: a base for the tile, which advances by slices,
+  // and an offset for each lane (at most 256 rows of 64 KiB).
+  uint32_t offx[XL], offw[WL], offs[SL];
+  bool sc_x[SL];
+  auto key = [](int r) { return (r >> 1) & 7; };   // swizzle of row r's chunks
 #pragma unroll
   for (int i = 0; i < XL; ++i) {
     const int r = 8 * (wave * XL + i) + (lane >> 3);
     const int64_t row = m0 + r < M ? m0 + r : M - 1;
-    srcx[i] = reinterpret_cast<const char*>(p.x) + row * ld + 16 * ((lane & 7) ^ (r & 7));
+    offx[i] = (uint32_t)((row - m0) * ld) + 16 * ((lane & 7) ^ key(r));
   }
 #pragma unroll
   for (int i = 0; i < WL; ++i) {
     const int r = 8 * (wave * WL + i) + (lane >> 3);
     const int64_t row = n0 + r < N ? n0 + r : N - 1;
-    srcw[i] = reinterpret_cast<const char*>(p.w) + row * ld + 16 * ((lane & 7) ^ (r & 7));
+    offw[i] = (uint32_t)((row - n0) * ld) + 16 * ((lane & 7) ^ key(r));
   }
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
-    const int r = 32 * (wave * SL + i) + (lane >> 1);
-    const bool of_x = r < BM;      // rows past both tiles repeat the last weight row
-    const int64_t first = of_x ? m0 + r : n0 + r - BM, rows = of_x ? M : N;
-    const int64_t row = first < rows ? first : rows - 1;
-    srcs[i] = reinterpret_cast<const char*>(of_x ? p.xs : p.ws) + row * 8 + 4 * (lane & 1);
-    steps[i] = rows * 8;
+    // 32 rows a load, of one operand (past both tiles: weight rows that no one reads)
+    const int r0 = 32 * (wave * SL + i), r = r0 + (lane >> 1);
+    sc_x[i] = r0 < BM;
+    const int64_t first = sc_x[i] ? m0 : n0, rows = sc_x[i] ? M : N;
+    const int64_t row = first + (sc_x[i] ? r : r - BM);
+    offs[i] = (uint32_t)(((row < rows ? row : rows - 1) - first) * 8) + 4 * (lane & 1);
   }
+  const uint8_t* basex = p.x + m0 * ld;
+  const uint8_t* basew = p.w + n0 * ld;
+  const uint8_t* basexs = p.xs + m0 * 8;
+  const uint8_t* basews = p.ws + n0 * 8;
   const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
-  auto issue = [&](int64_t kt) {
-    const uint32_t at = lds_base + ((uint32_t)kt % STAGES) * STAGE;
-#pragma unroll
-    for (int i = 0; i < XL; ++i)
-      dma16(srcx[i] + kt * 128, __builtin_amdgcn_readfirstlane(at + (wave * XL + i) * 1024));
-#pragma unroll
-    for (int i = 0; i < WL; ++i)
-      dma16(srcw[i] + kt * 128, __builtin_amdgcn_readfirstlane(at + XBYTES + (wave * WL + i) * 1024));
-#pragma unroll
-    for (int i = 0; i < SL; ++i)
-      dma4(srcs[i] + kt * steps[i],
+  // load u of slice kt's LPW to the buffer at `at`
+  auto issue_one = [&](int u, int64_t kt, uint32_t at) {
+    if (u < XL) {
+      dma16(basex + kt * 128, offx[u], __builtin_amdgcn_readfirstlane(at + (wave * XL + u) * 1024));
+    } else if (u < XL + WL) {
+      dma16(basew + kt * 128, offw[u - XL], __builtin_amdgcn_readfirstlane(at + XBYTES + (wave * WL + u - XL) * 1024));
+    } else {
+      const int i = u - XL - WL;
+      dma4(sc_x[i] ? basexs + kt * M * 8 : basews + kt * N * 8, offs[i],
            __builtin_amdgcn_readfirstlane(at + XBYTES + WBYTES + (wave * SL + i) * 256));
+    }
+  };
+  auto issue = [&](int64_t kt, int stage) {
+#pragma unroll
+    for (int u = 0; u < LPW; ++u) issue_one(u, kt, lds_base + stage * STAGE);
   };
 
-  v4f acc[FN][FM];
+  v16f acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  const int frow = lane & 15, fq = lane >> 4;
-  v4i fw[FN], fx[FM];
-  int sw[FN], sx[FM];
-  auto load_scales = [&](const char* st) {
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-      sw[i] = *reinterpret_cast<const uint16_t*>(st + XBYTES + WBYTES + (BM + wn * WN + i * 16 + frow) * 8 + 2 * fq);
-#pragma unroll
     for (int j = 0; j < FM; ++j)
-      sx[j] = *reinterpret_cast<const uint16_t*>(st + XBYTES + WBYTES + (wm * WM + j * 16 + frow) * 8 + 2 * fq);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  const int frow = lane & 31, fq = lane >> 5;
+  // Fragments of a K step (64 elements) of 32 rows; rows are 32 apart, so the
+  // swizzle is the lane's own.
+  const uint32_t lw = XBYTES + (wn * WN + frow) * 128, lx = (wm * WM + frow) * 128;
+  uint32_t chunk[NKK];
+#pragma unroll
+  for (int kk = 0; kk < NKK; ++kk) chunk[kk] = 16u * ((NKK * fq + kk) ^ key(frow));
+  const uint32_t lsw = XBYTES + WBYTES + (BM + wn * WN + frow) * 8 + NKK * fq;
+  const uint32_t lsx = XBYTES + WBYTES + (wm * WM + frow) * 8 + NKK * fq;
+  auto load_frags = [&](int kk, uint32_t st, v4i (&w)[FN], v4i (&x)[FM]) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) w[i] = *reinterpret_cast<const v4i*>(smem + (st + lw + chunk[kk]) + i * 4096);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) x[j] = *reinterpret_cast<const v4i*>(smem + (st + lx + chunk[kk]) + j * 4096);
   };
-  auto load_frags = [&](const char* st, int kk) {
+  auto load_scales = [&](uint32_t st, int (&w)[FN], int (&x)[FM]) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const int row = wn * WN + i * 16 + frow;
-      fw[i] = *reinterpret_cast<const v4i*>(st + XBYTES + row * 128 + 16 * ((2 * fq + kk) ^ (row & 7)));
-    }
+    for (int i = 0; i < FN; ++i) w[i] = *reinterpret_cast<const int*>(smem + (st + lsw) + i * 256);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int row = wm * WM + j * 16 + frow;
-      fx[j] = *reinterpret_cast<const v4i*>(st + row * 128 + 16 * ((2 * fq + kk) ^ (row & 7)));
-    }
+    for (int j = 0; j < FM; ++j) x[j] = *reinterpret_cast<const int*>(smem + (st + lsx) + j * 256);
   };
 
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s)
-    if (s < nk) issue(s);
-  for (int64_t kt = 0; kt < nk; ++kt) {
-    // slice kt has landed for this wave once only the later ones are in flight;
-    // the barrier publishes every wave's part and frees the slice before it
-    if (kt + STAGES - 2 < nk) wait_vmcnt<kAhead>();
-    else wait_vmcnt<0>();
-    lds_barrier();
-    if (kt + STAGES - 1 < nk) issue(kt + STAGES - 1);
-    const char* st = smem + ((uint32_t)kt % STAGES) * STAGE;
-    load_scales(st);
-    load_frags(st, 0);
+    if (s < nk) issue(s, s);
+  if (nk >= STAGES - 1) wait_vmcnt<kAhead>();
+  else wait_vmcnt<0>();
+  lds_barrier();
+  if (STAGES - 1 < nk) issue(STAGES - 1, STAGES - 1);
+  int stage = 0;
+  using yes = std::true_type;
+  using no = std::false_type;
+  int64_t kt = 0;
+  if constexpr (kDeep) {
+    // Small tiles: a step's products take less than an LDS read, so the fragments
+    // of a whole slice are read under the products of the slice before it (128x64
+    // tile, 1024 x 2048 x 8192: 18.4 us; step by step 21.3).  Behind the barrier every
+    // read of slice kt is done and slice kt + 1 is published.
+    struct Slice {
+      v4i w[NKK][FN], x[NKK][FM];
+      int sw[FN], sx[FM];
+    } one, two;
+    auto read = [&](Slice& s, uint32_t st) {
+      load_scales(st, s.sw, s.sx);
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+      for (int kk = 0; kk < NKK; ++kk) load_frags(kk, st, s.w[kk], s.x[kk]);
+    };
+    auto products = [&](auto kk, const Slice& s) {
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = mx_mfma<0>(fw[i], fx[j], acc[i][j], sw[i], sx[j]);
-    load_frags(st, 1);
+      for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+        for (int j = 0; j < FM; ++j)
+          acc[i][j] = mx_mfma<kk.value>(s.w[kk.value][i], s.x[kk.value][j], acc[i][j], s.sw[i], s.sx[j]);
+    };
+    auto all = [&](const Slice& s) {
+      products(std::integral_constant<int, 0>{}, s);
+      products(std::integral_constant<int, 1>{}, s);
+      products(std::integral_constant<int, 2>{}, s);
+      products(std::integral_constant<int, 3>{}, s);
+    };
+    auto slice = [&](int64_t kt, auto refill, const Slice& now, Slice& next) {
+      const uint32_t st = stage * STAGE;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      if constexpr (refill) wait_vmcnt<kAhead>();
+      else wait_vmcnt<0>();
+      lds_barrier();
+      read(next, stage * STAGE);
+      if constexpr (refill) {
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = mx_mfma<1>(fw[i], fx[j], acc[i][j], sw[i], sx[j]);
+        for (int u = 0; u < LPW; ++u) issue_one(u, kt + STAGES, lds_base + st);
+      }
+      all(now);
+    };
+    read(one, 0);
+    for (; kt + 1 < nk - STAGES; kt += 2) {
+      slice(kt, yes{}, one, two);
+      slice(kt + 1, yes{}, two, one);
+    }
+    if (kt < nk - STAGES) {
+      slice(kt, yes{}, one, two);
+      ++kt;
+      one = two;
+    }
+    for (; kt < nk - 1; ++kt) {
+      slice(kt, no{}, one, two);
+      one = two;
+    }
+    all(one);
+  } else {
+    // Large tiles: one slice in NKK steps, each step's fragments read under the
+    // products of the one before.  Before the last step every read of the slice is
+    // done, so behind one barrier the slice after it is published and its buffer
+    // refilled, a few loads at a time between the products, and the next slice's
+    // first fragments are read under the last step's products.
+    v4i fw[2][FN], fx[2][FM];
+    int sw[FN], sx[FM];
+    auto products = [&](auto kk) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          acc[i][j] = mx_mfma<kk.value>(fw[kk.value & 1][i], fx[kk.value & 1][j], acc[i][j], sw[i], sx[j]);
+    };
+    auto slice = [&](int64_t kt, auto refill, auto last) {
+      const uint32_t st = stage * STAGE;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      const uint32_t next = stage * STAGE;
+      load_frags(1, st, fw[1], fx[1]);
+      products(std::integral_constant<int, 0>{});
+      load_frags(2, st, fw[0], fx[0]);
+      products(std::integral_constant<int, 1>{});
+      load_frags(3, st, fw[1], fx[1]);
+      products(std::integral_constant<int, 2>{});
+      int nsw[FN], nsx[FM];
+      if constexpr (!last) {
+        if constexpr (refill) wait_vmcnt<kAhead>();
+        else wait_vmcnt<0>();
+        lds_barrier();
+        load_scales(next, nsw, nsx);
+        load_frags(0, next, fw[0], fx[0]);
+      }
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+          constexpr int kProducts = FN * FM;
+          const int t = i * FM + j;
+          acc[i][j] = mx_mfma<NKK - 1>(fw[1][i], fx[1][j], acc[i][j], sw[i], sx[j]);
+          if constexpr (refill) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = t * LPW / kProducts; u < (t + 1) * LPW / kProducts; ++u)
+              issue_one(u, kt + STAGES, lds_base + st);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      if constexpr (!last) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) sw[i] = nsw[i];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) sx[j] = nsx[j];
+      }
+    };
+    load_scales(0, sw, sx);
+    load_frags(0, 0, fw[0], fx[0]);
+    for (; kt < nk - STAGES; ++kt) slice(kt, yes{}, no{});
+    for (; kt < nk - 1; ++kt) slice(kt, no{}, no{});
+    slice(kt, no{}, yes{});
   }
 
-  // The finished tile goes through LDS (the ring is free behind the barrier), so
-  // that stores are whole 16-byte chunks of output rows.  A residual is read
-  // here, by the workgroup that writes its tile, before the barrier: it may be
-  // the output.
-  constexpr int ROWB = BN * 2 + 16;
-  static_assert(BM * ROWB <= STAGES * STAGE, "the staged tile must fit in the ring");
+  // The finished tile goes through LDS as fp32, one fragment row of each wavefront
+  // at a time and two buffers in turn, so that residual and output move in whole
+  // 16-byte chunks of rows.  The ring is free behind the first barrier.
+  constexpr int ROWB = BN * 4 + 16, ROWS = 32 * WAVES_M, BUF = ROWS * ROWB;
+  static_assert((FM > 1 ? 2 : 1) * BUF <= STAGES * STAGE, "the staged rows must fit in the ring");
+  constexpr int CPR = BN / 8, NTH = 64 * NW;   // 8 outputs a thread at a time
+  static_assert(NTH % CPR == 0 && ROWS % (NTH / CPR) == 0, "a thread keeps its columns");
+  const int cc = tid % CPR;
+  const int64_t n = n0 + 8 * cc;
+  float bias[8];
+  load_bias(p, n, bias);
+  const bool whole = n + 8 <= N;
   lds_barrier();
 #pragma unroll
-  for (int i = 0; i < FN; ++i) {
-    const int nl = wn * WN + i * 16 + 4 * fq;
-    float bias[4] = {0, 0, 0, 0};
-    if (p.bias) {
+  for (int j = 0; j < FM; ++j) {
+    char* buf = smem + (j & 1) * BUF;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) bias[r] = p.bias[n0 + nl + r < N ? n0 + nl + r : N - 1];
-    }
+    for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int ml = wm * WM + j * 16 + frow;
-      const int64_t m = m0 + ml < M ? m0 + ml : M - 1;
-      *reinterpret_cast<uint2*>(smem + ml * ROWB + nl * 2) = mx_finish(p, acc[i][j], m, n0 + nl, bias);
-    }
-  }
-  lds_barrier();
-  constexpr int CPR = BN / 8;   // 16-byte chunks of a tile row
-  uint16_t* out = static_cast<uint16_t*>(p.out);
-  for (int c = tid; c < BM * CPR; c += 64 * NW) {
-    const int rl = c / CPR, cc = c - rl * CPR;
-    const int64_t m = m0 + rl, n = n0 + cc * 8;
-    if (m >= M || n >= N) continue;
-    const char* sp = smem + rl * ROWB + cc * 16;
-    uint16_t* gp = out + m * N + n;
-    if ((N & 7) == 0) {
-      __builtin_nontemporal_store(*reinterpret_cast<const v4i*>(sp), reinterpret_cast<v4i*>(gp));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n + e < N) gp[e] = reinterpret_cast<const uint16_t*>(sp)[e];
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<v4f*>(buf + (wm * 32 + frow) * ROWB + (wn * WN + i * 32 + 8 * g + 4 * fq) * 4) =
+            v4f{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    lds_barrier();
+    if (n < N) {
+#pragma unroll 2
+      for (int r = tid / CPR; r < ROWS; r += NTH / CPR) {
+        const int64_t m = m0 + (r >> 5) * WM + j * 32 + (r & 31);
+        if (m >= M) continue;
+        const v4f* src = reinterpret_cast<const v4f*>(buf + r * ROWB + cc * 32);
+        const v4f a = src[0], c = src[1];
+        float y[8] = {a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
+        finish<8>(p, y, m, n, bias, whole);
+      }
     }
   }
 }
@@ -286,20 +426,9 @@ mx_few_kernel(MxGemm p) {
   for (int v = 1; v < WAVES; ++v) y += *reinterpret_cast<const v4f*>(part[v][j][lane]);
   const int64_t m = 16 * j + frow, n = n0 + 4 * fq;
   if (m >= M || n >= N) return;
-  float bias[4] = {0, 0, 0, 0};
-  if (p.bias) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) bias[r] = p.bias[n + r < N ? n + r : N - 1];
-  }
-  const uint2 v = mx_finish(p, y, m, n, bias);
-  uint16_t* out = static_cast<uint16_t*>(p.out) + m * N + n;
-  if ((N & 3) == 0) {
-    *reinterpret_cast<uint2*>(out) = v;
-  } else {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n + r < N) out[r] = (uint16_t)((r < 2 ? v.x : v.y) >> (16 * (r & 1)));
-  }
+  float bias[4], z[4] = {y[0], y[1], y[2], y[3]};
+  load_bias(p, n, bias);
+  finish<4>(p, z, m, n, bias, n + 4 <= N);
 }
 
 // K = 0: every sum is empty.
@@ -319,7 +448,7 @@ mx_empty_kernel(MxGemm p) {
 // resident on one XCD share a few bands of activations and panels of weights.
 template <int WAM, int WAN, int FM, int FN, int ST>
 hipError_t launch_tiles(const MxGemm& args, hipStream_t stream) {
-  constexpr int BM = 16 * FM * WAM, BN = 16 * FN * WAN, NW = WAM * WAN;
+  constexpr int BM = 32 * FM * WAM, BN = 32 * FN * WAN, NW = WAM * WAN;
   constexpr size_t lds = (size_t)ST * ((BM + BN) * 128 + ((BM + BN) / 32 + NW - 1) / NW * NW * 256);
   static_assert(lds <= 160 * 1024, "one CU's LDS");
   MxGemm a = args;
@@ -345,12 +474,22 @@ hipError_t launch_mx_gemm(const MxGemm& a, hipStream_t stream) {
     hipLaunchKernelGGL(mx_empty_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  if (a.M <= 16) return launch_few<1>(a, stream);
-  if (a.M <= 32) return launch_few<2>(a, stream);
+  // Few rows, by size of the weights: the kernel without LDS tiles reads them in
+  // one round trip (1 row, 2048 x 2048: 3.4 us against 5.2; 4096 x 4096 4.4 against
+  // 7.1; 24 rows, 4096 x 8192 9.3 against 11.2), the tiles' direct loads stream
+  // large ones faster (4 rows, 16384 x 8192: 12.5 against 18; 24 rows, 8192 x 2048
+  // 5.4 against 6.1).
+  if (a.M <= 16 && a.N * a.K <= ((int64_t)1 << 26)) return launch_few<1>(a, stream);
+  if (a.M > 16 && a.M <= 32 && a.N <= 4096) return launch_few<2>(a, stream);
+  // Tiles: the largest that fill the card's 256 CUs (128x128 in 4 wavefronts and 70
+  // KB runs twice on one), us: 8192^3 256x256 274, 128x128 315; 4096^3 47, 55;
+  // 1024 x 8192 x 2048 128x128 15.8, 128x64 19.8; 1024 x 2048 x 8192 128x64 18.4,
+  // 64x64 20, 128x128 32; 777 x 1003 x 768 64x64 5.0, 128x64 6.0.
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 256) return launch_tiles<2, 4, 8, 4, 2>(a, stream);
-  if (tiles(128, 128) >= 256) return launch_tiles<2, 2, 4, 4, 2>(a, stream);
-  return launch_tiles<2, 2, 2, 2, 4>(a, stream);
+  if (tiles(256, 256) >= 256) return launch_tiles<2, 4, 4, 2, 2>(a, stream);
+  if (tiles(128, 128) >= 384) return launch_tiles<2, 2, 2, 2, 2>(a, stream);
+  if (tiles(128, 64) >= 256) return launch_tiles<2, 2, 2, 1, 3>(a, stream);
+  return launch_tiles<2, 2, 1, 1, 4>(a, stream);
 }
 
 }  // namespace convrot

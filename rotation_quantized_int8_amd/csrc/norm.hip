@@ -177,7 +177,8 @@ __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by,
 // Rotation of a group whose row `lane` (elements 16 lane .. + 15) this lane
 // holds in fp32, in place: along the row in registers, a transpose in the
 // segment's LDS slot (16-byte chunks swizzled by row, conflict-free both ways),
-// along the column, and the transpose back.  The transform is that of +-1.
+// along the column, and the transpose back.  The transform is that of +-1: what it
+// leaves is 16 u.
 constexpr int kTurnSlot = 1024 + 64;   // bytes: 256 floats, and an offset of 16 banks to the next slot
 __device__ __forceinline__ void fwht16(float (&v)[16]) {
 #pragma unroll
@@ -375,7 +376,7 @@ norm_kernel(NormArgs a) {
       }
       if constexpr (kTurn) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[8 * c + i] = __fmaf_rn(t[i], 0.0625f, 0.0f);   // a zero becomes +0
+        for (int i = 0; i < 8; ++i) n[8 * c + i] = t[i];
       } else {
         store8(static_cast<uint16_t*>(a.values) + row * D, e0, D, narrow<kBF16>(t));
       }
@@ -385,7 +386,7 @@ norm_kernel(NormArgs a) {
       if (first(k) < D) {
         rotate_rows(n, slots + seg * kTurnSlot, sl);
         if constexpr (OUT == kOutMx)
-          mx_store<0>(n, row, a.M, D, first(k) / kGroup, sl, static_cast<uint8_t*>(a.values),
+          mx_store<4>(n, row, a.M, D, first(k) / kGroup, sl, static_cast<uint8_t*>(a.values),
                       static_cast<uint8_t*>(a.scales));
       }
     }
@@ -408,7 +409,7 @@ norm_kernel(NormArgs a) {
     }
     const bool finite = m < 0x7F800000u;
     const float s = finite ? __uint_as_float(m) / 127.0f : __uint_as_float(0x7FC00000u);
-    if (wave == 0 && lane == 0) static_cast<float*>(a.scales)[row] = s;
+    if (wave == 0 && lane == 0) static_cast<float*>(a.scales)[row] = s * 0.0625f;   // the values are 16 u
 #pragma unroll
     for (int k = 0; k < S; ++k)
       if (first(k) < D)
@@ -428,23 +429,33 @@ hipError_t launch(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Wavefronts a row and units a lane.  Many rows: one wavefront with up to 32
-// elements a lane (no barrier), more for wider rows.  Few rows: as many
-// wavefronts as the row has units for, which is where the latency is.
+// Wavefronts a row and units a lane (a unit is 8 or, quantised, 16 elements).
+// Quantised rows have one unit a lane: two are 1 us faster of 32 for 16384 rows
+// of 2048 and slower everywhere else (1024 rows 7.7 against 6.1 us, the residual
+// form of 16384 rows 70.6 against 65.7).  16-bit outputs have two where that still
+// leaves 16 wavefronts a CU (16384 rows of 2048: norm 26.8 against 30.3 us,
+// residual 55 against 58), else one, which is faster by latency (1024 rows of 1024:
+// norm 4.4 against 4.9 us, residual 5.6 against 6.6).  Four units a lane (residual,
+// one wavefront a row of 2048) leave 3 wavefronts a SIMD: 74 us.
 template <bool kBF16, int OUT, bool RES>
 hipError_t choose(const NormArgs& a, hipStream_t stream) {
-  constexpr int V = OUT == kOutInt8 || OUT == kOutMx ? 16 : 8, kMost = 32 / V;
+  constexpr int V = OUT == kOutInt8 || OUT == kOutMx ? 16 : 8;
   const int units = (a.D + 64 * V - 1) / (64 * V);   // of a wavefront's lanes, over the row
-  const bool few = a.M <= 512;
   if (units <= 1) return launch<kBF16, OUT, RES, 1, 1>(a, stream);
-  if (!few) {
-    if (units <= 2) return launch<kBF16, OUT, RES, 2, 1>(a, stream);
-    if (kMost == 4 && units <= 4) return launch<kBF16, OUT, RES, kMost, 1>(a, stream);
+  if constexpr (V == 8) {
+    if (a.M * units > 4096) {
+      if (units <= 2) return launch<kBF16, OUT, RES, 2, 1>(a, stream);
+      if (units <= 4) return launch<kBF16, OUT, RES, 2, 2>(a, stream);
+      if (units <= 8) return launch<kBF16, OUT, RES, 2, 4>(a, stream);
+    }
   }
   if (units <= 2) return launch<kBF16, OUT, RES, 1, 2>(a, stream);
-  if (units <= 4 && (few || kMost == 2)) return launch<kBF16, OUT, RES, 1, 4>(a, stream);
-  if (units <= 4 * kMost) return launch<kBF16, OUT, RES, kMost, 4>(a, stream);
-  return launch<kBF16, OUT, RES, kMost / 2, 16>(a, stream);   // 1024 elements a wavefront: D up to 16384
+  if (units <= 4) return launch<kBF16, OUT, RES, 1, 4>(a, stream);
+  if (units <= 8) return launch<kBF16, OUT, RES, 1, 8>(a, stream);
+  if constexpr (V == 8) {
+    if (units > 16) return launch<kBF16, OUT, RES, 2, 16>(a, stream);
+  }
+  return launch<kBF16, OUT, RES, 1, 16>(a, stream);
 }
 
 template <bool kBF16>
