@@ -177,6 +177,6 @@ def test_binding_refuses_before_the_library():
         with pytest.raises(ValueError, match="GPU"):
             call()
     with pytest.raises(ValueError, match="multiple"):
-        mx._empty4(2, 300, "cpu")
+        mx._empty4(2, 300, x)
     with pytest.raises(ValueError, match="sizes"):
         cr.mx_workspace_bytes(4, 5, 100)

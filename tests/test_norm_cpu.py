@@ -74,23 +74,22 @@ def test_exports_every_declared_symbol(L):
 
 
 def _desc(kind=2, eps=1e-6, weight=C, bias=D):
-    return norms._Desc(kind, eps, weight, bias)
+    return norms._DESC.pack(kind, eps, weight or 0, bias or 0)
 
 
 def _mod(scale=E, shift=F, gate=G, ss=512, hs=512, gs=512, dtype=0, rows=2, index=None):
-    return norms._Modulation(scale, shift, gate, ss, hs, gs, dtype, rows, index)
+    return norms._MOD.pack(scale or 0, shift or 0, gate or 0, ss, hs, gs, dtype, rows, index or 0)
 
 
 def _out(kind=0, values=H, scales=I):
-    return norms._Out(kind, values, scales)
+    return norms._OUT.pack(kind, values or 0, scales or 0)
 
 
 def _call(L, residual, x=A, xs=512, y=B, ys=512, dtype=0, m=4, d=512, norm=_desc(), post=None, mod=_mod(), out=_out(),
           h=J):
-    ref = norms._ref
     if not residual:
-        return L.convrot_norm(x, xs, dtype, m, d, ref(norm), ref(mod), ref(out), None)
-    return L.convrot_residual_norm(x, xs, y, ys, dtype, m, d, 1.0, ref(post), ref(norm), ref(mod), h, ref(out), None)
+        return L.convrot_norm(x, xs, dtype, m, d, norm, mod, out, None)
+    return L.convrot_residual_norm(x, xs, y, ys, dtype, m, d, 1.0, post, norm, mod, h, out, None)
 
 
 @pytest.mark.parametrize("residual", [False, True])
@@ -152,37 +151,63 @@ def test_binding_refuses_before_the_library():
             call(x.half())
         with pytest.raises(TypeError):
             call([1.0])
-    d = torch.device("cpu")
     with pytest.raises(ValueError, match="kind"):
-        norms._desc("batch", 0.0, None, None, 256, d)
+        norms._desc("batch", 0.0, None, None, 256, -1)
     with pytest.raises(TypeError):
-        norms._desc("rms", 0.0, x[0].half(), None, 256, d)
+        norms._desc("rms", 0.0, x[0].half(), None, 256, -1)
     with pytest.raises(ValueError):
-        norms._desc("rms", 0.0, x[0, :5], None, 256, d)
+        norms._desc("rms", 0.0, x[0, :5], None, 256, -1)
     with pytest.raises(ValueError, match="bits"):
-        norms._quantised(2, 256, 5, d)
+        norms._quantised(2, 256, 5, x)
     with pytest.raises(ValueError, match="multiple"):
-        norms._quantised(2, 300, 8, d)
+        norms._quantised(2, 300, 8, x)
+    with pytest.raises(ValueError):
+        norms._alike(x, x[:1])
+    with pytest.raises(ValueError):
+        norms._alike(x, x.half())
+
+
+def test_structures_are_packed_as_c_lays_them_out():
+    class Desc(ctypes.Structure):
+        _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+    class Mod(ctypes.Structure):
+        _fields_ = [*((n, ctypes.c_void_p) for n in ("scale", "shift", "gate")),
+                    *((n, ctypes.c_int64) for n in ("a", "b", "c")), ("dtype", ctypes.c_int), ("rows", ctypes.c_int64),
+                    ("index", ctypes.c_void_p)]
+
+    class Out(ctypes.Structure):
+        _fields_ = [("kind", ctypes.c_int), ("values", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+    for kind, packer, values in ((Desc, norms._DESC, (2, 0.5, 1 << 40, 5)), (Out, norms._OUT, (1, 3 << 40, 7)),
+                                 (Mod, norms._MOD, (1, 2 << 40, 3, 4, 5 << 33, 6, 2, 7 << 34, 8))):
+        raw = packer.pack(*values)
+        assert len(raw) == ctypes.sizeof(kind)
+        got = kind.from_buffer_copy(raw)
+        assert tuple(getattr(got, f[0]) for f in kind._fields_) == values
 
 
 def test_binding_checks_the_modulation():
     x = torch.zeros((6, 8), dtype=torch.float16)
     two, three = torch.zeros((2, 8), dtype=torch.float16), torch.zeros((3, 8), dtype=torch.float16)
-    m, kept = norms._modulation(x, two, two, None, None)
-    assert m.rows == 2 and m.dtype == 0 and m.gate is None and kept[0] is two
-    assert norms._modulation(x, two.float(), None, None, None)[0].dtype == 2
-    assert norms._modulation(x, two[0], None, None, None)[0].rows == 1
-    assert norms._modulation(x, None, None, None, None) == (None, [None] * 3)
+
+    def call(scale=None, shift=None, gate=None, index=None):
+        raw, kept = norms._modulation(x, 6, 8, scale, shift, gate, index)
+        return None if raw is None else norms._MOD.unpack(raw)
+
+    at = two.data_ptr()
+    assert call(two, two) == (at, at, 0, 8, 8, 0, 0, 2, 0)
+    assert call(two.float())[6] == 2 and call(two[0])[7] == 1 and call() is None
     wide = torch.zeros((2, 24), dtype=torch.float16)
-    assert norms._modulation(x, wide[:, 8:16], None, None, None)[0].scale_stride == 24
-    assert norms._modulation(x, two[:1].expand(6, 8), None, None, None)[0].scale_stride == 0
-    for bad in ((two, three), (two, two.float()), (two[:, :4], None), (torch.zeros((4, 8)).half(), None),
-                (two.bfloat16(), None)):
+    assert call(wide[:, 8:16])[:4] == (wide.data_ptr() + 16, 0, 0, 24)
+    assert call(two[:1].expand(6, 8))[3] == 0
+    for bad in ((two, three), (two, two.float()), (two[:, :4],), (torch.zeros((4, 8)).half(),), (two.bfloat16(),)):
         with pytest.raises((ValueError, TypeError)):
-            norms._modulation(x, *bad, None, None)
+            call(*bad)
     index = torch.zeros(6, dtype=torch.int32)
+    assert call(two, index=index)[8] == index.data_ptr()
     for bad in (index.long(), index[:5]):
         with pytest.raises((ValueError, TypeError)):
-            norms._modulation(x, two, None, None, bad)
+            call(two, index=bad)
     with pytest.raises(ValueError):
-        norms._modulation(x, None, None, None, index)
+        call(index=index)
