@@ -58,11 +58,14 @@ convrot_status convrot_mx_gemm(const uint8_t* x_codes, const uint8_t* x_scales, 
                                const uint8_t* w_scales, const float* bias, const void* residual, int64_t M,
                                int64_t N, int64_t K, void* Y, int dtype, void* stream);
 
-/* Bytes of workspace of convrot_mx_linear, (size_t)-1 for invalid sizes. */
+/* Bytes of workspace of convrot_mx_linear (0 where it needs none), (size_t)-1
+ * for invalid sizes. */
 size_t convrot_mx_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* The whole linear: X [M, K] of `x_dtype` quantised as by convrot_mx_act_quant
- * into the workspace, then convrot_mx_gemm with Y of `y_dtype`. */
+ * into the workspace, then convrot_mx_gemm with Y of `y_dtype` (few short rows:
+ * both in one launch, the same bits).  The workspace, which may be NULL where 0
+ * bytes are needed, must not overlap anything. */
 convrot_status convrot_mx_linear(const void* X, int x_dtype, int64_t M, int64_t K, const uint8_t* w_codes,
                                  const uint8_t* w_scales, int64_t N, const float* bias, const void* residual,
                                  void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);

@@ -41,6 +41,17 @@ __device__ __forceinline__ void rotate_rows(double (&v)[16], char* slot, int lan
   wave_lds_sync();
 }
 
+// The rotated values of an activation group from rotate_group's 16 u: fp16 keeps
+// the factor 2^4 (16 u stays in fp32's normal range) and gives it to the scale;
+// bf16 takes u itself, which may be as large or small as fp32 holds.  The sum
+// with 0 makes a zero +0.
+__host__ __device__ constexpr int mx_up(bool bf16) { return bf16 ? 0 : 4; }
+template <bool kBF16>
+__device__ __forceinline__ void mx_rotated(const double (&y)[16], float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = kBF16 ? (float)__fma_rn(y[i], 0.0625, 0.0) : (float)y[i] + 0.0f;
+}
+
 // Scale byte of the block of 32 that this lane and its neighbour (lane ^ 1)
 // hold 16 elements each of; kUp: f is 2^kUp times the value quantised.
 template <int kUp>
@@ -97,5 +108,9 @@ hipError_t launch_mx_act_quant(const void* X, bool bf16, int64_t M, int64_t K, u
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* V,
                                 bool bf16, hipStream_t stream);
 hipError_t launch_mx_gemm(const MxGemm& a, hipStream_t stream);
+// The whole linear in one launch for few short rows: a.x and a.xs are unused, X
+// is the activation [M, K].
+bool mx_fusable(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_fused(const MxGemm& a, const void* X, bool bf16, hipStream_t stream);
 
 }  // namespace convrot

@@ -96,7 +96,7 @@ convrot_status convrot_mx_gemm(const uint8_t* x_codes, const uint8_t* x_scales, 
 
 size_t convrot_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (!sizes_ok(M, N, K)) return (size_t)-1;
-  return M == 0 || N == 0 ? 0 : round256(codes_bytes(M, K)) + round256(scales_bytes(M, K));
+  return M == 0 || N == 0 || mx_fusable(M, N, K) ? 0 : round256(codes_bytes(M, K)) + round256(scales_bytes(M, K));
 }
 
 convrot_status convrot_mx_linear(const void* X, int x_dtype, int64_t M, int64_t K, const uint8_t* w_codes,
@@ -116,14 +116,14 @@ convrot_status convrot_mx_linear(const void* X, int x_dtype, int64_t M, int64_t 
   if (convrot_status st = check_device()) return st;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + round256(codes_bytes(M, K));
+  const MxGemm a{codes, scales, w_codes, w_scales, bias, residual, Y, M, N, K, y_dtype == CONVROT_DTYPE_BF16, 1};
+  if (mx_fusable(M, N, K)) return launched(launch_mx_fused(a, X, x_dtype == CONVROT_DTYPE_BF16, as_stream(stream)));
   if (K) {
     const hipError_t e =
         launch_mx_act_quant(X, x_dtype == CONVROT_DTYPE_BF16, M, K, codes, scales, as_stream(stream));
     if (e != hipSuccess) return CONVROT_ERR_LAUNCH;
   }
-  return launched(launch_mx_gemm(MxGemm{codes, scales, w_codes, w_scales, bias, residual, Y, M, N, K,
-                                        y_dtype == CONVROT_DTYPE_BF16, 1},
-                                 as_stream(stream)));
+  return launched(launch_mx_gemm(a, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -431,6 +431,68 @@ mx_few_kernel(MxGemm p) {
   finish<4>(p, z, m, n, bias, n + 4 <= N);
 }
 
+// The whole linear for few short rows (M G <= 32 rotation groups, G <= 32): every
+// workgroup quantises the activations itself, a group to 16 lanes, while its
+// weights are on their way, then works as mx_few_kernel does, in the same order.
+// One launch instead of two, and no workspace.
+constexpr int kFusedWaves = 8, kFusedGroups = 4 * kFusedWaves;
+template <bool kBF16>
+__global__ void __launch_bounds__(64 * kFusedWaves)
+mx_few_fused_kernel(MxGemm p, const uint16_t* __restrict__ X) {
+  extern __shared__ __align__(16) char smem[];      // kFusedGroups slots; the sums of the wavefronts later
+  __shared__ __align__(16) uint8_t codes[kFusedGroups * 128];
+  __shared__ __align__(8) uint8_t scales[kFusedGroups * 8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int frow = lane & 15, fq = lane >> 4;
+  const int M = (int)p.M, G = (int)(p.K / kGroup);
+  const int64_t N = p.N, ld = p.K / 2, n0 = (int64_t)blockIdx.x * 16;
+  const int64_t wrow = n0 + frow < N ? n0 + frow : N - 1;
+  v4i w[4][2];
+  int sw[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int g = wave + kFusedWaves * t;
+    if (g >= G) break;
+    const v4i* pw = reinterpret_cast<const v4i*>(p.w + wrow * ld + g * 128 + 32 * fq);
+    w[t][0] = __builtin_nontemporal_load(pw);
+    w[t][1] = __builtin_nontemporal_load(pw + 1);
+    sw[t] = *reinterpret_cast<const uint16_t*>(p.ws + (g * N + wrow) * 8 + 2 * fq);
+  }
+  const int seg = threadIdx.x >> 4, sl = threadIdx.x & 15;
+  if (seg < M * G) {
+    double y[16];
+    rotate_group<kBF16>(X + (int64_t)seg * kGroup, smem + seg * kSlotBytes, sl, y);   // groups of a row side by side
+    float f[16];
+    mx_rotated<kBF16>(y, f);
+    const int row = seg / G, g = seg - row * G;
+    mx_store<mx_up(kBF16)>(f, row, M, p.K, g, sl, codes, scales);
+  }
+  __syncthreads();
+  v4f acc = {0, 0, 0, 0};
+  const int xrow = frow < M ? frow : M - 1;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int g = wave + kFusedWaves * t;
+    if (g >= G) break;
+    const v4i* px = reinterpret_cast<const v4i*>(codes + xrow * ld + g * 128 + 32 * fq);
+    const int sx = *reinterpret_cast<const uint16_t*>(scales + (g * M + xrow) * 8 + 2 * fq);
+    acc = mx_mfma<0>(w[t][0], px[0], acc, sw[t], sx);
+    acc = mx_mfma<1>(w[t][1], px[1], acc, sw[t], sx);
+  }
+  v4f* part = reinterpret_cast<v4f*>(smem);         // the slots are free behind the barrier above
+  part[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave) return;
+  v4f y = part[lane];
+#pragma unroll
+  for (int v = 1; v < kFusedWaves; ++v) y += part[v * 64 + lane];
+  const int64_t n = n0 + 4 * fq;
+  if (frow >= M || n >= N) return;
+  float bias[4], z[4] = {y[0], y[1], y[2], y[3]};
+  load_bias(p, n, bias);
+  finish<4>(p, z, frow, n, bias, n + 4 <= N);
+}
+
 // K = 0: every sum is empty.
 __global__ void __launch_bounds__(256)
 mx_empty_kernel(MxGemm p) {
@@ -466,7 +528,30 @@ hipError_t launch_few(const MxGemm& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Few rows, by size of the weights: the kernel without LDS tiles reads them in
+// one round trip (1 row, 2048 x 2048: 3.4 us against 5.2; 4096 x 4096 4.4 against
+// 7.1; 24 rows, 4096 x 8192 9.3 against 11.2), the tiles' direct loads stream
+// large ones faster (4 rows, 16384 x 8192: 12.5 against 18; 24 rows, 8192 x 2048
+// 5.4 against 6.1).
+bool few_rows(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 ? N * K <= ((int64_t)1 << 26) : M <= 32 && N <= 4096;
+}
+
 }  // namespace
+
+bool mx_fusable(int64_t M, int64_t N, int64_t K) {
+  return K > 0 && M <= 16 && M * K <= kFusedGroups * kGroup && few_rows(M, N, K);
+}
+
+hipError_t launch_mx_fused(const MxGemm& a, const void* X, bool bf16, hipStream_t stream) {
+  const auto fn = bf16 ? &mx_few_fused_kernel<true> : &mx_few_fused_kernel<false>;
+  const size_t slots = (size_t)(a.M * (a.K / kGroup)) * kSlotBytes, sums = kFusedWaves * 64 * sizeof(v4f);
+  const size_t lds = slots > sums ? slots : sums;
+  if (const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fn), lds); e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3((unsigned)((a.N + 15) / 16)), dim3(64 * kFusedWaves), lds, stream, a,
+                     static_cast<const uint16_t*>(X));
+  return hipGetLastError();
+}
 
 hipError_t launch_mx_gemm(const MxGemm& a, hipStream_t stream) {
   if (a.K == 0) {
@@ -474,13 +559,7 @@ hipError_t launch_mx_gemm(const MxGemm& a, hipStream_t stream) {
     hipLaunchKernelGGL(mx_empty_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  // Few rows, by size of the weights: the kernel without LDS tiles reads them in
-  // one round trip (1 row, 2048 x 2048: 3.4 us against 5.2; 4096 x 4096 4.4 against
-  // 7.1; 24 rows, 4096 x 8192 9.3 against 11.2), the tiles' direct loads stream
-  // large ones faster (4 rows, 16384 x 8192: 12.5 against 18; 24 rows, 8192 x 2048
-  // 5.4 against 6.1).
-  if (a.M <= 16 && a.N * a.K <= ((int64_t)1 << 26)) return launch_few<1>(a, stream);
-  if (a.M > 16 && a.M <= 32 && a.N <= 4096) return launch_few<2>(a, stream);
+  if (few_rows(a.M, a.N, a.K)) return a.M <= 16 ? launch_few<1>(a, stream) : launch_few<2>(a, stream);
   // Tiles: the largest that fill the card's 256 CUs (128x128 in 4 wavefronts and 70
   // KB runs twice on one), us: 8192^3 256x256 274, 128x128 315; 4096^3 47, 55;
   // 1024 x 8192 x 2048 128x128 15.8, 128x64 19.8; 1024 x 2048 x 8192 128x64 18.4,

@@ -33,12 +33,8 @@ mx_act_quant_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K, uint8_
   double y[16];
   rotate_group<kBF16>(X + row * K + g * kGroup, smem + seg * kSlotBytes, lane, y);
   float f[16];
-  // fp16: 16 u stays in fp32's normal range, and 2^4 goes into the scale;
-  // bf16: u itself, which may be as large or small as fp32 holds.  The sum
-  // with 0 makes a zero +0.
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = kBF16 ? (float)__fma_rn(y[i], 0.0625, 0.0) : (float)y[i] + 0.0f;
-  mx_store<kBF16 ? 0 : 4>(f, row, M, K, g, lane, codes, scales);
+  mx_rotated<kBF16>(y, f);
+  mx_store<mx_up(kBF16)>(f, row, M, K, g, lane, codes, scales);
 }
 
 __global__ void __launch_bounds__(256)

@@ -138,10 +138,11 @@ def test_gemm_refusals(L):
 
 
 def test_linear_refusals(L):
-    need = 4 * 128 + 256                          # codes, and 32 bytes of scales, in pieces of 256
-    assert L.convrot_mx_workspace_bytes(4, 5, 256) == need
+    need = 40 * 128 + 512                         # codes, and 320 bytes of scales, in pieces of 256
+    assert L.convrot_mx_workspace_bytes(40, 5, 256) == need
+    assert L.convrot_mx_workspace_bytes(4, 5, 256) == 0          # few short rows: one launch
 
-    def call(x=A, xd=0, m=4, k=256, w=C, ws=D, n=5, bias=E, res=F, y=G, yd=1, work=H, nbytes=need):
+    def call(x=A, xd=0, m=40, k=256, w=C, ws=D, n=5, bias=E, res=F, y=G, yd=1, work=H, nbytes=need):
         return L.convrot_mx_linear(x, xd, m, k, w, ws, n, bias, res, y, yd, work, nbytes, None)
 
     for rows, k in BAD_ROWS:
@@ -159,7 +160,7 @@ def test_linear_refusals(L):
     for at in (A, C, D, E, F, G):
         assert call(work=at) == INVALID
     assert call(res=G + 16) == INVALID
-    assert L.convrot_mx_workspace_bytes(0, 5, 256) == 0 and L.convrot_mx_workspace_bytes(4, 5, 0) == 0
+    assert L.convrot_mx_workspace_bytes(0, 5, 256) == 0 and L.convrot_mx_workspace_bytes(40, 5, 0) == 0
 
 
 def test_binding_refuses_before_the_library():

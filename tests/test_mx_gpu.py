@@ -232,6 +232,21 @@ def test_linear_is_its_stages(m, dtype):
     _check_product(y[0], *O.product(xv, O.values(*O.unpack(_np(qw), _np(sw))), _np(bias)), 1024, other)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 256), (1, 1000, 8192), (4, 33, 2048), (16, 64, 512), (5, 17, 1536), (3, 16, 2560),
+                                   (2, 16400, 4096)])
+def test_one_launch_is_its_stages(m, n, k, dtype):
+    """Few short rows: every workgroup quantises them itself, to the same bits."""
+    gen = _gen(13, m, n, k)
+    x = _x(gen, m, k, dtype).to(DEV)
+    qw, sw = _random4(gen, n, k, 116, 122)
+    res = torch.randn((m, n), generator=gen).to(dtype).to(DEV)
+    want = cr.mx_gemm(*cr.mx_act_quant(x), qw, sw, residual=res, out_dtype=dtype)
+    assert torch.equal(cr.mx_linear(x, qw, sw, residual=res), want)
+    xv, wv = O.values(*O.quantize(O.rotate_f32(_np(x)))), O.values(*O.unpack(_np(qw), _np(sw)))
+    _check_product(want, *O.product(xv, wv, None, _np(res)), k, dtype)
+
+
 @pytest.mark.parametrize("m", [3, 24, 300, 2100])
 def test_residual_in_place_and_out(m):
     gen = _gen(9, m)
