@@ -41,6 +41,50 @@ __device__ __forceinline__ void rotate_rows(double (&v)[16], char* slot, int lan
   wave_lds_sync();
 }
 
+// Rotation of a group whose row `lane` (elements 16 lane .. + 15) this lane
+// holds in fp32, in place: along the row in registers, a transpose in the
+// segment's LDS slot (16-byte chunks swizzled by row, conflict-free both ways),
+// along the column, and the transpose back.  The transform is that of +-1: what it
+// leaves is 16 u.
+constexpr int kTurnSlot = 1024 + 64;   // bytes: 256 floats, and an offset of 16 banks to the next slot
+__device__ __forceinline__ void fwht16(float (&v)[16]) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+}
+__device__ __forceinline__ void rotate_rows(float (&v)[16], char* slot, int lane) {
+  const int key = (lane >> 2) & 3;
+  fwht16(v);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<float4*>(slot + 64 * lane + 16 * (c ^ key)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  wave_lds_sync();
+  float* sf = reinterpret_cast<float*>(slot) + (lane & 3);
+#pragma unroll
+  for (int a = 0; a < 16; ++a) v[a] = sf[16 * a + 4 * (key ^ (a >> 2))];
+  wave_lds_sync();
+  fwht16(v);
+#pragma unroll
+  for (int a = 0; a < 16; ++a) sf[16 * a + 4 * (key ^ (a >> 2))] = v[a];
+  wave_lds_sync();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4 t = *reinterpret_cast<const float4*>(slot + 64 * lane + 16 * (c ^ key));
+    v[4 * c] = t.x;
+    v[4 * c + 1] = t.y;
+    v[4 * c + 2] = t.z;
+    v[4 * c + 3] = t.w;
+  }
+  wave_lds_sync();
+}
+
 // The rotated values of an activation group from rotate_group's 16 u: fp16 keeps
 // the factor 2^4 (16 u stays in fp32's normal range) and gives it to the scale;
 // bf16 takes u itself, which may be as large or small as fp32 holds.  The sum

@@ -67,6 +67,11 @@ __device__ __forceinline__ int e2m1_twice(uint32_t code) {
   return code & 8 ? -m : m;
 }
 
+// Un-rotation.  A value is a multiple of 2^e / 2 up to 6 2^e, so while the scales
+// of a group lie within 2^12 of one another every partial sum of its 256 values
+// fits fp32's 24 bits and the transform is exact there; groups beyond that (or at
+// the ends of the scales' range, or with a NaN) take the fp64 one.  Blocks of zeros
+// have no say.
 template <bool kBF16>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
@@ -79,19 +84,41 @@ mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restric
   const int64_t row = u / G, g = u - row * G;
   const uint2 c = *reinterpret_cast<const uint2*>(codes + row * (K / 2) + g * 128 + 8 * lane);
   const uint32_t byte = scales[(g * rows + row) * 8 + (lane >> 1)];
-  // 2^(byte - 127) / 2 (the codes are taken twice) / 16 (the transform of +-1)
-  const double s = byte == 255u ? __longlong_as_double(0x7FF8000000000000ll)
-                                : __longlong_as_double((long long)(byte + 1023 - 127 - 5) << 52);
-  double v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = (double)e2m1_twice((i < 8 ? c.x : c.y) >> (4 * (i & 7))) * s;
+  const bool some = ((c.x | c.y) & 0x77777777u) != 0u;
+  // largest scale and smallest (as the largest of 255 - byte) over the 16 lanes
+  const uint32_t high = seg_max16_bits(some || byte == 255u ? byte : 0u);
+  const uint32_t low = 255u - seg_max16_bits(some ? 255u - byte : 0u);
+  char* slot = smem + seg * kSlotBytes;
   float f[16];
-  rotate_rows(v, smem + seg * kSlotBytes, lane, f);
+  if (high < 240u && low >= 8u && high <= low + 12u) {
+    const float s = __uint_as_float((byte > 8u ? byte - 4u : 4u) << 23);   // 1/16 of it: the transform of +-1
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const f2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 1),
+                       __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 3)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[8 * j + 2 * i] = p[i][0], f[8 * j + 2 * i + 1] = p[i][1];
+    }
+    rotate_rows(f, slot, lane);
+  } else {
+    // 2^(byte - 127) / 2 (the codes are taken twice) / 16
+    const double s = byte == 255u ? __longlong_as_double(0x7FF8000000000000ll)
+                                  : __longlong_as_double((long long)(byte + 1023 - 127 - 5) << 52);
+    double v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = (double)e2m1_twice((i < 8 ? c.x : c.y) >> (4 * (i & 7))) * s;
+    rotate_rows(v, slot, lane, f);
+  }
   uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o[i] = kBF16 ? (uint32_t)f32_to_bf16_rn(f[2 * i]) | (uint32_t)f32_to_bf16_rn(f[2 * i + 1]) << 16
+  for (int i = 0; i < 8; ++i) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    o[i] = kBF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){f[2 * i], f[2 * i + 1]}, b2))
                  : pack_f16x2_rn(f[2 * i], f[2 * i + 1]);
+  }
   uint4* dst = reinterpret_cast<uint4*>(V + row * K + g * kGroup + 16 * lane);
   dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);

@@ -137,6 +137,28 @@ def test_dequantize_bit_exact(rows, k, dtype):
     assert torch.equal(cr.mx_dequantize(q, s, dtype).cpu(), want)
 
 
+@pytest.mark.parametrize("low,high", [(120, 121), (120, 132), (120, 133), (8, 20), (7, 19), (228, 239), (230, 240), (0, 254)])
+def test_dequantize_spans_of_scales(low, high):
+    """Groups whose scales lie close together, far apart and at either end, with blocks of zeros among them."""
+    gen = _gen(14, low, high)
+    q, s = _random4(gen, 50, 768, low, high + 1)
+    q.view(50, 24, 16)[torch.rand((50, 24), generator=gen).to(DEV) < 0.2] = 0x80
+    s[torch.rand(s.shape, generator=gen).to(DEV) < 0.3] = low
+    s[:, 3, 2], s[:, 4, 1] = 0, 254
+    q.view(50, 24, 16)[3, 2::8] = q.view(50, 24, 16)[4, 1::8] = 0
+    got, held = cr.mx_dequantize(q, s, BF16), O.unpack(_np(q), _np(s))
+    exact = O.dequantize(*held)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = torch.from_numpy(exact.astype(np.float32)).to(BF16)
+    if high - low <= 45:
+        assert torch.equal(got.cpu().nan_to_num(), want.nan_to_num())
+    else:   # past 45 binades the fp64 sums round: 8 additions, each 2^-53 of what has met so far
+        size = np.abs(O.values(*held)).reshape(50, 3, 256).sum(-1).repeat(256, 1) / 16
+        fits = np.abs(exact) < 3e38
+        err = np.abs(_np(got) - exact)[fits]
+        assert (err <= (2.0 ** -8 * np.abs(exact) + 2.0 ** -50 * size + _step(BF16))[fits]).all()
+
+
 def test_dequantize_extreme_scales():
     s = torch.arange(256, dtype=torch.uint8)[None, :, None].expand(1, 256, 8).contiguous().to(DEV)
     q = torch.full((256, 128), 0xF7, dtype=torch.uint8, device=DEV)            # 6, -6
