@@ -10,38 +10,6 @@ namespace convrot {
 constexpr int kMxBlock = 32;
 
 // Rotation of a group whose row `lane` (elements 16 lane .. + 15) this lane
-// holds in fp64: along the row in registers, a transpose in the segment's LDS
-// slot (kSlotBytes; 16-byte chunks swizzled by row, conflict-free both ways),
-// along the column, the one rounding to fp32, and a transpose back.  On return
-// f[] holds fp32(16 v H) for elements 16 lane .. + 15 (the transform of +-1;
-// callers give v / 16).
-__device__ __forceinline__ void rotate_rows(double (&v)[16], char* slot, int lane, float (&f)[16]) {
-  fwht16(v);
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    *reinterpret_cast<double2*>(slot + 128 * lane + 16 * (q ^ (lane & 7))) = make_double2(v[2 * q], v[2 * q + 1]);
-  wave_lds_sync();
-  const double* sd = reinterpret_cast<const double*>(slot);
-#pragma unroll
-  for (int a = 0; a < 16; ++a) v[a] = sd[16 * a + 2 * ((lane >> 1) ^ (a & 7)) + (lane & 1)];
-  wave_lds_sync();
-  fwht16(v);
-  float* sf = reinterpret_cast<float*>(slot);
-#pragma unroll
-  for (int a = 0; a < 16; ++a) sf[16 * a + 4 * ((lane >> 2) ^ ((a >> 2) & 3)) + (lane & 3)] = (float)v[a];
-  wave_lds_sync();
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const float4 t = *reinterpret_cast<const float4*>(slot + 64 * lane + 16 * (c ^ ((lane >> 2) & 3)));
-    f[4 * c] = t.x;
-    f[4 * c + 1] = t.y;
-    f[4 * c + 2] = t.z;
-    f[4 * c + 3] = t.w;
-  }
-  wave_lds_sync();
-}
-
-// Rotation of a group whose row `lane` (elements 16 lane .. + 15) this lane
 // holds in fp32, in place: along the row in registers, a transpose in the
 // segment's LDS slot (16-byte chunks swizzled by row, conflict-free both ways),
 // along the column, and the transpose back.  The transform is that of +-1: what it
@@ -81,6 +49,34 @@ __device__ __forceinline__ void rotate_rows(float (&v)[16], char* slot, int lane
     v[4 * c + 1] = t.y;
     v[4 * c + 2] = t.z;
     v[4 * c + 3] = t.w;
+  }
+  wave_lds_sync();
+}
+
+// The same in fp64 (kSlotBytes), rounded once to fp32: f[] holds fp32(16 v H).
+__device__ __forceinline__ void rotate_rows(double (&v)[16], char* slot, int lane, float (&f)[16]) {
+  fwht16(v);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<double2*>(slot + 128 * lane + 16 * (q ^ (lane & 7))) = make_double2(v[2 * q], v[2 * q + 1]);
+  wave_lds_sync();
+  const double* sd = reinterpret_cast<const double*>(slot);
+#pragma unroll
+  for (int a = 0; a < 16; ++a) v[a] = sd[16 * a + 2 * ((lane >> 1) ^ (a & 7)) + (lane & 1)];
+  wave_lds_sync();
+  fwht16(v);
+  float* sf = reinterpret_cast<float*>(slot) + (lane & 3);
+  const int key = (lane >> 2) & 3;
+#pragma unroll
+  for (int a = 0; a < 16; ++a) sf[16 * a + 4 * (key ^ (a >> 2))] = (float)v[a];
+  wave_lds_sync();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4 r = *reinterpret_cast<const float4*>(slot + 64 * lane + 16 * (c ^ key));
+    f[4 * c] = r.x;
+    f[4 * c + 1] = r.y;
+    f[4 * c + 2] = r.z;
+    f[4 * c + 3] = r.w;
   }
   wave_lds_sync();
 }

@@ -460,8 +460,10 @@ mx_few_fused_kernel(MxGemm p, const uint16_t* __restrict__ X) {
   }
   const int seg = threadIdx.x >> 4, sl = threadIdx.x & 15;
   if (seg < M * G) {
+    // groups of a row lie side by side
+    const v4i* px = reinterpret_cast<const v4i*>(X + (int64_t)seg * kGroup + 16 * sl);
     double y[16];
-    rotate_group<kBF16>(X + (int64_t)seg * kGroup, smem + seg * kSlotBytes, sl, y);   // groups of a row side by side
+    rotate_loaded<kBF16>(px[0], px[1], smem + seg * kSlotBytes, sl, y);
     float f[16];
     mx_rotated<kBF16>(y, f);
     const int row = seg / G, g = seg - row * G;

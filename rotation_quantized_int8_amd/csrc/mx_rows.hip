@@ -20,21 +20,39 @@ namespace {
 
 constexpr int kSegs = 16;   // groups of a 256-thread workgroup
 
+// Rows and groups one after the other; a workgroup whose grid does not cover them
+// all takes every gridDim-th 16 groups and has the next ones' loads in flight
+// while it works on these.
 template <bool kBF16>
 __global__ void __launch_bounds__(256)
 mx_act_quant_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales) {
   __shared__ __align__(16) char smem[kSegs * kSlotBytes];
   const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  const int64_t G = K / kGroup;
-  const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
-  if (u >= M * G) return;
-  const int64_t row = u / G, g = u - row * G;
-  double y[16];
-  rotate_group<kBF16>(X + row * K + g * kGroup, smem + seg * kSlotBytes, lane, y);
-  float f[16];
-  mx_rotated<kBF16>(y, f);
-  mx_store<mx_up(kBF16)>(f, row, M, K, g, lane, codes, scales);
+  const uint32_t G = (uint32_t)(K / kGroup);
+  const int64_t total = M * G, step = (int64_t)gridDim.x * kSegs;
+  const v4i* src = reinterpret_cast<const v4i*>(X) + 2 * lane;   // 32 chunks of 16 bytes a group, rows dense
+  int64_t u = (int64_t)blockIdx.x * kSegs + seg;
+  if (u >= total) return;
+  v4i r0 = src[32 * u], r1 = src[32 * u + 1];
+  for (;;) {
+    const int64_t next = u + step;
+    const bool more = next < total;
+    char* slot = smem + seg * kSlotBytes;
+    park_row(slot, lane, r0, r1);
+    if (more) {
+      r0 = src[32 * next];
+      r1 = src[32 * next + 1];
+    }
+    double y[16];
+    float f[16];
+    rotate_staged<kBF16>(slot, lane, y);
+    mx_rotated<kBF16>(y, f);
+    const int64_t row = u / G;
+    mx_store<mx_up(kBF16)>(f, row, M, K, u - row * G, lane, codes, scales);
+    if (!more) return;
+    u = next;
+  }
 }
 
 __global__ void __launch_bounds__(256)
@@ -46,15 +64,13 @@ mx_quantize_weights_kernel(const float* __restrict__ W, int64_t N, int64_t K, ui
   const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
   if (u >= N * G) return;
   const int64_t row = u / G, g = u - row * G;
-  const float4* src = reinterpret_cast<const float4*>(W + row * K + g * kGroup + 16 * lane);
+  const v4f* src = reinterpret_cast<const v4f*>(W + row * K + g * kGroup + 16 * lane);
   double v[16];   // the sum with 0 makes a zero +0, and so every zero after it
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float4 t = src[c];
-    v[4 * c] = __fma_rn((double)t.x, 0.0625, 0.0);
-    v[4 * c + 1] = __fma_rn((double)t.y, 0.0625, 0.0);
-    v[4 * c + 2] = __fma_rn((double)t.z, 0.0625, 0.0);
-    v[4 * c + 3] = __fma_rn((double)t.w, 0.0625, 0.0);
+    const v4f t = src[c];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * c + i] = __fma_rn((double)t[i], 0.0625, 0.0);
   }
   float f[16];
   rotate_rows(v, smem + seg * kSlotBytes, lane, f);
@@ -137,7 +153,10 @@ hipError_t launch_mx_quantize_weights(const float* W, int64_t N, int64_t K, uint
 hipError_t launch_mx_act_quant(const void* X, bool bf16, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales,
                                hipStream_t stream) {
   const auto fn = bf16 ? &mx_act_quant_kernel<true> : &mx_act_quant_kernel<false>;
-  hipLaunchKernelGGL(fn, grid_of(M, K), dim3(256), 0, stream, static_cast<const uint16_t*>(X), M, K, codes, scales);
+  int64_t resident = 0;
+  if (const hipError_t e = resident_grid(reinterpret_cast<const void*>(fn), 256, 0, &resident); e != hipSuccess) return e;
+  const int64_t blocks = (M * (K / kGroup) + kSegs - 1) / kSegs;
+  hipLaunchKernelGGL(fn, dim3((unsigned)(blocks < resident ? blocks : resident)), dim3(256), 0, stream, static_cast<const uint16_t*>(X), M, K, codes, scales);
   return hipGetLastError();
 }
 

@@ -78,16 +78,21 @@ __device__ __forceinline__ v8u narrow(const float (&v)[8]) {
 }
 
 // 8 neighbouring elements from e0 of a 16-bit row of D (zeros past its end).
+// kWhole: the chunk lies wholly inside the row, or wholly outside.
+template <bool kWhole>
 __device__ __forceinline__ v8u load8(const uint16_t* row, int e0, int D) {
-  if (e0 + 8 <= D) return *reinterpret_cast<const v8u_any*>(row + e0);
+  if (kWhole ? e0 < D : e0 + 8 <= D) return *reinterpret_cast<const v8u_any*>(row + e0);
   v8u v = {0, 0, 0, 0, 0, 0, 0, 0};
+  if constexpr (!kWhole) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (e0 + i < D) v[i] = row[e0 + i];
+    for (int i = 0; i < 8; ++i)
+      if (e0 + i < D) v[i] = row[e0 + i];
+  }
   return v;
 }
+template <bool kWhole>
 __device__ __forceinline__ void load8(const float* row, int e0, int D, float (&f)[8]) {
-  if (e0 + 8 <= D) {
+  if (kWhole || e0 + 8 <= D) {
     const v4f a = *reinterpret_cast<const v4f_any*>(row + e0), b = *reinterpret_cast<const v4f_any*>(row + e0 + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
@@ -97,18 +102,19 @@ __device__ __forceinline__ void load8(const float* row, int e0, int D, float (&f
   }
 }
 // The same of a modulation's row.
-template <bool kBF16>
+template <bool kBF16, bool kWhole>
 __device__ __forceinline__ void load_mod(const void* base, int64_t at, int f32, int e0, int D, float (&f)[8]) {
   if (f32) {
-    load8(static_cast<const float*>(base) + at, e0, D, f);
+    load8<kWhole>(static_cast<const float*>(base) + at, e0, D, f);
   } else {
-    const v8u v = load8(static_cast<const uint16_t*>(base) + at, e0, D);
+    const v8u v = load8<kWhole>(static_cast<const uint16_t*>(base) + at, e0, D);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = widen<kBF16>(v[i]);
   }
 }
+template <bool kWhole>
 __device__ __forceinline__ void store8(uint16_t* row, int e0, int D, v8u v) {
-  if (e0 + 8 <= D) {
+  if (kWhole || e0 + 8 <= D) {
     *reinterpret_cast<v8u_any*>(row + e0) = v;
   } else {
 #pragma unroll
@@ -126,8 +132,7 @@ constexpr float kSmall = 0x1p-90f, kUp = 0x1p96f;
 // 2^96 times.
 template <int V, int S, int WAVES, typename At, typename First, typename ScaleBy>
 __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by, int kind, float eps, int D,
-                                           float2 (*part)[16], float& mu, float& r) {
-  const float inv = 1.0f / (float)D;
+                                           float inv, float2 (*part)[16], float& mu, float& r) {
   for (int round = 0;; ++round) {
     mu = 0.0f;
     if (kind == kNormLayer) {
@@ -150,10 +155,11 @@ __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by,
 #pragma unroll
       for (int c = 0; c < V / 8; ++c) {
         const int left = D - first(k) - 8 * c;
+        if (V == 16 && left <= 0) continue;   // quantised rows: whole chunks
         float p[8], w = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = at(k, c, i) - mu;
-        if (left < 8) {
+        if (V == 8 && left < 8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) p[i] = i < left ? p[i] : 0.0f;
         }
@@ -166,7 +172,7 @@ __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by,
     e *= inv;
     const float var = fmaxf(__fmaf_rn(-e, e, q * inv), 0.0f) + eps;
     mu += e;
-    r = 1.0f / sqrtf(var);
+    r = __builtin_amdgcn_rsqf(var);   // within one ulp
     if ((q <= 0x1p120f && var >= kSmall) || round) return;
     const float by = q <= 0x1p120f ? kUp : 1.0f / kUp;
     scale_by(by);
@@ -201,7 +207,7 @@ norm_kernel(NormArgs a) {
   const int wave = WAVES == 1 ? 0 : wave_id;
   const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + wave_id : blockIdx.x;
   if (row >= a.M) return;
-  const int64_t mrow = a.index ? a.index[row] : row / a.each;
+  const int64_t mrow = a.index ? a.index[row] : (int64_t)((uint64_t)row * a.each_mul >> a.each_shift);
   if (mrow < 0 || mrow >= a.mod_rows) return;       // of no sequence: the whole row's wavefronts leave
   const int D = a.D;
   auto first = [&](int k) { return ((wave + WAVES * k) * 64 + lane) * V; };
@@ -210,7 +216,7 @@ norm_kernel(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < S; ++k)
 #pragma unroll
-    for (int c = 0; c < C; ++c) xr[k][c] = load8(a.x + row * a.x_stride, first(k) + 8 * c, D);
+    for (int c = 0; c < C; ++c) xr[k][c] = load8<kTurn>(a.x + row * a.x_stride, first(k) + 8 * c, D);
   auto rescale = [&](v8u (&raw)[S][C], float by) {
 #pragma unroll
     for (int k = 0; k < S; ++k)
@@ -228,11 +234,11 @@ norm_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
-      for (int c = 0; c < C; ++c) yr[k][c] = load8(a.y + row * a.y_stride, first(k) + 8 * c, D);
+      for (int c = 0; c < C; ++c) yr[k][c] = load8<kTurn>(a.y + row * a.y_stride, first(k) + 8 * c, D);
     float mu = 0.0f, r = 1.0f;
     if (a.post.kind != kNormNone)
       statistics<V, S, WAVES>([&](int k, int c, int i) { return widen<kBF16>(yr[k][c][i]); }, first,
-                              [&](float by) { rescale(yr, by); }, a.post.kind, a.post.eps, D, &part[0], mu, r);
+                              [&](float by) { rescale(yr, by); }, a.post.kind, a.post.eps, D, a.inv_d, &part[0], mu, r);
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
@@ -248,18 +254,18 @@ norm_kernel(NormArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) t[i] = (t[i] - mu) * r;
           if (a.post.weight) {
-            load8(a.post.weight, e0, D, p);
+            load8<kTurn>(a.post.weight, e0, D, p);
 #pragma unroll
             for (int i = 0; i < 8; ++i) t[i] *= p[i];
           }
           if (a.post.bias) {
-            load8(a.post.bias, e0, D, p);
+            load8<kTurn>(a.post.bias, e0, D, p);
 #pragma unroll
             for (int i = 0; i < 8; ++i) t[i] += p[i];
           }
         }
         if (a.gate) {
-          load_mod<kBF16>(a.gate, mrow * a.gate_stride, a.mod_f32, e0, D, p);
+          load_mod<kBF16, kTurn>(a.gate, mrow * a.gate_stride, a.mod_f32, e0, D, p);
 #pragma unroll
           for (int i = 0; i < 8; ++i) t[i] *= p[i];
         }
@@ -267,9 +273,9 @@ norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = __fmaf_rn(a.residual_scale, widen<kBF16>(xr[k][c][i]), t[i]);
-          h[k][c][i] = i < left ? v : 0.0f;
+          h[k][c][i] = kTurn || i < left ? v : 0.0f;
         }
-        store8(a.h + row * D, e0, D, narrow<kBF16>(h[k][c]));
+        store8<kTurn>(a.h + row * D, e0, D, narrow<kBF16>(h[k][c]));
       }
   }
   if constexpr (OUT == kOutNone) return;
@@ -293,7 +299,7 @@ norm_kernel(NormArgs a) {
           rescale(xr, by);
         }
       },
-      a.norm.kind, a.norm.eps, D, &part[3], mu, r);
+      a.norm.kind, a.norm.eps, D, a.inv_d, &part[3], mu, r);
   float f[kTurn ? (OUT == kOutInt8 ? S : 1) : 1][16];
   const int seg = (int)threadIdx.x >> 4, sl = lane & 15;
 #pragma unroll
@@ -311,22 +317,22 @@ norm_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = (at(k, c, i) - mu) * r;
       if (a.norm.weight) {
-        load8(a.norm.weight, e0, D, p);
+        load8<kTurn>(a.norm.weight, e0, D, p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] *= p[i];
       }
       if (a.norm.bias) {
-        load8(a.norm.bias, e0, D, p);
+        load8<kTurn>(a.norm.bias, e0, D, p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] += p[i];
       }
       if (a.scale) {
-        load_mod<kBF16>(a.scale, mrow * a.scale_stride, a.mod_f32, e0, D, p);
+        load_mod<kBF16, kTurn>(a.scale, mrow * a.scale_stride, a.mod_f32, e0, D, p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] = __fmaf_rn(t[i], p[i], t[i]);
       }
       if (a.shift) {
-        load_mod<kBF16>(a.shift, mrow * a.shift_stride, a.mod_f32, e0, D, p);
+        load_mod<kBF16, kTurn>(a.shift, mrow * a.shift_stride, a.mod_f32, e0, D, p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] += p[i];
       }
@@ -334,7 +340,7 @@ norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[8 * c + i] = t[i];
       } else {
-        store8(static_cast<uint16_t*>(a.values) + row * D, e0, D, narrow<kBF16>(t));
+        store8<kTurn>(static_cast<uint16_t*>(a.values) + row * D, e0, D, narrow<kBF16>(t));
       }
     }
     if constexpr (kTurn) {

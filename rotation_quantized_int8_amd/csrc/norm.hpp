@@ -27,7 +27,9 @@ struct NormArgs {
   int64_t scale_stride, shift_stride, gate_stride;
   int mod_f32;                    // the modulation is fp32 (else the rows' type)
   int64_t mod_rows;
-  int64_t each;                   // rows of x per row of the modulation (index null)
+  uint32_t each_mul;              // index null: row r has the modulation's row r each_mul >> each_shift,
+  int each_shift;                 // r / each of each rows side by side (r < 2^31)
+  float inv_d;                    // 1 / D
   const int32_t* index;
   uint16_t* h;
   void* values;

@@ -79,7 +79,8 @@ convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_str
   a.norm = view(norm);
   a.h = static_cast<uint16_t*>(H);
   a.mod_rows = 1;
-  a.each = M;
+  a.inv_d = 1.0f / (float)D;
+  int64_t each = M;
   size_t mod_size = 2;
   if (mod) {
     mod_size = mod->dtype == CONVROT_NORM_DTYPE_F32 ? 4 : 2;
@@ -95,8 +96,12 @@ convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_str
     a.mod_f32 = mod_size == 4;
     a.mod_rows = mod->rows;
     a.index = mod->index;
-    a.each = mod->index ? 1 : M / mod->rows;
+    each = mod->index ? 1 : M / mod->rows;
   }
+  // r / each as a product: 2^31 each <= 2^shift, so the error of mul, below 1 in 2^shift / each, moves no r < 2^31
+  a.each_shift = 31;
+  while (((int64_t)1 << (a.each_shift - 31)) < each) ++a.each_shift;
+  a.each_mul = (uint32_t)(((uint64_t)1 << a.each_shift) / (uint64_t)each + 1);
   if (out) {
     a.values = out->values;
     a.scales = out->scales;
