@@ -38,12 +38,12 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Sums over the row's wavefronts, in their order.  `part` is written by this sum
-// alone until the next barrier has passed.
-template <int WAVES>
+// Sums over the row's wavefronts, in their order (b only where kTwo).  `part` is
+// written by this sum alone until the next barrier has passed.
+template <int WAVES, bool kTwo>
 __device__ __forceinline__ void row_sums(float& a, float& b, float2* part) {
   a = wave_sum(a);
-  b = wave_sum(b);
+  if constexpr (kTwo) b = wave_sum(b);
   if constexpr (WAVES > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(a, b);
     __syncthreads();
@@ -146,7 +146,7 @@ __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by,
           for (int i = 0; i < 8; ++i) p[i] = at(k, c, i);
           s += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
         }
-      row_sums<WAVES>(s, none, part[0]);
+      row_sums<WAVES, false>(s, none, part[0]);
       mu = s * inv;
     }
     float e = 0.0f, q = 0.0f;
@@ -168,7 +168,7 @@ __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by,
         q += w;
         if (kind == kNormLayer) e += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       }
-    row_sums<WAVES>(e, q, part[1 + round]);
+    row_sums<WAVES, true>(e, q, part[1 + round]);
     e *= inv;
     const float var = fmaxf(__fmaf_rn(-e, e, q * inv), 0.0f) + eps;
     mu += e;
