@@ -65,7 +65,8 @@ size_t convrot_mx_workspace_bytes(int64_t M, int64_t N, int64_t K);
 /* The whole linear: X [M, K] of `x_dtype` quantised as by convrot_mx_act_quant
  * into the workspace, then convrot_mx_gemm with Y of `y_dtype` (few short rows:
  * both in one launch, the same bits).  The workspace, which may be NULL where 0
- * bytes are needed, must not overlap anything. */
+ * bytes are needed, must not overlap anything, and calls that may run at the
+ * same time need one each. */
 convrot_status convrot_mx_linear(const void* X, int x_dtype, int64_t M, int64_t K, const uint8_t* w_codes,
                                  const uint8_t* w_scales, int64_t N, const float* bias, const void* residual,
                                  void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);

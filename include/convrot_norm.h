@@ -40,7 +40,8 @@ enum { CONVROT_NORM_DTYPE_F32 = 2 };   /* a modulation in fp32 (else its convrot
 
 typedef struct convrot_norm_desc {
   int kind;              /* CONVROT_NORM_RMS or CONVROT_NORM_LAYER */
-  float eps;             /* finite, at least 0 */
+  float eps;             /* finite, at least 0 (below 2^-126 but not 0: 2^-126); with 0 a row without spread
+                            gives NaN, as the formula does */
   const float* weight;   /* fp32 [D] or NULL (1) */
   const float* bias;     /* fp32 [D] or NULL (0) */
 } convrot_norm_desc;

@@ -127,10 +127,12 @@ constexpr float kSmall = 0x1p-90f, kUp = 0x1p96f;
 
 // A row in fp32, element i of chunk c of unit k as at(k, c, i) (0 past the row's
 // end; `first(k)` is the unit's first element), to its mu and r: t = (at - mu) r.
-// `scale_by` multiplies the row by a power of two, which t does not feel: a row
-// whose squares pass fp32 is taken 2^-96 times, one whose squares vanish (eps 0)
-// 2^96 times.
-template <int V, int S, int WAVES, typename At, typename First, typename ScaleBy>
+// kRange: the row may leave the range of fp32's squares (fp16 ones do not).  Then
+// `scale_by` multiplies it by a power of two, which t does not feel: a row whose
+// squares pass fp32 is taken 2^-96 times, one whose squares vanish next to a
+// vanishing eps 2^96 times.  (With a mean beyond 1 such a row has no spread at all:
+// its differences would be at least the spacing of its values.)
+template <int V, int S, int WAVES, bool kRange, typename At, typename First, typename ScaleBy>
 __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by, int kind, float eps, int D,
                                            float inv, float2 (*part)[16], float& mu, float& r) {
   for (int round = 0;; ++round) {
@@ -173,7 +175,7 @@ __device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by,
     const float var = fmaxf(__fmaf_rn(-e, e, q * inv), 0.0f) + eps;
     mu += e;
     r = __builtin_amdgcn_rsqf(var);   // within one ulp
-    if ((q <= 0x1p120f && var >= kSmall) || round) return;
+    if (!kRange || round || (q <= 0x1p120f && (var >= kSmall || fabsf(mu) > 1.0f))) return;
     const float by = q <= 0x1p120f ? kUp : 1.0f / kUp;
     scale_by(by);
     if (eps > 0.0f) eps = fmaxf(eps * by * by, 0x1p-126f);   // still above 0: a row of one value gives 0
@@ -237,7 +239,7 @@ norm_kernel(NormArgs a) {
       for (int c = 0; c < C; ++c) yr[k][c] = load8<kTurn>(a.y + row * a.y_stride, first(k) + 8 * c, D);
     float mu = 0.0f, r = 1.0f;
     if (a.post.kind != kNormNone)
-      statistics<V, S, WAVES>([&](int k, int c, int i) { return widen<kBF16>(yr[k][c][i]); }, first,
+      statistics<V, S, WAVES, kBF16>([&](int k, int c, int i) { return widen<kBF16>(yr[k][c][i]); }, first,
                               [&](float by) { rescale(yr, by); }, a.post.kind, a.post.eps, D, a.inv_d, &part[0], mu, r);
 #pragma unroll
     for (int k = 0; k < S; ++k)
@@ -285,7 +287,7 @@ norm_kernel(NormArgs a) {
   };
 
   float mu, r;
-  statistics<V, S, WAVES>(
+  statistics<V, S, WAVES, kBF16 || RES>(
       at, first,
       [&](float by) {
         if constexpr (RES) {

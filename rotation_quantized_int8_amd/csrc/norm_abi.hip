@@ -33,8 +33,11 @@ convrot_status check_desc(const convrot_norm_desc* d) {
   return CONVROT_OK;
 }
 
+// An eps in fp32's subnormals counts as the smallest normal number.
 NormDesc view(const convrot_norm_desc* d) {
-  return d ? NormDesc{d->kind, d->eps, d->weight, d->bias} : NormDesc{kNormNone, 0.0f, nullptr, nullptr};
+  if (!d) return NormDesc{kNormNone, 0.0f, nullptr, nullptr};
+  const float eps = d->eps > 0.0f && d->eps < 0x1p-126f ? 0x1p-126f : d->eps;
+  return NormDesc{d->kind, eps, d->weight, d->bias};
 }
 
 convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_stride, bool residual, int dtype,

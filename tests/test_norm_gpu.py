@@ -290,6 +290,23 @@ def test_no_eps(d, dtype):
         _close(cr.norm(y.to(DEV), eps=0.0), want, np.abs(want) + 2)
 
 
+@pytest.mark.parametrize("eps", [1e-6, 1e-20, 1e-30, 1e-38, 1e-44])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [24, 512, 4096])
+def test_rows_without_spread(d, dtype, eps):
+    """Rows of one value of any size give 0 with any eps above 0, and their rms norm a row of one value."""
+    big = 6e4 if dtype is F16 else 1e30
+    x = torch.tensor([0.0, 1.0, -3.140625, 2.0 ** -14, big, -big, 0.01])[:, None].expand(-1, d).contiguous().to(dtype).to(DEV)
+    zero = torch.zeros_like(x)
+    assert not cr.norm(x, eps=eps).any()
+    h, n = cr.residual_norm(x, zero, eps=eps, post="layer", post_eps=eps)
+    assert torch.equal(h, x) and not n.any()
+    v = _np(x)
+    want = v / np.sqrt(v * v + max(eps, 2.0 ** -126))
+    for n in (cr.norm(x, kind="rms", eps=eps), cr.residual_norm(x, zero, kind="rms", eps=eps)[1]):
+        _close(n, want, np.abs(want))
+
+
 @pytest.mark.parametrize("m,d", [(5, 40), (6, 2048), (3, 4096)])
 def test_in_place_and_strides(m, d):
     """h over x or y; rows read from slices and broadcast modulations in place."""
