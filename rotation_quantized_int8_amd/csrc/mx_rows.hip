@@ -11,7 +11,16 @@
 // Work split.  As in the int8 prologue 16 lanes own a group of 256, each the 16
 // elements of one row of the 16 x 16 view, so a block of 32 is two neighbouring
 // lanes: one lane permutation completes its maximum.  No scale spans a row, so
-// groups are independent and no workgroup barrier is needed.
+// groups are independent and no workgroup barrier is needed.  A workgroup's 16
+// groups are the same one of 16 neighbouring rows, whose scales are one line of 128
+// bytes (16 groups of one row write 16 pieces of 8 bytes, 18 % more to memory; times
+// level to 4 %).
+//
+// Bound and measured (us on the GPU, inputs in turn): activations by the vector
+// unit, two thirds busy with fp64 sums and conversions (a quarter of the rate), next
+// to memory: 8192 x 8192 48 (3.6 TB/s), 16384 x 2048 29, 1024 x 8192 9.5; one group a
+// workgroup and no loads ahead 54 for the first.  Weights by memory: 8192 x 2048 16.4
+// (4.7 TB/s).  Values back by memory: 16384 x 2048 20 (4.3 TB/s), in fp64 36.
 
 #include "mx.hpp"
 
@@ -20,61 +29,86 @@ namespace {
 
 constexpr int kSegs = 16;   // groups of a 256-thread workgroup
 
-// Rows and groups one after the other; a workgroup whose grid does not cover them
-// all takes every gridDim-th 16 groups and has the next ones' loads in flight
-// while it works on these.
+// The groups of [rows, K]: 16 rows at a time, group after group (fewer than 2^31,
+// so n / (16 G) is a product; only the last rows, if there are not 16, divide).
+struct Units {
+  uint32_t rows, G, total, mul;
+  int shift;
+};
+__device__ __forceinline__ void unit_of(const Units& t, uint32_t u, uint32_t& row, uint32_t& g) {
+  const uint32_t block = (uint32_t)((uint64_t)u * t.mul >> t.shift), in = u - block * 16u * t.G;
+  const uint32_t left = t.rows - 16u * block;
+  g = left >= 16u ? in >> 4 : in / left;
+  row = 16u * block + (left >= 16u ? in & 15u : in - g * left);
+}
+Units units(int64_t rows, int64_t K) {
+  Units t{(uint32_t)rows, (uint32_t)(K / kGroup), (uint32_t)(rows * (K / kGroup)), 0u, 31};
+  const uint64_t d = 16ull * t.G;
+  while ((1ull << (t.shift - 31)) < d) ++t.shift;
+  t.mul = (uint32_t)((1ull << t.shift) / d + 1);
+  return t;
+}
+
+// A workgroup whose grid does not cover all groups takes every gridDim-th 16 and
+// has the next ones' loads in flight while it works on these.
 template <bool kBF16>
 __global__ void __launch_bounds__(256)
-mx_act_quant_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K, uint8_t* __restrict__ codes,
+mx_act_quant_kernel(const uint16_t* __restrict__ X, int64_t K, Units t, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales) {
   __shared__ __align__(16) char smem[kSegs * kSlotBytes];
   const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  const uint32_t G = (uint32_t)(K / kGroup);
-  const int64_t total = M * G, step = (int64_t)gridDim.x * kSegs;
-  const v4i* src = reinterpret_cast<const v4i*>(X) + 2 * lane;   // 32 chunks of 16 bytes a group, rows dense
-  int64_t u = (int64_t)blockIdx.x * kSegs + seg;
-  if (u >= total) return;
-  v4i r0 = src[32 * u], r1 = src[32 * u + 1];
+  uint32_t u = blockIdx.x * kSegs + seg, row, g;
+  if (u >= t.total) return;
+  auto source = [&](uint32_t row, uint32_t g) {
+    return reinterpret_cast<const v4i*>(X + row * K + g * kGroup + 16 * lane);
+  };
+  unit_of(t, u, row, g);
+  const v4i* src = source(row, g);
+  v4i r0 = src[0], r1 = src[1];
+  char* slot = smem + seg * kSlotBytes;
   for (;;) {
-    const int64_t next = u + step;
-    const bool more = next < total;
-    char* slot = smem + seg * kSlotBytes;
+    const uint32_t next = u + gridDim.x * kSegs;
+    const bool more = next < t.total;
+    uint32_t next_row = 0, next_g = 0;
     park_row(slot, lane, r0, r1);
     if (more) {
-      r0 = src[32 * next];
-      r1 = src[32 * next + 1];
+      unit_of(t, next, next_row, next_g);
+      src = source(next_row, next_g);
+      r0 = src[0];
+      r1 = src[1];
     }
     double y[16];
     float f[16];
     rotate_staged<kBF16>(slot, lane, y);
     mx_rotated<kBF16>(y, f);
-    const int64_t row = u / G;
-    mx_store<mx_up(kBF16)>(f, row, M, K, u - row * G, lane, codes, scales);
+    mx_store<mx_up(kBF16)>(f, row, t.rows, K, g, lane, codes, scales);
     if (!more) return;
     u = next;
+    row = next_row;
+    g = next_g;
   }
 }
 
 __global__ void __launch_bounds__(256)
-mx_quantize_weights_kernel(const float* __restrict__ W, int64_t N, int64_t K, uint8_t* __restrict__ codes,
+mx_quantize_weights_kernel(const float* __restrict__ W, int64_t K, Units t, uint8_t* __restrict__ codes,
                            uint8_t* __restrict__ scales) {
   __shared__ __align__(16) char smem[kSegs * kSlotBytes];
   const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  const int64_t G = K / kGroup;
-  const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
-  if (u >= N * G) return;
-  const int64_t row = u / G, g = u - row * G;
+  const uint32_t u = blockIdx.x * kSegs + seg;
+  if (u >= t.total) return;
+  uint32_t row, g;
+  unit_of(t, u, row, g);
   const v4f* src = reinterpret_cast<const v4f*>(W + row * K + g * kGroup + 16 * lane);
   double v[16];   // the sum with 0 makes a zero +0, and so every zero after it
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const v4f t = src[c];
+    const v4f w = src[c];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * c + i] = __fma_rn((double)t[i], 0.0625, 0.0);
+    for (int i = 0; i < 4; ++i) v[4 * c + i] = __fma_rn((double)w[i], 0.0625, 0.0);
   }
   float f[16];
   rotate_rows(v, smem + seg * kSlotBytes, lane, f);
-  mx_store<0>(f, row, N, K, g, lane, codes, scales);
+  mx_store<0>(f, row, t.rows, K, g, lane, codes, scales);
 }
 
 // An e2m1 code as the integer 2 c: 0 1 2 3 4 6 8 12 and their negatives.
@@ -90,16 +124,16 @@ __device__ __forceinline__ int e2m1_twice(uint32_t code) {
 // have no say.
 template <bool kBF16>
 __global__ void __launch_bounds__(256)
-mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
-                     int64_t K, uint16_t* __restrict__ V) {
+mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, Units t,
+                     uint16_t* __restrict__ V) {
   __shared__ __align__(16) char smem[kSegs * kSlotBytes];
   const int seg = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  const int64_t G = K / kGroup;
-  const int64_t u = (int64_t)blockIdx.x * kSegs + seg;
-  if (u >= rows * G) return;
-  const int64_t row = u / G, g = u - row * G;
+  const uint32_t u = blockIdx.x * kSegs + seg;
+  if (u >= t.total) return;
+  uint32_t row, g;
+  unit_of(t, u, row, g);
   const uint2 c = *reinterpret_cast<const uint2*>(codes + row * (K / 2) + g * 128 + 8 * lane);
-  const uint32_t byte = scales[(g * rows + row) * 8 + (lane >> 1)];
+  const uint32_t byte = scales[((int64_t)g * t.rows + row) * 8 + (lane >> 1)];
   const bool some = ((c.x | c.y) & 0x77777777u) != 0u;
   // largest scale and smallest (as the largest of 255 - byte) over the 16 lanes
   const uint32_t high = seg_max16_bits(some || byte == 255u ? byte : 0u);
@@ -140,13 +174,14 @@ mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restric
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-dim3 grid_of(int64_t rows, int64_t K) { return dim3((unsigned)((rows * (K / kGroup) + kSegs - 1) / kSegs)); }
+dim3 grid_of(const Units& t) { return dim3((t.total + kSegs - 1) / kSegs); }
 
 }  // namespace
 
 hipError_t launch_mx_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* codes, uint8_t* scales,
                                       hipStream_t stream) {
-  hipLaunchKernelGGL(mx_quantize_weights_kernel, grid_of(N, K), dim3(256), 0, stream, W, N, K, codes, scales);
+  const Units t = units(N, K);
+  hipLaunchKernelGGL(mx_quantize_weights_kernel, grid_of(t), dim3(256), 0, stream, W, K, t, codes, scales);
   return hipGetLastError();
 }
 
@@ -155,16 +190,18 @@ hipError_t launch_mx_act_quant(const void* X, bool bf16, int64_t M, int64_t K, u
   const auto fn = bf16 ? &mx_act_quant_kernel<true> : &mx_act_quant_kernel<false>;
   int64_t resident = 0;
   if (const hipError_t e = resident_grid(reinterpret_cast<const void*>(fn), 256, 0, &resident); e != hipSuccess) return e;
-  const int64_t blocks = (M * (K / kGroup) + kSegs - 1) / kSegs;
-  hipLaunchKernelGGL(fn, dim3((unsigned)(blocks < resident ? blocks : resident)), dim3(256), 0, stream, static_cast<const uint16_t*>(X), M, K, codes, scales);
+  const Units t = units(M, K);
+  const dim3 all = grid_of(t);
+  hipLaunchKernelGGL(fn, all.x < resident ? all : dim3((unsigned)resident), dim3(256), 0, stream,
+                     static_cast<const uint16_t*>(X), K, t, codes, scales);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* V,
                                 bool bf16, hipStream_t stream) {
   const auto fn = bf16 ? &mx_dequantize_kernel<true> : &mx_dequantize_kernel<false>;
-  hipLaunchKernelGGL(fn, grid_of(rows, K), dim3(256), 0, stream, codes, scales, rows, K,
-                     static_cast<uint16_t*>(V));
+  const Units t = units(rows, K);
+  hipLaunchKernelGGL(fn, grid_of(t), dim3(256), 0, stream, codes, scales, K, t, static_cast<uint16_t*>(V));
   return hipGetLastError();
 }
 

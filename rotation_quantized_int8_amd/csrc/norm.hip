@@ -207,7 +207,11 @@ norm_kernel(NormArgs a) {
   __shared__ uint32_t top[16];
   const int lane = threadIdx.x & 63, wave_id = threadIdx.x >> 6;
   const int wave = WAVES == 1 ? 0 : wave_id;
-  const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + wave_id : blockIdx.x;
+  // 4-bit scales of neighbouring rows share a line: each XCD (workgroup number mod 8) takes rows side by side, so
+  // that its L2 puts the line together
+  uint32_t block = blockIdx.x;
+  if (OUT == kOutMx && (gridDim.x & 7) == 0) block = (block & 7) * (gridDim.x >> 3) + (block >> 3);
+  const int64_t row = WAVES == 1 ? (int64_t)block * (blockDim.x >> 6) + wave_id : block;
   if (row >= a.M) return;
   const int64_t mrow = a.index ? a.index[row] : (int64_t)((uint64_t)row * a.each_mul >> a.each_shift);
   if (mrow < 0 || mrow >= a.mod_rows) return;       // of no sequence: the whole row's wavefronts leave
