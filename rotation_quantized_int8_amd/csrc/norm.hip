@@ -20,7 +20,7 @@
 // Bound and measured (us on the GPU, inputs in turn, 16384 rows of 2048 in bf16):
 // 16-bit outputs by memory: norm 27 (5.0 TB/s), residual with a norm of y and the
 // next norm 54 (5.0 TB/s; a large copy reaches 5.1).  Quantised ones by the vector
-// unit, 95 % busy (33 instructions an element, a third of them the rotation and the
+// unit, 80 % busy (33 instructions an element, a third of them the rotation and the
 // codes): to 4 bits 31 (2.8 TB/s), the residual form 66.  1024 rows of 2048 to int8
 // 8.2, 3 rows 5.0: latency of a row's chain (load, two sums, modulation, rotation).
 
@@ -218,10 +218,12 @@ norm_kernel(NormArgs a) {
   // that its L2 puts the line together
   uint32_t block = blockIdx.x;
   if (OUT == kOutMx && (gridDim.x & 7) == 0) block = (block & 7) * (gridDim.x >> 3) + (block >> 3);
-  const int64_t row = WAVES == 1 ? (int64_t)block * (blockDim.x >> 6) + wave_id : block;
-  if (row >= a.M) return;
-  const int64_t mrow = a.index ? a.index[row] : (int64_t)((uint64_t)row * a.each_mul >> a.each_shift);
-  if (mrow < 0 || mrow >= a.mod_rows) return;       // of no sequence: the whole row's wavefronts leave
+  const uint32_t row32 = WAVES == 1 ? block * (blockDim.x >> 6) + wave_id : block;
+  if (row32 >= a.M) return;
+  const uint32_t mrow32 =
+      a.index ? (uint32_t)a.index[row32] : (uint32_t)((uint64_t)row32 * a.each_mul >> a.each_shift);
+  if (mrow32 >= a.mod_rows) return;       // of no sequence (negative ones too): the whole row's wavefronts leave
+  const int64_t row = row32, mrow = mrow32;
   const int D = a.D;
   auto first = [&](int k) { return ((wave + WAVES * k) * 64 + lane) * V; };
 
@@ -400,7 +402,7 @@ hipError_t launch(const NormArgs& a, hipStream_t stream) {
   const size_t lds = kTurn ? (size_t)threads / 16 * kTurnSlot : 0;
   const auto fn = &norm_kernel<kBF16, OUT, RES, S, WAVES>;
   if (const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fn), lds); e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3((unsigned)((a.M + rows - 1) / rows)), dim3(threads), lds, stream, a);
+  hipLaunchKernelGGL(fn, dim3((a.M + rows - 1) / rows), dim3(threads), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -418,7 +420,7 @@ hipError_t choose(const NormArgs& a, hipStream_t stream) {
   const int units = (a.D + 64 * V - 1) / (64 * V);   // of a wavefront's lanes, over the row
   if (units <= 1) return launch<kBF16, OUT, RES, 1, 1>(a, stream);
   if constexpr (V == 8) {
-    if (a.M * units > 4096) {
+    if ((int64_t)a.M * units > 4096) {
       if (units <= 2) return launch<kBF16, OUT, RES, 2, 1>(a, stream);
       if (units <= 4) return launch<kBF16, OUT, RES, 2, 2>(a, stream);
       if (units <= 8) return launch<kBF16, OUT, RES, 2, 4>(a, stream);

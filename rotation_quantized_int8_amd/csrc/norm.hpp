@@ -18,15 +18,15 @@ struct NormDesc {
 struct NormArgs {
   const uint16_t* x;
   const uint16_t* y;              // the block's output (residual form) or null
-  int64_t x_stride, y_stride;
-  int64_t M;
+  uint32_t x_stride, y_stride;    // elements, below 2^31 (32 bits: the kernel is short of scalar registers)
+  uint32_t M;
   int D;
   float residual_scale;
   NormDesc post, norm;
   const void *scale, *shift, *gate;   // rows of the modulation or null
-  int64_t scale_stride, shift_stride, gate_stride;
+  uint32_t scale_stride, shift_stride, gate_stride;
   int mod_f32;                    // the modulation is fp32 (else the rows' type)
-  int64_t mod_rows;
+  uint32_t mod_rows;
   uint32_t each_mul;              // index null: row r has the modulation's row r each_mul >> each_shift,
   int each_shift;                 // r / each of each rows side by side (r < 2^31)
   float inv_d;                    // 1 / D

@@ -73,9 +73,9 @@ convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_str
   NormArgs a{};
   a.x = static_cast<const uint16_t*>(X);
   a.y = static_cast<const uint16_t*>(Y);
-  a.x_stride = x_stride;
-  a.y_stride = y_stride;
-  a.M = M;
+  a.x_stride = (uint32_t)x_stride;
+  a.y_stride = (uint32_t)y_stride;
+  a.M = (uint32_t)M;
   a.D = (int)D;
   a.residual_scale = residual_scale;
   a.post = view(post);
@@ -93,11 +93,11 @@ convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_str
     a.scale = mod->scale;
     a.shift = mod->shift;
     a.gate = residual ? mod->gate : nullptr;
-    a.scale_stride = mod->scale_stride;
-    a.shift_stride = mod->shift_stride;
-    a.gate_stride = mod->gate_stride;
+    a.scale_stride = (uint32_t)mod->scale_stride;
+    a.shift_stride = (uint32_t)mod->shift_stride;
+    a.gate_stride = (uint32_t)mod->gate_stride;
     a.mod_f32 = mod_size == 4;
-    a.mod_rows = mod->rows;
+    a.mod_rows = (uint32_t)mod->rows;
     a.index = mod->index;
     each = mod->index ? 1 : M / mod->rows;
   }

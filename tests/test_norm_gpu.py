@@ -174,6 +174,33 @@ def test_residual_norm(m, d, dtype, post):
     assert none is None and torch.equal(h2, h)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("m,d", [(2100, 1000), (2052, 1024), (4100, 513), (1030, 2041), (1026, 2048), (520, 4096),
+                                 (516, 4095), (5000, 40)])
+def test_many_rows(m, d, dtype):
+    """The variants with two units a lane, which many rows take."""
+    c = _Case(m, d, dtype, images=2, mod=dtype, affine=True)
+    _close(cr.norm(c.x.to(DEV), eps=EPS, **c.gpu(*NAMES)), *c.normed(_np(c.x)))
+    h, n = cr.residual_norm(c.x.to(DEV), c.y.to(DEV), eps=EPS, post="layer", post_eps=EPS,
+                            post_weight=c.post_weight.to(DEV), **c.gpu(*NAMES, "gate"))
+    want = c.h("layer", 1.0)
+    hs = c.h_size(want)
+    _close(h, want, hs, "h")
+    wn, size = c.normed(want)
+    _close(n, wn, size + hs / np.sqrt((want * want).mean(1, keepdims=True) + EPS), "n")
+    h2, _ = cr.residual_norm(c.x.to(DEV), c.y.to(DEV), kind=None, post="layer", post_eps=EPS,
+                             post_weight=c.post_weight.to(DEV), gate=c.gate)
+    assert torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("m,d", [(8, 1280), (64, 768), (4096, 256), (1000, 2304)])
+def test_many_quantised_rows(m, d):
+    """Grids of a whole number of workgroups an XCD (their rows go side by side), and others."""
+    c = _Case(m, d, BF16, images=1, mod=BF16, affine=False)
+    n, size = c.normed(_np(c.x))
+    _equal4(*cr.norm_quant(c.x.to(DEV), bits=4, eps=EPS, **c.gpu("scale", "shift")), n, size)
+
+
 QUANT = [(1, 256), (5, 512), (6, 768), (4, 1024), (9, 1280), (16, 2048), (3, 2304), (2, 4096), (3, 8192), (2, 8448),
          (2, 16384)]
 
