@@ -96,9 +96,16 @@ __device__ __forceinline__ void mx_rotated(const double (&y)[16], float (&f)[16]
 // hold 16 elements each of; kUp: f is 2^kUp times the value quantised.
 template <int kUp>
 __device__ __forceinline__ uint32_t mx_scale_byte(const float (&f)[16]) {
-  uint32_t m = 0;
+  // the bits order like |f| within a sign, NaN on top: the largest as signed numbers is of the positive values, as
+  // unsigned ones of the negative, if there are any (three at a time, without clearing signs)
+  int pos = 0;
+  uint32_t neg = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);   // orders like |f|; NaN on top
+  for (int i = 0; i < 16; i += 2) {
+    pos = max(max(pos, __float_as_int(f[i])), __float_as_int(f[i + 1]));
+    neg = max(max(neg, __float_as_uint(f[i])), __float_as_uint(f[i + 1]));
+  }
+  uint32_t m = max((uint32_t)pos, neg & 0x7FFFFFFFu);
   m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));
   const int eb = (int)(m >> 23);
   return eb == 255 ? 255u : (uint32_t)max(eb - 2 - kUp, 0);

@@ -20,9 +20,10 @@
 // Bound and measured (us on the GPU, inputs in turn, 16384 rows of 2048 in bf16):
 // 16-bit outputs by memory: norm 27 (5.0 TB/s), residual with a norm of y and the
 // next norm 54 (5.0 TB/s; a large copy reaches 5.1).  Quantised ones by the vector
-// unit, 80 % busy (33 instructions an element, a third of them the rotation and the
-// codes): to 4 bits 31 (2.8 TB/s), the residual form 66.  1024 rows of 2048 to int8
-// 8.2, 3 rows 5.0: latency of a row's chain (load, two sums, modulation, rotation).
+// unit (80 % busy with some 30 instructions an element, a third of them the rotation
+// and the codes): to 4 bits 29 (2.9 TB/s; 30.2 with the rows widened where they are
+// read).  1024 rows of 2048 to int8 8.2, 3 rows of the residual form to 4 bits 4.7:
+// latency of a row's chain (load, two sums, modulation, rotation).
 
 #include "norm.hpp"
 
@@ -243,7 +244,18 @@ norm_kernel(NormArgs a) {
         raw[k][c] = narrow<kBF16>(p);
       }
   };
-  float h[RES ? S : 1][C][8];       // the residual form's rows; the plain one widens x where it is read
+  // In fp32 throughout: the residual form's rows, and the quantised ones (fewer instructions than widening
+  // where they are read); the plain form into 16 bits waits for memory and keeps its registers.
+  constexpr bool kHeld = RES || kTurn;
+  float h[kHeld ? S : 1][C][8];
+  if constexpr (kHeld && !RES) {
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][c][i] = widen<kBF16>(xr[k][c][i]);
+  }
   if constexpr (RES) {
     v8u yr[S][C];
 #pragma unroll
@@ -295,7 +307,7 @@ norm_kernel(NormArgs a) {
   }
   if constexpr (OUT == kOutNone) return;
   auto at = [&](int k, int c, int i) {
-    if constexpr (RES) return h[k][c][i];
+    if constexpr (kHeld) return h[k][c][i];
     else return widen<kBF16>(xr[k][c][i]);
   };
 
@@ -303,7 +315,7 @@ norm_kernel(NormArgs a) {
   statistics<V, S, WAVES, kBF16 || RES>(
       at, first,
       [&](float by) {
-        if constexpr (RES) {
+        if constexpr (kHeld) {
 #pragma unroll
           for (int k = 0; k < S; ++k)
 #pragma unroll
