@@ -30,6 +30,7 @@ struct NormArgs {
   uint32_t each_mul;              // index null: row r has the modulation's row r each_mul >> each_shift,
   int each_shift;                 // r / each of each rows side by side (r < 2^31)
   float inv_d;                    // 1 / D
+  double inv_wide;                // the same
   const int32_t* index;
   uint16_t* h;
   void* values;
@@ -37,5 +38,7 @@ struct NormArgs {
 };
 
 hipError_t launch_norm(const NormArgs& a, bool bf16, NormOut out, hipStream_t stream);
+// The quantised forms (out kOutInt8 or kOutMx), by launch_norm.
+hipError_t launch_norm_quant(const NormArgs& a, bool bf16, NormOut out, hipStream_t stream);
 
 }  // namespace convrot

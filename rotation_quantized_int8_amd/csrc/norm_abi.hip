@@ -83,6 +83,7 @@ convrot_status run(const void* X, int64_t x_stride, const void* Y, int64_t y_str
   a.h = static_cast<uint16_t*>(H);
   a.mod_rows = 1;
   a.inv_d = 1.0f / (float)D;
+  a.inv_wide = 1.0 / (double)D;
   int64_t each = M;
   size_t mod_size = 2;
   if (mod) {
