@@ -13,11 +13,12 @@
  * with post a norm without modulation, or y itself; what follows takes h
  * before its rounding.  Outputs of 16 bits: all arithmetic is fp32 up to their
  * one rounding: the mean first, then the squares of the differences, with what
- * the mean's rounding left taken out.  Quantised outputs: all arithmetic is fp64
- * up to u = fp32(n H), so that codes and scales are the formula's (H from h's
- * fp32 value).  Rows of any finite size have their norm (in fp32 one whose
- * squares leave its range is taken times a power of two); an h that passes fp32,
- * an infinity or a NaN shows in its own row alone.
+ * the mean's rounding left taken out (h itself is an fp32 number there).
+ * Quantised outputs: all arithmetic is fp64 up to u = fp32(n H), so that codes
+ * and scales are the formula's (H from h's fp32 value).  Rows of any finite size
+ * have their norm (a row that fp32 does not hold is taken in fp64); an h that
+ * passes fp32, an infinity or a NaN shows in its own row alone, as the formula
+ * has it: a NaN in the whole row.
  *
  * Conventions are those of convrot.h, but for these.  Rows of X, Y and of the
  * modulation have strides in elements (0 .. 2^31 - 1) with D contiguous

@@ -5,10 +5,9 @@
 // Mathematics.  h = residual_scale x + gate post(y) (or x), n = ((h - mu) r
 // weight + bias)(1 + scale) + shift, in one pass: a row is held in registers
 // from its load to its last output.  All of it is fp32.  The mean is taken first,
-// then the sums of d = h - mu and of d^2, whose first takes out what the rounding
-// of mu left, so that rows of one value give 0 and a mean far above the spread
-// costs no digits.  A row whose squares leave fp32's range is taken times a power
-// of two instead.
+// then the sums of d = h - mu and of d^2; what the first says that mu is off stays
+// apart, so that rows of one value give 0 and a mean far above the spread costs no
+// digits.  Rows that fp32 does not hold are taken in fp64.
 //
 // Work split.  WAVES wavefronts own a row, each lane S units of 8 neighbouring
 // elements (one 16-byte load).  One wavefront a row needs no barrier; four such
@@ -57,64 +56,113 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float2* part) {
   }
 }
 
-constexpr float kSmall = 0x1p-90f, kUp = 0x1p96f;
+// What the sums of a row's wavefronts pass through.
+struct RowParts {
+  float2 means[16], sums[16];
+};
 
-// A row in fp32, element i of unit k as at(k, i) (0 past the row's
-// end; `first(k)` is the unit's first element), to its mu and r: t = (at - mu) r.
-// kRange: the row may leave the range of fp32's squares (fp16 ones do not).  Then
-// `scale_by` multiplies it by a power of two, which t does not feel: a row whose
-// squares pass fp32 is taken 2^-96 times, one whose squares vanish next to a
-// vanishing eps 2^96 times.  (With a mean beyond 1 such a row has no spread at all:
-// its differences would be at least the spacing of its values.)
-template <int S, int WAVES, bool kRange, typename At, typename First, typename ScaleBy>
-__device__ __forceinline__ void statistics(At at, First first, ScaleBy scale_by, int kind, float eps, int D,
-                                           float inv, float2 (*part)[16], float& mu, float& r) {
-  for (int round = 0;; ++round) {
-    mu = 0.0f;
-    if (kind == kNormLayer) {
-      float s = 0.0f, none = 0.0f;
+// A row in fp32, unit k's 8 elements in v[k] (0 past the row's end; `first(k)` is the
+// unit's first element), to (v - mu) r.  The mean is mu + e: e, the mean of the
+// differences, is what the rounding of mu left, and stays apart, since a mean far
+// above the spread may lie between two fp32 numbers.  Rows that fp32 does not hold are
+// taken in fp64: those whose squares leave its range, and those where e passes the
+// spread itself (rows of one value among them, which then give 0).
+template <int S, int WAVES, typename First>
+__device__ __forceinline__ void normalise(float (&v)[S][8], First first, int kind, float eps, const NormArgs& a,
+                                          RowParts& parts, double (*wide)[16]) {
+  const int D = a.D;
+  float mu = 0.0f, none = 0.0f, e = 0.0f, q = 0.0f;
+  if (kind == kNormLayer) {
 #pragma unroll
-      for (int k = 0; k < S; ++k) {
-        float p[8];
+    for (int k = 0; k < S; ++k)
+      mu += ((v[k][0] + v[k][1]) + (v[k][2] + v[k][3])) + ((v[k][4] + v[k][5]) + (v[k][6] + v[k][7]));
+    row_sums<WAVES, false>(mu, none, parts.means);
+    mu *= a.inv_d;
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = at(k, i);
-        s += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      }
-      row_sums<WAVES, false>(s, none, part[0]);
-      mu = s * inv;
+  for (int k = 0; k < S; ++k) {
+    const int left = D - first(k);
+    float p[8], w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = v[k][i] - mu;
+    if (left < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = i < left ? p[i] : 0.0f;
     }
-    float e = 0.0f, q = 0.0f;
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int left = D - first(k);
-      float p[8], w = 0.0f;
+    for (int i = 0; i < 8; ++i) w = __fmaf_rn(p[i], p[i], w);
+    q += w;
+    if (kind == kNormLayer) e += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+  }
+  row_sums<WAVES, true>(e, q, parts.sums);
+  mu = as_fp32(mu);   // so that the differences are taken again, and do not hold registers next to v
+  e *= a.inv_d;
+  const float var = __fmaf_rn(-e, e, q * a.inv_d);
+  // the same bits in every lane of the row's wavefronts; an infinity or a NaN fails too
+  if (__builtin_expect(q <= 0x1p120f && var + eps >= 0x1p-90f && e * e <= var, 1)) {
+    const float r = __builtin_amdgcn_rsqf(var + eps);   // within one ulp
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = at(k, i) - mu;
-      if (left < 8) {
+    for (int k = 0; k < S; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = i < left ? p[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) v[k][i] = ((v[k][i] - mu) - e) * r;
+    return;
+  }
+  // rare: one element after the other, in few registers, so that the ordinary rows keep theirs
+  double m = 0.0, z = 0.0;
+  if (kind == kNormLayer) {
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m += (double)as_fp32(v[k][i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    m = quotient(row_sum<WAVES>(m, wide[0]), (double)D, a.inv_wide);
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w = __fmaf_rn(p[i], p[i], w);
-      q += w;
-      if (kind == kNormLayer) e += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+  for (int k = 0; k < S; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double d = first(k) + i < D ? (double)as_fp32(v[k][i]) - m : 0.0;
+      z = __fma_rn(d, d, z);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    row_sums<WAVES, true>(e, q, part[1 + round]);
-    e *= inv;
-    const float var = fmaxf(__fmaf_rn(-e, e, q * inv), 0.0f) + eps;
-    mu += e;
-    r = __builtin_amdgcn_rsqf(var);   // within one ulp
-    if (!kRange || round || (q <= 0x1p120f && (var >= kSmall || fabsf(mu) > 1.0f))) return;
-    const float by = q <= 0x1p120f ? kUp : 1.0f / kUp;
-    scale_by(by);
-    if (eps > 0.0f) eps = fmaxf(eps * by * by, 0x1p-126f);   // still above 0: a row of one value gives 0
+  z = inverse_root(row_sum<WAVES>(z, wide[1]) * a.inv_wide + (double)eps);
+#pragma unroll
+  for (int k = 0; k < S; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[k][i] = (float)(((double)v[k][i] - m) * z);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// t = t weight + bias.
+template <int S, typename First>
+__device__ __forceinline__ void affine(float (&t)[S][8], First first, const NormDesc& n, int D) {
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    const int e0 = first(k);
+    if (e0 >= D) continue;
+    float p[8];
+    if (n.weight) {
+      load8<false>(n.weight, e0, D, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[k][i] *= p[i];
+    }
+    if (n.bias) {
+      load8<false>(n.bias, e0, D, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[k][i] += p[i];
+    }
   }
 }
 
 template <bool kBF16, int OUT, bool RES, int S, int WAVES>
 __global__ void __launch_bounds__(WAVES <= 4 ? 256 : 64 * WAVES)
 norm_kernel(NormArgs a) {
-  __shared__ float2 part[6][16];
+  __shared__ RowParts parts[2];
+  __shared__ double wide[2][16];   // of both norms: a barrier of the second's sums lies between
   const int lane = threadIdx.x & 63, wave_id = threadIdx.x >> 6;
   const int wave = WAVES == 1 ? 0 : wave_id;
   const uint32_t row32 = WAVES == 1 ? blockIdx.x * (blockDim.x >> 6) + wave_id : blockIdx.x;
@@ -124,114 +172,65 @@ norm_kernel(NormArgs a) {
   const int64_t row = row32, mrow = mrow32;
   const int D = a.D;
   auto first = [&](int k) { return ((wave + WAVES * k) * 64 + lane) * 8; };
+  auto widen8 = [](v8u raw, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = widen<kBF16>(raw[i]);
+  };
 
   v8u xr[S];
 #pragma unroll
   for (int k = 0; k < S; ++k) xr[k] = load8<false>(a.x + row * a.x_stride, first(k), D);
-  auto rescale = [&](v8u (&raw)[S], float by) {
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      float p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = widen<kBF16>(raw[k][i]) * by;
-      raw[k] = narrow<kBF16>(p);
-    }
-  };
-  float h[RES ? S : 1][8];   // the residual form's rows in fp32; x itself is widened where it is read
+  float v[S][8];
   if constexpr (RES) {
     v8u yr[S];
 #pragma unroll
     for (int k = 0; k < S; ++k) yr[k] = load8<false>(a.y + row * a.y_stride, first(k), D);
-    float mu = 0.0f, r = 1.0f;
-    if (a.post.kind != kNormNone)
-      statistics<S, WAVES, kBF16>([&](int k, int i) { return widen<kBF16>(yr[k][i]); }, first,
-                                  [&](float by) { rescale(yr, by); }, a.post.kind, a.post.eps, D, a.inv_d, &part[0],
-                                  mu, r);
+#pragma unroll
+    for (int k = 0; k < S; ++k) widen8(yr[k], v[k]);
+    if (a.post.kind != kNormNone) {
+      normalise<S, WAVES>(v, first, a.post.kind, a.post.eps, a, parts[0], wide);
+      affine<S>(v, first, a.post, D);
+    }
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      const int e0 = first(k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] = 0.0f;
-      if (e0 >= D) continue;
-      float t[8], p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = widen<kBF16>(yr[k][i]);
-      if (a.post.kind != kNormNone) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = (t[i] - mu) * r;
-        if (a.post.weight) {
-          load8<false>(a.post.weight, e0, D, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] *= p[i];
-        }
-        if (a.post.bias) {
-          load8<false>(a.post.bias, e0, D, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] += p[i];
-        }
-      }
-      if (a.gate) {
+      const int e0 = first(k), left = D - e0;
+      if (a.gate && left > 0) {
+        float p[8];
         load_mod<kBF16, false>(a.gate, mrow * a.gate_stride, a.mod_f32, e0, D, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] *= p[i];
+        for (int i = 0; i < 8; ++i) v[k][i] *= p[i];
       }
-      const int left = D - e0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = __fmaf_rn(a.residual_scale, widen<kBF16>(xr[k][i]), t[i]);
-        h[k][i] = i < left ? v : 0.0f;
+        const float h = __fmaf_rn(a.residual_scale, widen<kBF16>(xr[k][i]), v[k][i]);
+        v[k][i] = i < left ? h : 0.0f;
       }
-      store8<false>(a.h + row * D, e0, D, narrow<kBF16>(h[k]));
+      if (left > 0) store8<false>(a.h + row * D, e0, D, narrow<kBF16>(v[k]));
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < S; ++k) widen8(xr[k], v[k]);
   }
   if constexpr (OUT == kOutNone) return;
-  auto at = [&](int k, int i) {
-    if constexpr (RES) return h[k][i];
-    else return widen<kBF16>(xr[k][i]);
-  };
 
-  float mu, r;
-  statistics<S, WAVES, kBF16 || RES>(
-      at, first,
-      [&](float by) {
-        if constexpr (RES) {
-#pragma unroll
-          for (int k = 0; k < S; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[k][i] *= by;
-        } else {
-          rescale(xr, by);
-        }
-      },
-      a.norm.kind, a.norm.eps, D, a.inv_d, &part[3], mu, r);
+  normalise<S, WAVES>(v, first, a.norm.kind, a.norm.eps, a, parts[1], wide);
+  affine<S>(v, first, a.norm, D);
 #pragma unroll
   for (int k = 0; k < S; ++k) {
     const int e0 = first(k);
     if (e0 >= D) continue;
-    float t[8], p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = (at(k, i) - mu) * r;
-    if (a.norm.weight) {
-      load8<false>(a.norm.weight, e0, D, p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] *= p[i];
-    }
-    if (a.norm.bias) {
-      load8<false>(a.norm.bias, e0, D, p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] += p[i];
-    }
+    float p[8];
     if (a.scale) {
       load_mod<kBF16, false>(a.scale, mrow * a.scale_stride, a.mod_f32, e0, D, p);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __fmaf_rn(t[i], p[i], t[i]);
+      for (int i = 0; i < 8; ++i) v[k][i] = __fmaf_rn(v[k][i], p[i], v[k][i]);
     }
     if (a.shift) {
       load_mod<kBF16, false>(a.shift, mrow * a.shift_stride, a.mod_f32, e0, D, p);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] += p[i];
+      for (int i = 0; i < 8; ++i) v[k][i] += p[i];
     }
-    store8<false>(static_cast<uint16_t*>(a.values) + row * D, e0, D, narrow<kBF16>(t));
+    store8<false>(static_cast<uint16_t*>(a.values) + row * D, e0, D, narrow<kBF16>(v[k]));
   }
 }
 

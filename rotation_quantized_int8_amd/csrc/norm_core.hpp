@@ -79,4 +79,64 @@ __device__ __forceinline__ void store8(uint16_t* row, int e0, int D, v8u v) {
   }
 }
 
+// Statistics in fp64.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double joined(uint32_t lo, uint32_t hi) {
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the wavefront, the same bits in every lane.
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp_f64<0xB1>(v);
+  v += dpp_f64<0x4E>(v);
+  v += dpp_f64<0x141>(v);
+  v += dpp_f64<0x140>(v);
+  uint64_t b = __builtin_bit_cast(uint64_t, v);
+  uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+  const auto l16 = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+  const auto h16 = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+  v = joined(l16[0], h16[0]) + joined(l16[1], h16[1]);
+  b = __builtin_bit_cast(uint64_t, v);
+  lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+  const auto l32 = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+  const auto h32 = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+  return joined(l32[0], h32[0]) + joined(l32[1], h32[1]);
+}
+
+// Sum over the row's wavefronts, in their order.  `part` is written by this sum
+// alone until the next barrier has passed.
+template <int WAVES>
+__device__ __forceinline__ double row_sum(double v, double* part) {
+  v = wave_sum(v);
+  if constexpr (WAVES > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += part[w];
+  }
+  return v;
+}
+// v^-1/2: the hardware's estimate (some 24 bits) and two Newton steps; 0 for an
+// infinity, an infinity for 0.
+__device__ __forceinline__ double inverse_root(double v) {
+  const double y0 = __builtin_amdgcn_rsq(v);
+  double y = y0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __fma_rn(0.5 * y, __fma_rn(-v * y, y, 1.0), y);
+  return y0 > 0.0 && y0 < __builtin_inf() ? y : y0;
+}
+
+// s / d, with inv 1 / d: a product, and what it is off.  The sum of d equal values gives the value.
+__device__ __forceinline__ double quotient(double s, double d, double inv) {
+  const double v = s * inv;
+  return __fma_rn(__fma_rn(-v, d, s), inv, v);
+}
+
 }  // namespace convrot

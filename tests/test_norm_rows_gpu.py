@@ -1,0 +1,100 @@
+"""Rows of 16 bits out that go wrong more easily than others, against 64 bits.
+
+The arithmetic is fp32: mu + e is within 2^-19 of the spread of the row's mean (e is
+the mean of differences, whose sum passes at most 29 additions), r within 2^-19, an
+element has up to 6 more roundings: with T the sizes that meet in it after the
+mean is taken out, |d| <= h |n| + tiny + 2^-18 T (h half a step of the type, tiny half
+of its smallest).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import rotation_quantized_int8_amd as cr
+from oracle import norm_oracle as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    cr.lib()
+    torch.cuda.set_device(0)
+
+
+def _np(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def _close(got, want, size, what=""):
+    h = torch.finfo(got.dtype).eps / 2
+    tiny = {F16: 2.0 ** -25, BF16: 2.0 ** -134}[got.dtype]
+    err, bound = np.abs(_np(got) - want), h * np.abs(want) + tiny + 2.0 ** -18 * size
+    at = np.unravel_index(np.argmax(err - bound), err.shape)
+    assert (err <= bound).all(), (what, at, err[at], bound[at], want[at])
+
+
+SIZES = [24, 1000, 1003, 2048, 4096, 8200, 16384]
+
+
+def _far(d, dtype):
+    """Rows whose mean is far above their spread: steps of the type near a large value."""
+    gen = torch.Generator().manual_seed(d)
+    big, step = (60000.0, 32.0) if dtype is F16 else (2.0 ** 20 + 2.0 ** 15, 2.0 ** 13)
+    x = torch.full((6, d), big, dtype=torch.float64)
+    x[0, d // 2] += step
+    x[1, 0] += step
+    x[2, ::2] += step
+    x[3] += step * torch.randint(-2, 3, (d,), generator=gen)
+    x[4] = -x[0]
+    x[5, -1] -= step
+    assert x.to(dtype).double().equal(x)
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", SIZES)
+def test_mean_far_above_the_spread(d, dtype):
+    x = _far(d, dtype)
+    want = O.norm(_np(x), "layer", EPS)
+    _close(cr.norm(x.to(DEV), eps=EPS), want, np.abs(want) + 1)
+    zero = torch.zeros_like(x)
+    h, n = cr.residual_norm(zero.to(DEV), x.to(DEV), kind="layer", eps=EPS, post="layer", post_eps=EPS)
+    _close(h, want, np.abs(want) + 1, "h")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", SIZES)
+def test_residual_whose_mean_is_far_above_its_spread(d, dtype):
+    """h exact in fp32: a value of few bits and steps of 2^-4 and less next to 2^14."""
+    gen = torch.Generator().manual_seed(d + 1)
+    x = torch.full((3, d), 2.0 ** 14)
+    y = torch.zeros((3, d))
+    y[0, d // 3] = 2.0 ** -4
+    y[1] = torch.randint(-8, 9, (d,), generator=gen) * 2.0 ** -6
+    y[2, ::3] = 2.0 ** -8
+    v = x.double().numpy() + y.double().numpy()
+    want = O.norm(v, "layer", 1e-12)
+    h, n = cr.residual_norm(x.to(dtype).to(DEV), y.to(dtype).to(DEV), eps=1e-12)
+    # a row whose spread is that of one step has its mean within 2^-20 of a step
+    spread = np.sqrt(v.var(1, keepdims=True) + 1e-12)
+    _close(n, want, np.abs(want) + 1 + np.abs(y.numpy()).max(1, keepdims=True) / spread)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", SIZES)
+def test_any_size_of_row_without_eps(d, dtype):
+    """Rows of the type's smallest and largest values, far means and none, under eps 0."""
+    gen = torch.Generator().manual_seed(d + 2)
+    base = torch.randn((4, d), generator=gen, dtype=torch.float64)
+    base[2:] += 64
+    for f in ((2.0 ** -14, 1.0, 2.0 ** 9) if dtype is F16 else (2.0 ** -118, 2.0 ** -64, 1.0, 2.0 ** 40, 2.0 ** 119)):
+        x = (base * f).to(dtype)
+        want = O.norm(_np(x), "layer", 0.0)
+        _close(cr.norm(x.to(DEV), eps=0.0), want, np.abs(want) + 1, f)
