@@ -98,3 +98,28 @@ def test_any_size_of_row_without_eps(d, dtype):
         x = (base * f).to(dtype)
         want = O.norm(_np(x), "layer", 0.0)
         _close(cr.norm(x.to(DEV), eps=0.0), want, np.abs(want) + 1, f)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("d", [40, 1024, 4099, 8192])
+def test_not_finite_as_the_formula_has_it(d, kind, dtype):
+    """A NaN makes its row's statistics and so the whole row NaN; an infinity makes r 0 (rms) or the mean infinite."""
+    gen = torch.Generator().manual_seed(d + 3)
+    x = torch.randn((5, d), generator=gen).to(dtype)
+    x[1, d // 2], x[2, 3], x[3, 0] = float("nan"), float("inf"), float("-inf")
+    n = cr.norm(x.to(DEV), kind=kind, eps=EPS).cpu()
+    with np.errstate(invalid="ignore"):
+        want = O.norm(_np(x), kind, EPS)
+    assert torch.equal(torch.isnan(n), torch.from_numpy(np.isnan(want)))
+    assert torch.isnan(n[1]).all() and not n[2:4].nan_to_num().any()
+    y = torch.zeros_like(x).to(DEV)
+    h, n2 = cr.residual_norm(x.to(DEV), y, kind=kind, eps=EPS)
+    assert torch.equal(torch.isnan(n2).cpu(), torch.isnan(n)) and torch.equal(h.cpu().nan_to_num(), x.nan_to_num())
+    h, n3 = cr.residual_norm(y, x.to(DEV), kind=None, post=kind, post_eps=EPS)
+    assert n3 is None and torch.equal(torch.isnan(h).cpu(), torch.isnan(n))
+    if d % 256 == 0:
+        q, s = cr.norm_quant(x.to(DEV), bits=4, kind=kind, eps=EPS)
+        assert (s[:, 1] == 255).all() and not q[1].any()
+        q, s = cr.norm_quant(x.to(DEV), bits=8, kind=kind, eps=EPS)
+        assert torch.isnan(s).tolist() == [False, True, True, True, False] and not q[1:4].any()
