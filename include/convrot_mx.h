@@ -46,8 +46,10 @@ convrot_status convrot_mx_act_quant(const void* X, int dtype, int64_t M, int64_t
                                     uint8_t* scales, void* stream);
 
 /* The rows that codes and scales stand for, un-rotated: V [rows, K] of `dtype`
- * = out((c 2^e) H), fp64 sums (exact while a group's values span at most 45
- * binades), one rounding.  A NaN scale gives NaN in its whole group. */
+ * = out(fp32((c 2^e) H)), fp64 sums (exact while a group's values span at most 45
+ * binades) and then two roundings, to fp32 as u has them and from there to the
+ * type; the first changes nothing while the scales of a group lie within 2^12 of
+ * one another.  A NaN scale gives NaN in its whole group. */
 convrot_status convrot_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* V,
                                      int dtype, void* stream);
 

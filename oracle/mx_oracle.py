@@ -78,7 +78,7 @@ def values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
 
 
 def dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
-    """The rows themselves, un-rotated, float64 (before the one rounding)."""
+    """The rows themselves, un-rotated, float64 (before the roundings to fp32 and to the type)."""
     v = values(codes, scales)
     return (v.reshape(-1, 256) @ hadamard256()).reshape(v.shape)
 

@@ -120,8 +120,8 @@ __device__ __forceinline__ int e2m1_twice(uint32_t code) {
 // Un-rotation.  A value is a multiple of 2^e / 2 up to 6 2^e, so while the scales
 // of a group lie within 2^12 of one another every partial sum of its 256 values
 // fits fp32's 24 bits and the transform is exact there; groups beyond that (or at
-// the ends of the scales' range, or with a NaN) take the fp64 one.  Blocks of zeros
-// have no say.
+// the ends of the scales' range, or with a NaN) take the fp64 one, whose sums are
+// rounded to fp32 before they are rounded to the type.  Blocks of zeros have no say.
 template <bool kBF16>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, Units t,
