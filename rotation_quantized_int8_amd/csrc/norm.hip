@@ -242,11 +242,13 @@ hipError_t launch(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Wavefronts a row and units a lane: two units where that still leaves 16 wavefronts
-// a CU (16384 rows of 2048: norm 26.8 against 30.3 us, residual 55 against 58), else
-// one, which is faster by latency (1024 rows of 1024: norm 4.4 against 4.9 us,
-// residual 5.6 against 6.6).  Four units a lane (residual, one wavefront a row of
-// 2048) leave 3 wavefronts a SIMD: 74 us.
+// Wavefronts a row and units a lane: two units where that still leaves 8 wavefronts
+// a CU (16384 rows of 2048: norm 26.8 against 30.3 us, residual 55 against 58; 4000
+// rows of 5000: norm 21 against 26, residual 41 against 43), else one, which is faster
+// by latency (1024 rows of 1024: norm 4.4 against 4.9 us, residual 5.6 against 6.6).
+// Four units a lane (residual, one wavefront a row of 2048) leave 3 wavefronts a
+// SIMD: 74 us.  A grid has fewer than 2^32 threads in every case: with M D at most
+// 2^35 the most are 2^35 / 2049 rows of 256, 2^35 / 4097 of 512 and 2^35 / 8193 of 1024.
 template <bool kBF16, int OUT, bool RES>
 hipError_t choose(const NormArgs& a, hipStream_t stream) {
   const int units = (a.D + 511) / 512;   // of a wavefront's lanes, over the row
@@ -255,6 +257,7 @@ hipError_t choose(const NormArgs& a, hipStream_t stream) {
     if (units <= 2) return launch<kBF16, OUT, RES, 2, 1>(a, stream);
     if (units <= 4) return launch<kBF16, OUT, RES, 2, 2>(a, stream);
     if (units <= 8) return launch<kBF16, OUT, RES, 2, 4>(a, stream);
+    if (units <= 16) return launch<kBF16, OUT, RES, 2, 8>(a, stream);
   }
   if (units <= 2) return launch<kBF16, OUT, RES, 1, 2>(a, stream);
   if (units <= 4) return launch<kBF16, OUT, RES, 1, 4>(a, stream);

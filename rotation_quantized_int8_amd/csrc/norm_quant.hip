@@ -259,7 +259,8 @@ hipError_t launch(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Wavefronts a row: one unit of 16 elements a lane.
+// Wavefronts a row: one unit of 16 elements a lane.  A grid has fewer than 2^32
+// threads in every case, as those of norm.hip.
 template <bool kBF16, int OUT, bool RES>
 hipError_t choose(const NormArgs& a, hipStream_t stream) {
   const int units = (a.D + 1023) / 1024;

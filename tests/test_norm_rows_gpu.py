@@ -123,3 +123,35 @@ def test_not_finite_as_the_formula_has_it(d, kind, dtype):
         assert (s[:, 1] == 255).all() and not q[1].any()
         q, s = cr.norm_quant(x.to(DEV), bits=8, kind=kind, eps=EPS)
         assert torch.isnan(s).tolist() == [False, True, True, True, False] and not q[1:4].any()
+
+
+@pytest.mark.parametrize("m,d", [(600, 5000), (1030, 8190)])
+def test_many_long_rows(m, d):
+    """The variant of two units a lane and eight wavefronts a row."""
+    gen = torch.Generator().manual_seed(m)
+    x, y = (torch.randn((m, d), generator=gen).to(BF16) for _ in range(2))
+    want = O.norm(_np(x), "layer", EPS)
+    _close(cr.norm(x.to(DEV), eps=EPS), want, np.abs(want) + 1)
+    v = _np(x) + O.norm(_np(y), "rms", EPS)
+    h, n = cr.residual_norm(x.to(DEV), y.to(DEV), eps=EPS, post="rms", post_eps=EPS)
+    _close(h, v, np.abs(v) + np.abs(_np(x)) + 1, "h")
+    want = O.norm(v, "layer", EPS)
+    _close(n, want, 3 * np.abs(want) + 10, "n")
+    h2, _ = cr.residual_norm(x.to(DEV), y.to(DEV), kind=None, post="rms", post_eps=EPS)
+    assert torch.equal(h2, h)
+
+
+def test_more_rows_than_a_grid_of_1024_threads_each():
+    """2^22 rows and one of 4104: every one is written (one row in memory, read with stride 0)."""
+    m, d = (1 << 22) + 1, 4104
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 34 GB of GPU memory")
+    x = torch.randn((1, d), generator=torch.Generator().manual_seed(1)).to(F16).to(DEV)
+    out = torch.zeros((m, d), dtype=F16, device=DEV)
+    cr.norm(x.expand(m, d), eps=EPS, out=out)
+    want = O.norm(_np(x), "layer", EPS)
+    _close(out[:1], want, np.abs(want) + 1)
+    for a in range(0, m, 1 << 18):
+        assert (out[a:a + (1 << 18)] == out[0]).all(), a
+    del out
+    torch.cuda.empty_cache()
