@@ -10,7 +10,8 @@ h = residual_scale x + gate post(y).  scale, shift and gate are rows of a
 modulation, [rows, D] (or [D]) of x's dtype or fp32, with any stride between
 rows (slices of a conditioning's projection are read in place): each serves
 M / rows consecutive rows of x, or those whose ``index`` (int32 [M]) names it.
-A row with an index out of range is padding: nothing is written for it.
+A row with an index out of range is padding: nothing is written for it, so it
+keeps what ``out`` held, or whatever the memory of a new output held.
 
 As in the rest of the package only arguments are marshalled here; every step
 runs in the library's HIP kernels on the current stream.
@@ -148,13 +149,31 @@ def _dense(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Te
     return t
 
 
-def _quantised(m: int, d: int, bits: int, like: torch.Tensor) -> Tuple[int, torch.Tensor, torch.Tensor]:
-    if bits == 4:
+def _given(t: torch.Tensor, shape: tuple, dtype: torch.dtype, like: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device or t.data_ptr() % 16:
+        raise ValueError(f"out's {name} must be a contiguous {dtype} tensor {list(shape)} on x's device, aligned to 16 bytes")
+    return t
+
+
+def _quantised(m: int, d: int, bits: int, like: torch.Tensor, out=None) -> Tuple[int, torch.Tensor, torch.Tensor]:
+    """The output's kind, and codes and scales, new or (either of the two) given."""
+    if out is not None:
+        values, scales = out
+        if values is None or scales is None:
+            _, v, s = _quantised(m, d, bits, like)
+            values, scales = v if values is None else values, s if scales is None else scales
+        if bits == 4:
+            return (_OUT_MXFP4, _given(values, (m, d // 2), torch.uint8, like, "codes"),
+                    _given(scales, (d // GROUP, m, 8), torch.uint8, like, "scales"))
+    elif bits == 4:
         return (_OUT_MXFP4, *_empty4(m, d, like))
     if bits != 8:
         raise ValueError("bits must be 4 or 8")
     if d % GROUP:
         raise ValueError(f"the row length must be a multiple of {GROUP}, got {d}")
+    if out is not None:
+        return (_OUT_INT8, _given(values, (m, d), torch.int8, like, "codes"),
+                _given(scales, (m,), torch.float32, like, "scales"))
     return _OUT_INT8, like.new_empty((m, d), dtype=torch.int8), like.new_empty((m,), dtype=torch.float32)
 
 
@@ -183,12 +202,13 @@ def norm(x: torch.Tensor, kind: str = "layer", eps: float = 1e-6, weight: Option
 def norm_quant(x: torch.Tensor, bits: int, kind: str = "layer", eps: float = 1e-6,
                weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None,
-               index: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+               index: Optional[torch.Tensor] = None,
+               out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The norm of x [..., D] (M rows), rotated and quantised: with bits 8 the
     codes int8 [M, D] and scales fp32 [M] that gemm_i8_f16 takes, with bits 4
-    the codes and scales that mx_gemm takes."""
+    the codes and scales that mx_gemm takes (into ``out``, where given)."""
     rows = _rows(x, "x")
-    how, values, scales = _quantised(*rows[2:], bits, x)
+    how, values, scales = _quantised(*rows[2:], bits, x, out)
     _norm(*rows, kind, eps, weight, bias, scale, shift, index, how, values, scales)
     return values, scales
 
@@ -250,15 +270,17 @@ def residual_norm_quant(x: torch.Tensor, y: torch.Tensor, bits: int, kind: str =
                         gate: Optional[torch.Tensor] = None, index: Optional[torch.Tensor] = None,
                         residual_scale: float = 1.0, post: Optional[str] = None, post_eps: float = 1e-6,
                         post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
-                        out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                        out=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """residual_norm with the norm rotated and quantised as by norm_quant:
-    returns (h, codes, scales); h into ``out`` where given (x or y itself)."""
+    returns (h, codes, scales).  ``out`` is where h goes (x or y itself may be
+    it), or a tuple of where all three go, None for a new one."""
     rows = _rows(x, "x")
     _alike(x, y)
     if kind is None:
         raise ValueError("kind must be 'rms' or 'layer'")
-    h = _dense(out, x, "out")
-    how, values, scales = _quantised(*rows[2:], bits, x)
+    h, codes = (out[0], out[1:]) if isinstance(out, (tuple, list)) else (out, None)
+    h = _dense(h, x, "out's h")
+    how, values, scales = _quantised(*rows[2:], bits, x, codes)
     _residual(*rows, y, kind, eps, weight, bias, scale, shift, gate, index, residual_scale, post, post_eps, post_weight,
               post_bias, h, how, values, scales)
     return h, values, scales
