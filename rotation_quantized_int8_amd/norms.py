@@ -127,6 +127,8 @@ def _modulation(x: torch.Tensor, m: int, d: int, scale, shift, gate, index) -> T
         if index is not None:
             raise ValueError("index names rows of scale, shift or gate, which are not given")
         return None, kept
+    if rows == 0 and m == 0:             # an empty batch
+        return None, kept
     if index is not None:
         if index.dtype is not torch.int32:
             raise TypeError(f"index must be int32, got {index.dtype}")
@@ -134,8 +136,6 @@ def _modulation(x: torch.Tensor, m: int, d: int, scale, shift, gate, index) -> T
             raise ValueError(f"index must be [{m}] on x's device")
         index = index.contiguous()
         kept.append(index)
-    elif rows == 0 and m == 0:
-        return None, kept                # an empty batch
     elif rows == 0 or m % rows:
         raise ValueError(f"{m} rows do not split into {rows} equal parts (give index)")
     return _MOD.pack(*at, *step, _MOD_F32 if dtype is torch.float32 else _DTYPES[dtype], rows,
