@@ -155,3 +155,18 @@ def test_more_rows_than_a_grid_of_1024_threads_each():
         assert (out[a:a + (1 << 18)] == out[0]).all(), a
     del out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("post", ["layer", "rms"])
+@pytest.mark.parametrize("m,d", [(5, 33), (3, 1001), (4, 2048), (2, 8200), (2100, 1000)])
+def test_weight_and_bias_of_the_norm_of_y(m, d, post, dtype):
+    gen = torch.Generator().manual_seed(1000 * m + d)
+    x, y = (torch.randn((m, d), generator=gen).to(dtype) for _ in range(2))
+    w, b = 1 + 0.2 * torch.randn((d,), generator=gen), torch.randn((d,), generator=gen)
+    for weight, bias in ((w, b), (None, b), (w, None)):
+        h, _ = cr.residual_norm(x.to(DEV), y.to(DEV), kind=None, residual_scale=0.5, post=post, post_eps=EPS,
+                                post_weight=None if weight is None else weight.to(DEV),
+                                post_bias=None if bias is None else bias.to(DEV))
+        p = O.norm(_np(y), post, EPS, None if weight is None else _np(weight), None if bias is None else _np(bias))
+        _close(h, 0.5 * _np(x) + p, np.abs(p) + np.abs(_np(x)) + 2 * np.abs(_np(b)) + 4)
