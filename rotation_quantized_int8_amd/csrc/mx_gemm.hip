@@ -8,23 +8,24 @@
 // rotation group (8 blocks, 128 bytes a row) lane half q takes blocks 4q .. 4q + 3,
 // one an instruction, so that its four scales are one word of the layout
 // [K / 256, rows, 8].  Of the two shapes this one is faster (operands in registers:
-// 8.7 PFLOP/s against 6.2 with 16x16x128, whose issue takes as long as its product;
-// with operands of random bits 6.1, where the clock gives way).
+// 9.0 PFLOP/s against 4.8 with 16x16x128; with operands of random bits 6.6 against
+// 4.6, where the clock gives way).
 //
 // Data flow.  Tiles as in the int8 product: direct global->LDS loads into a ring
 // of STAGES slices of one rotation group, 16-byte chunks XOR-swizzled by
-// (row >> 1) & 7 (16 rows cover all banks; row & 7 leaves 7 times the conflicts); the slice's scales, 8 bytes a row, follow the
-// codes in the same ring.  The weight tile is the left operand, so a lane's
+// (row >> 1) & 7 (16 rows cover all banks; row & 7 leaves 7 times the conflicts);
+// the slice's scales, 8 bytes a row, follow the codes in the same ring.  The weight tile is the left operand, so a lane's
 // accumulators are fours of neighbouring outputs of one row.
 //
-// Bound and measured (us on the GPU, operands in turn).  Large: 8192^3 270 (4.1
-// PFLOP/s) in tiles of 256x256, the matrix cores busy half of the cycles at the 1.9
-// GHz that the card holds under it; copies of the kernel take 280 as it is, 260
-// without its loads, 220 without loads and barriers (operands of one value, where the
-// clock stays up: 225, 200, 175).  Middle: 1024 x 2048 x 8192 20, one workgroup a CU, by
-// the LDS (three fragments read for two products) next to its loads.  Small: 777 x
-// 1003 x 768 5.0, 24 x 8192 x 2048 5.5, a launch, a round trip for the first slice and
-// 0.25 a slice.  1 x 2048 x 2048 with its quantisation 4.1.
+// Bound and measured (us, one call after another in a graph, operands in turn; a call
+// traced alone takes 0.5 to 1 more).  Large: 8192^3 254 to 270 (4.1 to 4.3 PFLOP/s)
+// in tiles of 256x256, the matrix cores busy 53 % of the cycles at the 1.8 GHz that
+// the card holds under it, the rest waits of wavefronts that enter and leave a slice
+// together.  Middle: 1024 x 2048 x 8192 18.7, with bias and residual 21.4: 256
+// workgroups put one wavefront on a SIMD, whose barrier, LDS reads and products stand
+// in line (matrix cores 13 % busy).  Small: 777 x 1003 x 768 4.3, 24 x 8192 x 2048 4.5,
+// a launch, a round trip for the first slice and 0.25 a slice.  1 x 2048 x 2048 with
+// its quantisation 3.5.
 //
 // Rows past M or N repeat the last valid row for the loads and are dropped in
 // the epilogue.
@@ -234,7 +235,7 @@ mx_gemm_kernel(MxGemm p) {
   if constexpr (kDeep) {
     // Small tiles: a step's products take less than an LDS read, so the fragments
     // of a whole slice are read under the products of the slice before it (128x64
-    // tile, 1024 x 2048 x 8192: 18.4 us; step by step 21.3).  Behind the barrier every
+    // tile, 1024 x 2048 x 8192 without bias: 18.4 us; step by step 21.3).  Behind the barrier every
     // read of slice kt is done and slice kt + 1 is published.
     struct Slice {
       v4i w[NKK][FN], x[NKK][FM];
@@ -573,7 +574,7 @@ hipError_t launch_mx_gemm(const MxGemm& a, hipStream_t stream) {
   if (few_rows(a.M, a.N, a.K)) return a.M <= 16 ? launch_few<1>(a, stream) : launch_few<2>(a, stream);
   // Tiles: the largest that fill the card's 256 CUs (128x128 in 4 wavefronts and 70
   // KB runs twice on one), us: 8192^3 256x256 274, 128x128 315; 4096^3 47, 55;
-  // 1024 x 8192 x 2048 128x128 15.8, 128x64 19.8; 1024 x 2048 x 8192 128x64 18.4,
+  // 1024 x 8192 x 2048 128x128 15.8, 128x64 19.8; 1024 x 2048 x 8192 128x64 18.4 (no bias),
   // 64x64 20, 128x128 32; 777 x 1003 x 768 64x64 5.0, 128x64 6.0.
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   if (tiles(256, 256) >= 256) return launch_tiles<2, 4, 4, 2, 2>(a, stream);

@@ -16,11 +16,14 @@
 // bytes (16 groups of one row write 16 pieces of 8 bytes, 18 % more to memory; times
 // level to 4 %).
 //
-// Bound and measured (us on the GPU, inputs in turn): activations by the vector
-// unit, two thirds busy with fp64 sums and conversions (a quarter of the rate), next
-// to memory: 8192 x 8192 48 (3.6 TB/s), 16384 x 2048 29, 1024 x 8192 9.5; one group a
-// workgroup and no loads ahead 54 for the first.  Weights by memory: 8192 x 2048 16.4
-// (4.7 TB/s).  Values back by memory: 16384 x 2048 20 (4.3 TB/s), in fp64 36.
+// Bound and measured (us, one call after another in a graph, inputs in turn; a call
+// traced alone takes 1 to 4 more).  Activations: 8192 x 8192 44 (3.9 TB/s), 16384 x
+// 2048 22, 1024 x 8192 7.5; one group a workgroup and no loads ahead are 15 % slower.
+// The vector unit is 60 % busy and memory three quarters: the slots leave 4
+// wavefronts a SIMD, which wait for LDS and loads in turn (sums in fp32 where they
+// are certain are level, so their width is not what bounds it).  Weights by memory:
+// 8192 x 2048 14.8 (5.2 TB/s).  Values back by memory: 16384 x 2048 18.5 (4.6 TB/s),
+// in fp64 36.
 
 #include "mx.hpp"
 

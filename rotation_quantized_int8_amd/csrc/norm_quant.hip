@@ -14,12 +14,13 @@
 // of the rotation's 16 x 16 view, 16 lanes to a group.  One wavefront a row needs no
 // barrier; four such rows share a workgroup.
 //
-// Bound and measured (us on the GPU, inputs in turn, bf16 rows of 2048, modulated):
-// the vector unit, where a conversion to or from fp64 takes four times an addition's
-// issue: four an element are a third of the work.  16384 rows to 4 bits 43 (fp32: 26),
-// to int8 45 (37), the residual form 70 and 69 (53 and 61); 1024 rows 4.7 and 5.8
-// (4.3 and 6.0), residual 6.8 and 7.8; 3 rows 3.6 and 4.2, residual 4.6 and 5.1:
-// latency of a row's chain (load, two sums, modulation, rotation).
+// Bound and measured (us, one call after another in a graph, inputs in turn, bf16 rows
+// of 2048, modulated; a call traced alone takes 1 to 4 more): 16384 rows to 4 bits 43
+// (fp32: 26), to int8 45 (37), the residual form 70 and 69 (53 and 61): the vector
+// unit, some 38 instructions an element of 4 to 5 cycles (an fp32 addition takes 2.8),
+// at the 4 wavefronts a SIMD that the slots leave.  1024 rows 4.7 and 5.9 (4.3 and
+// 6.0), residual 6.8 and 8.3; 3 rows 3.6 and 4.1, residual 4.6 and 5.2: latency of a
+// row's chain (load, two sums, modulation, rotation).
 
 #include "norm_core.hpp"
 

@@ -11,8 +11,9 @@
 // partial sum of the 256-point transform is a multiple of 2^-24 below 2^24:
 // 48 significand bits.  The butterflies therefore run in fp64, where they are
 // exact, and the result is rounded once (to fp32, or to fp16 through
-// round-to-odd).  gfx950 issues fp64 adds at the full vector rate, so this
-// costs the same number of VALU operations as an inexact fp32 transform.
+// round-to-odd).  This is the same number of vector operations as an inexact
+// fp32 transform; an fp64 addition issues in 5.2 cycles of a wavefront and an
+// fp64 conversion in 4.3, as an integer operation does, an fp32 addition in 2.8.
 //
 // Layout.  A 256-group is viewed as a 16x16 matrix G[a][b] (element 16a + b)
 // and H = H16 (x) H16 (up to the 1/16), so the transform is a 16-point
