@@ -15,9 +15,10 @@
 // element, a last partial unit goes element by element.
 //
 // Bound and measured (us, one call after another in a graph, inputs in turn, bf16).
-// 16384 rows of 2048 by memory: norm 24.5 (5.5 TB/s; a large copy reaches 5.2), residual
-// with a norm of y and the next norm 52 (5.2), h alone 33.  1024 rows 3.7 and 6.5, 3
-// rows 2.7 and 3.8: latency, the parameters' loads behind the sums one after another.
+// 16384 rows of 2048 by memory: norm 24.5, residual with a norm of y and the next norm
+// 52 (5.2 TB/s, as a large copy), h alone 33 (the last cache holds part of the inputs
+// of the first and the third).  1024 rows 3.7 and 6.5, 3 rows 2.7 and 3.8: latency, the
+// parameters' loads behind the sums one after another.
 
 #include "norm_core.hpp"
 
